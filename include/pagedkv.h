@@ -82,6 +82,11 @@ typedef enum { PKV_F32 = 0, PKV_F16 = 1, PKV_BF16 = 2, PKV_FP8_E4M3 = 3 } pkv_dt
                                  /* length disagrees with its group's prefix      */
 #define PKV_DEV_LAUNCH      64u  /* a kernel found its shared memory not 1 KiB    */
                                  /* aligned and computed nothing                  */
+#define PKV_DEV_NOMEM      128u  /* paged_build_tables: too few free blocks       */
+#define PKV_DEV_FREE_LIST  256u  /* paged_build_tables: the ring's state or a     */
+                                 /* taken entry is out of range, or more blocks   */
+                                 /* come back than the ring has room for          */
+#define PKV_DEV_TOKENS     512u  /* paged_build_tables: more than max_tokens      */
 /* After PKV_DEV_TIMEOUT the launch that set it may have ended with bulk
  * copies still in flight into its shared memory (the drain after a timeout
  * is itself bounded).  Treat the stream as failed: that launch's outputs,
@@ -128,6 +133,71 @@ typedef struct {
 int paged_kv_write(const pkv_cache* cache, const void* k, const void* v,
                    const int64_t* slot_mapping, int64_t num_tokens,
                    cudaStream_t stream);
+
+/*
+ * pkv_rotary -- a rotary embedding with one or several position axes (one
+ * for text; time, height and width for images and video), as the kernels
+ * take it.  Filled by paged_rotary_init; plain data, copied by value.
+ */
+#define PKV_ROTARY_MAX_PAIRS 128
+#define PKV_ROTARY_MAX_AXES 8
+typedef struct {
+  int32_t rotary_dim;    /* R: leading elements of a head that rotate (even)  */
+  int32_t num_axes;
+  int32_t interleaved;   /* pair i is (2i, 2i + 1), else (i, i + R / 2)       */
+  int32_t reserved;
+  uint64_t step[PKV_ROTARY_MAX_PAIRS];  /* turns per position, units of 2^-64 */
+  uint8_t axis[PKV_ROTARY_MAX_PAIRS];   /* which axis gives pair i's position */
+} pkv_rotary;
+
+/*
+ * paged_rotary_init -- prepare a rotary embedding (host only).
+ *
+ *   rotary_dim   even, 2 .. 256
+ *   num_axes     1 .. 8
+ *   inv_freq     host, double[rotary_dim / 2]: radians per position of each
+ *                pair, of magnitude at most 2^20
+ *   pair_axis    host, int32[rotary_dim / 2]: axis of each pair (NULL with
+ *                one axis)
+ */
+int paged_rotary_init(pkv_rotary* rotary, int32_t rotary_dim, int32_t num_axes,
+                      const double* inv_freq, const int32_t* pair_axis, int32_t interleaved);
+
+/*
+ * paged_rope_kv_write -- rotate each token's queries and keys by its
+ * positions, store keys and values in the token's slot.
+ *
+ * paged_kv_write with the rotary embedding in front of it, in one pass.  For
+ * token t and pair i of rotary (elements x, y of every query and key head):
+ *     a = positions[axis_i][t] * inv_freq_i
+ *     x' = x cos a - y sin a,   y' = y cos a + x sin a
+ * in float32 from angles reduced exactly, for any 32-bit position (negative
+ * ones too).  Elements from rotary_dim on, and values, are copied.  q_out
+ * and the pool rows are rounded once (FP8 pools: e4m3(x / scale[h]) from the
+ * float32 values, as in paged_kv_write).  Every token's query is written;
+ * keys and values only where slot_mapping[t] >= 0 (a negative slot marks
+ * padding).  A slot >= num_blocks * b is skipped and sets
+ * PKV_DEV_SLOT_RANGE.  Two tokens with the same slot race.
+ *
+ *   q, k, v       device, token t's heads at q + t * q_stride (and so on):
+ *                 [num_heads or num_kv_heads][head_dim] contiguous, io type;
+ *                 16-byte aligned, strides in elements, multiples of 16
+ *                 bytes (slices of one fused projection are fine)
+ *   positions     device, int32[num_axes][num_tokens]
+ *   slot_mapping  device, int64[num_tokens]
+ *   num_heads     query heads (any count)
+ *   q_out         device, as q with q_out_stride; may be q (same stride)
+ *
+ * head_dim as for paged_kv_write; rotary_dim at most head_dim.  With halves
+ * (not interleaved) whose length rotary_dim / 2 is not a whole number of
+ * 16-byte vectors the kernel moves single elements, and head_dim is at most
+ * 512 (else PKV_ERR_GEOMETRY).
+ */
+int paged_rope_kv_write(const pkv_cache* cache, const pkv_rotary* rotary, const void* q,
+                        int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping,
+                        int64_t num_tokens, int32_t num_heads, void* q_out, int64_t q_out_stride,
+                        cudaStream_t stream);
 
 /*
  * paged_attention_partition_size -- the partition length (in positions) a
@@ -241,6 +311,60 @@ int paged_attention_prefill(const pkv_cache* cache, const void* q, int64_t total
                             const int32_t* block_tables, int32_t max_blocks_per_seq,
                             const int32_t* seq_lens, int32_t num_heads, float scale, void* out,
                             cudaStream_t stream);
+
+/*
+ * paged_attention_cross -- attention of each sequence's queries to all of
+ * its encoder's cached states: cross attention, where queries and states
+ * have lengths of their own and no query is masked from any state.
+ *
+ * The encoder's keys and values lie in the pool like a sequence's own
+ * (written by paged_kv_write), under a table of their own.  Sequence s has
+ * Q = query_starts[s+1] - query_starts[s] >= 0 queries and
+ * L = enc_lens[s] >= 0 states, either the longer:
+ *     z_t = scale * dot(q[query_starts[s] + i][h], K_t)      t = 0 .. L-1
+ *     out[query_starts[s] + i][h] = softmax-weighted mean of V_t as in
+ *     paged_attention_decode; zeros where L = 0 (a request without an
+ *     encoder's states; no error)
+ * accumulated in float32.  One query per sequence is the decode step; forks
+ * that read one encoder's states (beams, parallel samples) are best given as
+ * several queries of one sequence, which reads each page once for all.
+ * When there are too few query rows to fill the GPU the states are split
+ * into runs that are computed apart and merged.
+ *
+ * fp16, bf16, fp32 and FP8 pools; head_dim, block_size and head grouping as
+ * for paged_attention_decode.  fp16 and bf16 pools, and FP8 pools of
+ * head_dim 128, run on tensor cores, where probabilities are rounded to the
+ * 16-bit operand type (bf16 pools: bf16; others: fp16) and sums are not.
+ *
+ *   q, out        device, [total_queries][num_heads][head_dim], cache dtype
+ *                 (io_dtype for FP8 pools)
+ *   query_starts  device, int32[num_seqs + 1], non-decreasing, last <=
+ *                 total_queries; rows of out from the last on are left as
+ *                 they were
+ *   max_queries   host bound on any sequence's Q (sizes the launch), >= 1
+ *   block_tables, scale: as for paged_attention_decode
+ *   enc_lens      device, int32[num_seqs]
+ *   max_enc_len   host bound on enc_lens (0 = max_blocks_per_seq * b), at
+ *                 most 2^30
+ *   workspace     device, >= paged_attention_cross_workspace_bytes(...) with
+ *                 the same arguments (max_enc_len there is the bound itself,
+ *                 not 0), 16-byte aligned; may be NULL when that is 0.  Calls
+ *                 that may overlap need one each.
+ *
+ * A sequence with Q > max_queries or L outside [0, max_enc_len] gets zero
+ * rows and PKV_DEV_SEQ_LEN, one whose used table entries leave
+ * [0, num_blocks) zero rows and PKV_DEV_TABLE_RANGE; one whose query range
+ * leaves [0, total_queries) sets PKV_DEV_SEQ_LEN and is not written.
+ */
+size_t paged_attention_cross_workspace_bytes(const pkv_cache* cache, int64_t total_queries,
+                                             int32_t num_seqs, int32_t num_heads,
+                                             int32_t max_queries, int32_t max_enc_len);
+int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_queries,
+                          const int32_t* query_starts, int32_t num_seqs, int32_t max_queries,
+                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                          const int32_t* enc_lens, int32_t max_enc_len, int32_t num_heads,
+                          float scale, void* out, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
 
 /*
  * paged_attention_decode_shared -- paged_attention_decode for batches in
@@ -381,6 +505,64 @@ int paged_block_copy(const pkv_cache* cache, const int64_t* src_dst_pairs,
 int paged_block_swap(const pkv_cache* cache, void* host_k, void* host_v, int64_t host_blocks,
                      const int64_t* src_dst_pairs, int64_t num_pairs, int32_t direction,
                      cudaStream_t stream);
+
+/*
+ * paged_build_tables -- one step's block tables, slot map, query starts and
+ * positions, built on the device from the rows' lengths.
+ *
+ * The device counterpart of the host block manager's admit, append and
+ * release ([vLLM-TGI] "Exact CPU block manager and copy-on-write") for
+ * callers whose lengths live on the device (a decode loop in a CUDA graph, a
+ * scheduler on the GPU).  Row s holds old_lens[s] positions and is to hold
+ * new_lens[s]: more (admission, prefill chunk, decode step), fewer (rollback
+ * of drafted tokens), 0 (release), or as many.  With b = block_size,
+ * have = ceil(old / b) and want = ceil(new / b):
+ *   - a row that grows takes want - have blocks from the head of the ring of
+ *     free blocks into table entries have .. want - 1, rows in order, logical
+ *     blocks in order;
+ *   - a row that shrinks gives entries want .. have - 1 back behind the
+ *     ring's tail in the same order; they can be taken from the next call on;
+ *     the table entries themselves stay as they were, as does every entry
+ *     past a row's length;
+ *   - query_starts[s] counts the new tokens of the rows before s (new - old
+ *     where the row grows, else 0); token t of row s has position
+ *     p = old_lens[s] + t - query_starts[s], positions[t] = p and
+ *     slot_mapping[t] = table[s][p / b] * b + p % b;
+ *   - entries from query_starts[num_seqs] up to max_tokens are padding: slot
+ *     -1, position 0.
+ * The outputs feed paged_kv_write, paged_rope_kv_write and the attention
+ * calls as they are.  Every block belongs to one row: tables with shared
+ * blocks (forks) are the host block manager's.
+ *
+ * All or nothing: if the free blocks do not cover the step (PKV_DEV_NOMEM),
+ * the new tokens exceed max_tokens (PKV_DEV_TOKENS), a length is outside
+ * [0, max_blocks_per_seq * b] (PKV_DEV_SEQ_LEN), an entry that is given back
+ * or written to is outside [0, num_blocks) (PKV_DEV_TABLE_RANGE), or the ring
+ * is inconsistent (PKV_DEV_FREE_LIST), then seq_lens = old_lens, the state,
+ * ring and tables stay as they were, query_starts is all zeros and every
+ * token is padding.
+ *
+ *   free_list       device, int32[num_blocks]: a ring of block ids; updated
+ *                   in place (only behind the tail)
+ *   free_state      device, int64[2] {head, count}: the free blocks are
+ *                   free_list[(head + i) % num_blocks], i < count
+ *   free_state_out  device, int64[2]: the state after the step; may be
+ *                   free_state
+ *   old_lens, new_lens  device, int32[num_seqs]; at most 65535 rows
+ *   block_tables    device, int32[num_seqs][max_blocks_per_seq], updated
+ *   seq_lens        device, int32[num_seqs]: the lengths after the step; may
+ *                   be old_lens or new_lens
+ *   query_starts    device, int32[num_seqs + 1]
+ *   slot_mapping    device, int64[max_tokens]
+ *   positions       device, int32[max_tokens]
+ *   max_tokens      0 .. 2^30; with 0 the two arrays may be NULL
+ */
+int paged_build_tables(int64_t num_blocks, int32_t block_size, int32_t* free_list,
+                       const int64_t* free_state, const int32_t* old_lens,
+                       const int32_t* new_lens, int32_t num_seqs, int32_t* block_tables,
+                       int32_t max_blocks_per_seq, int32_t* seq_lens, int64_t* free_state_out,
+                       int32_t* query_starts, int64_t* slot_mapping, int32_t* positions,
+                       int64_t max_tokens, cudaStream_t stream);
 
 /*
  * paged_get_device_error -- synchronise `stream`, then read and clear the

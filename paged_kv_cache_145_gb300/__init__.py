@@ -17,8 +17,9 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import (PKV_DEV_PAIR_RANGE, PKV_DEV_SEQ_LEN, PKV_DEV_SLOT_RANGE,  # noqa: F401
-                   PKV_DEV_TABLE_RANGE, PKV_DEV_TIMEOUT, PKV_ERR_NOMEM, PKV_SWAP_IN,
+from ._lib import (PKV_DEV_FREE_LIST, PKV_DEV_NOMEM, PKV_DEV_PAIR_RANGE,  # noqa: F401
+                   PKV_DEV_SEQ_LEN, PKV_DEV_SLOT_RANGE, PKV_DEV_TABLE_RANGE, PKV_DEV_TIMEOUT,
+                   PKV_DEV_TOKENS, PKV_ERR_NOMEM, PKV_SWAP_IN,
                    PKV_SWAP_OUT)
 
 _DTYPE_CODE = {torch.float32: _lib.PKV_F32, torch.float16: _lib.PKV_F16, torch.bfloat16: _lib.PKV_BF16,
@@ -30,6 +31,8 @@ __all__ = [
     "paged_attention_workspace_bytes", "paged_attention_partition_size",
     "paged_block_copy", "paged_block_swap", "paged_get_device_error",
     "paged_selftest_wait_timeout", "paged_selftest_read_stream", "paged_attention_decode_shared",
+    "paged_build_tables", "RotaryAxes", "paged_rope_kv_write", "paged_attention_cross",
+    "paged_attention_cross_workspace_bytes",
     "library_path",
 ]
 
@@ -45,6 +48,34 @@ def _ptr(t):
 def _stream(stream):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+class _on:
+    """Enters a tensor's device, and the stream that the call runs on, so that
+    what the call allocates belongs to that stream; gives the stream's
+    handle."""
+
+    __slots__ = ("device", "stream", "inner")
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+        self.device, self.stream, self.inner = device, stream, None
+
+    def __enter__(self):
+        if self.stream is not None:
+            self.inner = torch.cuda.stream(self.stream)  # enters the stream's device too
+            self.inner.__enter__()
+            return self.stream.cuda_stream
+        if torch.cuda.current_device() != self.device.index:
+            self.inner = torch.cuda.device(self.device)
+            self.inner.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
+        return False
 
 
 def _need(t, name, dtype=None, device=None):
@@ -119,6 +150,96 @@ def paged_kv_write(cache, k, v, slot_mapping, stream=None):
         raise ValueError("k and v must be [num_tokens, kv_heads, head_dim]")
     _lib.check(_lib.lib().paged_kv_write(cache.ref, _ptr(k), _ptr(v), _ptr(slot_mapping), n,
                                          _stream(stream)), "paged_kv_write")
+
+
+class RotaryAxes:
+    """A rotary embedding with one or several position axes.
+
+    ``rotary_dim``: leading elements of a head that rotate (even);
+    ``inv_freq``: radians per position of each of the ``rotary_dim / 2``
+    pairs; ``pair_axis``: the axis whose position turns each pair (None: one
+    axis); ``interleaved``: pairs are neighbours (2i, 2i + 1) instead of
+    halves (i, i + rotary_dim / 2).
+    """
+
+    def __init__(self, rotary_dim, inv_freq, pair_axis=None, interleaved=False):
+        freq = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
+        if freq.shape != (rotary_dim // 2,):
+            raise ValueError("inv_freq must hold rotary_dim / 2 frequencies")
+        axes = None
+        if pair_axis is not None:
+            axes = np.ascontiguousarray(np.asarray(pair_axis, dtype=np.int32))
+            if axes.shape != freq.shape or axes.min(initial=0) < 0:
+                raise ValueError("pair_axis must name an axis for each pair")
+        self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
+        self.num_axes = 1 if axes is None else int(axes.max(initial=0)) + 1
+        self._c = _lib.pkv_rotary()
+        _lib.check(_lib.lib().paged_rotary_init(
+            ctypes.byref(self._c), self.rotary_dim, self.num_axes, freq.ctypes.data,
+            None if axes is None else axes.ctypes.data, int(self.interleaved)), "RotaryAxes")
+
+    @classmethod
+    def sections(cls, sections, base=10000.0, interleaved=False):
+        """Contiguous runs of pairs, one per axis (``[16, 24, 24]``: the first
+        16 of 64 pairs turn with axis 0, ...), at frequencies
+        ``base ** (-2 i / rotary_dim)``."""
+        pairs = int(sum(sections))
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+        return cls(2 * pairs, [float(base) ** (-i / pairs) for i in range(pairs)], axis, interleaved)
+
+    @property
+    def ref(self):
+        return ctypes.byref(self._c)
+
+
+def _need_rows(t, name, heads, dim, dtype, device):
+    """[T, heads, dim] whose heads are contiguous; tokens may be strided."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != dtype or t.device != device:
+        raise ValueError("%s must be %s on %s, got %s on %s" % (name, dtype, device, t.dtype, t.device))
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError("%s must be [num_tokens, %d, %d]" % (name, heads, dim))
+    s = t.stride()
+    if (dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim):
+        raise ValueError("%s must have contiguous heads" % name)
+    return s[0]
+
+
+def paged_rope_kv_write(cache, rotary, q, k, v, positions, slot_mapping, q_out=None, stream=None):
+    """Rotate ``q`` ``[T, H, D]`` and ``k`` ``[T, Hk, D]`` by the tokens'
+    positions and store ``k`` and ``v`` at ``slot_mapping`` (int64 ``[T]``).
+
+    ``positions``: int32 ``[num_axes, T]`` (or ``[T]`` with one axis).  q, k
+    and v may be slices of one projection (heads contiguous, tokens strided
+    by a multiple of 16 bytes).  ``q_out`` may be ``q``; it is allocated when
+    not given.  Returns ``q_out``.
+    """
+    dev = cache.device
+    if q.dim() != 3:
+        raise ValueError("q must be [num_tokens, num_heads, head_dim]")
+    n, heads = q.shape[0], q.shape[1]
+    qs = _need_rows(q, "q", heads, cache.head_dim, cache.io_dtype, dev)
+    ks = _need_rows(k, "k", cache.num_kv_heads, cache.head_dim, cache.io_dtype, dev)
+    vs = _need_rows(v, "v", cache.num_kv_heads, cache.head_dim, cache.io_dtype, dev)
+    _need(positions, "positions", torch.int32, dev)
+    _need(slot_mapping, "slot_mapping", torch.int64, dev)
+    if k.shape[0] != n or v.shape[0] != n or slot_mapping.shape != (n,):
+        raise ValueError("q, k, v and slot_mapping must hold one entry per token")
+    if positions.shape != (rotary.num_axes, n) and not (rotary.num_axes == 1 and
+                                                        positions.shape == (n,)):
+        raise ValueError("positions must be [num_axes, num_tokens]")
+    with _on(dev, stream) as st:
+        if q_out is None:
+            q_out = torch.empty((n, heads, cache.head_dim), dtype=cache.io_dtype, device=dev)
+        os = _need_rows(q_out, "q_out", heads, cache.head_dim, cache.io_dtype, dev)
+        if q_out.shape[0] != n:
+            raise ValueError("q_out must have q's shape")
+        _lib.check(_lib.lib().paged_rope_kv_write(
+            cache.ref, rotary.ref, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+            positions.data_ptr(), slot_mapping.data_ptr(), n, heads, q_out.data_ptr(), os, st),
+            "paged_rope_kv_write")
+    return q_out
 
 
 def paged_attention_partition_size(cache, num_seqs, num_heads, max_seq_len, partition_size=0):
@@ -244,6 +365,64 @@ def paged_attention_prefill(cache, q, query_starts, block_tables, seq_lens, scal
     return out
 
 
+def paged_attention_cross_workspace_bytes(cache, total_queries, num_seqs, num_heads, max_queries,
+                                          max_enc_len):
+    """Bytes of workspace that :func:`paged_attention_cross` needs."""
+    return int(_lib.lib().paged_attention_cross_workspace_bytes(
+        cache.ref, total_queries, num_seqs, num_heads, max_queries, max_enc_len))
+
+
+def paged_attention_cross(cache, q, query_starts, block_tables, enc_lens, scale, max_queries,
+                          max_enc_len=0, out=None, workspace=None, stream=None):
+    """Attention of each sequence's queries to all of its encoder's cached
+    states (no causal mask).
+
+    ``q``: ``[total_queries, H, D]``, sequence s's queries at
+    ``query_starts[s] .. query_starts[s + 1] - 1``; ``query_starts``: int32
+    ``[S + 1]``; ``block_tables``: int32 ``[S, max_blocks]`` of the encoder's
+    states; ``enc_lens``: int32 ``[S]``, how many there are (0: zero rows);
+    ``max_queries``: host bound on a sequence's queries; ``max_enc_len``:
+    host bound on ``enc_lens`` (0 = table width x block size).  Rows of
+    ``out`` behind the last sequence's are left as they were.  Returns
+    ``out``.
+    """
+    dev = cache.device
+    _need(q, "q", cache.io_dtype, dev)
+    _need(query_starts, "query_starts", torch.int32, dev)
+    _need(block_tables, "block_tables", torch.int32, dev)
+    _need(enc_lens, "enc_lens", torch.int32, dev)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError("q must be [total_queries, num_heads, head_dim]")
+    num_seqs = enc_lens.numel()
+    if enc_lens.shape != (num_seqs,) or query_starts.shape != (num_seqs + 1,) or \
+            block_tables.dim() != 2 or block_tables.shape[0] != num_seqs:
+        raise ValueError("enc_lens must be [S], query_starts [S + 1] and block_tables [S, max_blocks]")
+    max_queries, max_enc_len = int(max_queries), int(max_enc_len)
+    lib = _lib.lib()
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _need(out, "out", cache.io_dtype, dev)
+            if out.shape != q.shape:
+                raise ValueError("out must have q's shape")
+        if workspace is None:
+            bound = max_enc_len if max_enc_len else block_tables.shape[1] * cache.block_size
+            need = lib.paged_attention_cross_workspace_bytes(cache.ref, q.shape[0], num_seqs,
+                                                             q.shape[1], max_queries, bound)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _need(workspace, "workspace", None, dev)
+        ws, ws_len = (None, 0) if workspace is None else (
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        _lib.check(lib.paged_attention_cross(
+            cache.ref, q.data_ptr(), q.shape[0], query_starts.data_ptr(), num_seqs, max_queries,
+            block_tables.data_ptr(), block_tables.shape[1], enc_lens.data_ptr(), max_enc_len,
+            q.shape[1], float(scale), out.data_ptr(), ws, ws_len, st), "paged_attention_cross")
+    return out
+
+
 def paged_block_copy(cache, pairs, stream=None):
     """Copy blocks ``pairs[i, 0] -> pairs[i, 1]`` (int64 ``[n, 2]``)."""
     _need(pairs, "pairs", torch.int64, cache.device)
@@ -277,6 +456,64 @@ def paged_block_swap(cache, host_k, host_v, pairs, direction, stream=None):
     _lib.check(_lib.lib().paged_block_swap(cache.ref, _ptr(host_k), _ptr(host_v), host_k.shape[0],
                                            _ptr(pairs), n, int(direction), _stream(stream)),
                "paged_block_swap")
+
+
+def _output(t, name, shape, dtype, device):
+    """``t`` checked against what the call writes, or a new tensor."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, name, dtype, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    return t
+
+
+def paged_build_tables(free_list, free_state, old_lens, new_lens, block_tables, block_size,
+                       max_tokens, seq_lens=None, free_state_out=None, query_starts=None,
+                       slot_mapping=None, positions=None, stream=None):
+    """Block tables, slot map, query starts and positions of one step, on the
+    device: rows go from ``old_lens`` to ``new_lens`` positions, taking blocks
+    from a ring of free ones or giving them back.
+
+    ``free_list``: int32 ``[num_blocks]`` ring, updated in place;
+    ``free_state``: int64 ``[2]`` (head, count); ``old_lens``/``new_lens``:
+    int32 ``[S]``; ``block_tables``: int32 ``[S, max_blocks]``, updated in
+    place; ``max_tokens``: length of the slot map (tokens past the step's are
+    padding, slot -1).  Outputs are allocated when not given;
+    ``seq_lens`` may be ``old_lens`` and ``free_state_out`` may be
+    ``free_state``.  Returns ``(seq_lens, free_state_out, query_starts,
+    slot_mapping, positions)``.  A step that cannot be taken whole changes
+    nothing and sets a device error bit (``PKV_DEV_NOMEM`` when blocks run
+    out).
+    """
+    _need(free_list, "free_list", torch.int32)
+    dev = free_list.device
+    _need(free_state, "free_state", torch.int64, dev)
+    _need(old_lens, "old_lens", torch.int32, dev)
+    _need(new_lens, "new_lens", torch.int32, dev)
+    _need(block_tables, "block_tables", torch.int32, dev)
+    n = old_lens.numel()
+    if free_list.dim() != 1 or free_state.shape != (2,):
+        raise ValueError("free_list must be [num_blocks] and free_state [2]")
+    if old_lens.shape != (n,) or new_lens.shape != (n,) or block_tables.dim() != 2 or \
+            block_tables.shape[0] != n:
+        raise ValueError("old_lens and new_lens must be [S] and block_tables [S, max_blocks]")
+    max_tokens = int(max_tokens)
+    if max_tokens < 0:
+        raise ValueError("max_tokens must not be negative")
+    with _on(dev, stream) as st:
+        seq_lens = _output(seq_lens, "seq_lens", (n,), torch.int32, dev)
+        free_state_out = _output(free_state_out, "free_state_out", (2,), torch.int64, dev)
+        query_starts = _output(query_starts, "query_starts", (n + 1,), torch.int32, dev)
+        slot_mapping = _output(slot_mapping, "slot_mapping", (max_tokens,), torch.int64, dev)
+        positions = _output(positions, "positions", (max_tokens,), torch.int32, dev)
+        _lib.check(_lib.lib().paged_build_tables(
+            free_list.numel(), int(block_size), free_list.data_ptr(), free_state.data_ptr(),
+            old_lens.data_ptr(), new_lens.data_ptr(), n, block_tables.data_ptr(),
+            block_tables.shape[1], seq_lens.data_ptr(), free_state_out.data_ptr(),
+            query_starts.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), max_tokens,
+            st), "paged_build_tables")
+    return seq_lens, free_state_out, query_starts, slot_mapping, positions
 
 
 def paged_get_device_error(stream=None):

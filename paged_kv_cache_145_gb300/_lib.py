@@ -19,6 +19,9 @@ PKV_DEV_PAIR_RANGE = 8
 PKV_DEV_TIMEOUT = 16
 PKV_DEV_SHARING = 32
 PKV_DEV_LAUNCH = 64
+PKV_DEV_NOMEM = 128
+PKV_DEV_FREE_LIST = 256
+PKV_DEV_TOKENS = 512
 
 PKV_ERR_WORKSPACE = -5
 PKV_ERR_NOMEM = -8
@@ -41,10 +44,22 @@ class pkv_cache(ctypes.Structure):
     ]
 
 
+class pkv_rotary(ctypes.Structure):
+    _fields_ = [
+        ("rotary_dim", ctypes.c_int32),
+        ("num_axes", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("step", ctypes.c_uint64 * 128),
+        ("axis", ctypes.c_uint8 * 128),
+    ]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _CACHE = ctypes.POINTER(pkv_cache)
+_ROTARY = ctypes.POINTER(pkv_rotary)
 
 # name -> (restype, argtypes); every symbol the header declares.
 SIGNATURES = {
@@ -62,6 +77,15 @@ SIGNATURES = {
                                                _I32, ctypes.c_float, _P, _P]),
     "paged_block_copy": (ctypes.c_int, [_CACHE, _P, _I64, _P]),
     "paged_block_swap": (ctypes.c_int, [_CACHE, _P, _P, _I64, _P, _I64, _I32, _P]),
+    "paged_attention_cross_workspace_bytes": (ctypes.c_size_t, [_CACHE, _I64, _I32, _I32, _I32,
+                                                                _I32]),
+    "paged_attention_cross": (ctypes.c_int, [_CACHE, _P, _I64, _P, _I32, _I32, _P, _I32, _P, _I32,
+                                             _I32, ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
+    "paged_rotary_init": (ctypes.c_int, [_ROTARY, _I32, _I32, _P, _P, _I32]),
+    "paged_rope_kv_write": (ctypes.c_int, [_CACHE, _ROTARY, _P, _I64, _P, _I64, _P, _I64, _P, _P,
+                                           _I64, _I32, _P, _I64, _P]),
+    "paged_build_tables": (ctypes.c_int, [_I64, _I32, _P, _P, _P, _P, _I32, _P, _I32, _P, _P, _P,
+                                          _P, _P, _I64, _P]),
     "paged_get_device_error": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "paged_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, _P]),
     "paged_selftest_read_stream": (ctypes.c_int, [_P, ctypes.c_size_t, _P, _P]),

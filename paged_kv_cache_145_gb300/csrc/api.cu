@@ -2,15 +2,24 @@
 // The semantics of each call are documented in include/pagedkv.h.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
 
+#include "cross.cuh"
 #include "decode_launch.cuh"
 #include "prefill.cuh"
 
 int pkv_launch_kv_write(const pkv_cache* c, const void* k, const void* v, const int64_t* slots,
                         int64_t num_tokens, size_t elem_bytes, cudaStream_t stream);
+int pkv_launch_cross(const pkv::CrossParams& p, int dtype, int io_dtype, int num_seqs, int dim,
+                     cudaStream_t stream);
+int pkv_launch_rope_write(const pkv_cache* c, const pkv_rotary* rot, const void* q,
+                          int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const int32_t* positions, const int64_t* slots,
+                          int64_t num_tokens, int num_heads, void* q_out, int64_t q_out_stride,
+                          cudaStream_t stream);
 int pkv_launch_kv_write_fp8(const pkv_cache* c, const void* k, const void* v,
                             const int64_t* slots, int64_t num_tokens, cudaStream_t stream);
 int pkv_launch_decode_fp8(const pkv::DecodeParams& p, int num_seqs, int head_dim, int block_size,
@@ -246,6 +255,44 @@ int paged_kv_write(const pkv_cache* cache, const void* k, const void* v,
                              stream);
 }
 
+int paged_rope_kv_write(const pkv_cache* cache, const pkv_rotary* rotary, const void* q,
+                        int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping,
+                        int64_t num_tokens, int32_t num_heads, void* q_out, int64_t q_out_stride,
+                        cudaStream_t stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  rc = check_scales(cache);
+  if (rc) return rc;
+  if (!rotary) return PKV_ERR_NULL;
+  if (rotary->rotary_dim < 2 || rotary->rotary_dim % 2 ||
+      rotary->rotary_dim > 2 * PKV_ROTARY_MAX_PAIRS || rotary->num_axes < 1 ||
+      rotary->num_axes > PKV_ROTARY_MAX_AXES)
+    return PKV_ERR_ARG;
+  if (rotary->rotary_dim > cache->head_dim) return PKV_ERR_GEOMETRY;
+  if (num_tokens < 0 || num_tokens > INT32_MAX || num_heads < 1) return PKV_ERR_ARG;
+  for (int i = 0; i < rotary->rotary_dim / 2; ++i)
+    if (rotary->axis[i] >= rotary->num_axes) return PKV_ERR_ARG;
+  if (num_tokens == 0) return PKV_OK;
+  if (!q || !k || !v || !positions || !slot_mapping || !q_out) return PKV_ERR_NULL;
+  const int64_t D = cache->head_dim;
+  const int64_t io = cache->dtype == PKV_FP8_E4M3 ? 2 : (int64_t)elem_bytes(cache->dtype);
+  const int64_t rows[4] = {q_stride, q_out_stride, k_stride, v_stride};
+  for (int i = 0; i < 4; ++i) {
+    const int64_t heads = i < 2 ? num_heads : cache->num_kv_heads;
+    if (num_tokens > 1 && rows[i] < heads * D) return PKV_ERR_ARG;
+    if (num_tokens > 1 && rows[i] * io % 16) return PKV_ERR_ALIGN;
+  }
+  // FP8 rows of 16 codes hold whole 16-byte vectors of the io type too.
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+    return PKV_ERR_ALIGN;
+  if (!pkv_error_word()) return PKV_ERR_CUDA;
+  return pkv_launch_rope_write(cache, rotary, q, q_stride, k, k_stride, v, v_stride, positions,
+                               slot_mapping, num_tokens, num_heads, q_out, q_out_stride, stream);
+}
+
 int32_t paged_attention_partition_size(const pkv_cache* cache, int32_t num_seqs,
                                        int32_t num_heads, int32_t max_seq_len,
                                        int32_t requested) {
@@ -469,6 +516,123 @@ int paged_attention_prefill(const pkv_cache* cache, const void* q, int64_t total
                                      cache->block_size, group, mk, mv, stream);
   return (f16 ? pkv_launch_prefill_tc_f16 : pkv_launch_prefill_tc_bf16)(
       p, num_seqs, cache->head_dim, cache->block_size, group, mk, mv, stream);
+}
+
+namespace {
+
+// Split of cross attention's states: the longest parts that still give about
+// two thread blocks per SM, in whole 128-position runs.  rows: rows per
+// thread block.
+struct CrossSplit {
+  int parts, part;
+};
+
+CrossSplit cross_split(const pkv_cache* c, int num_seqs, int num_heads, int max_queries,
+                       int max_len) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+    cudaGetLastError();
+    sms = 1;
+  }
+  const int64_t rows = (int64_t)max_queries * (num_heads / c->num_kv_heads);
+  const int64_t blocks = (int64_t)num_seqs * c->num_kv_heads * ((rows + pkv::kCrossRows - 1) / pkv::kCrossRows);
+  constexpr int kRun = 128;
+  const int64_t runs = std::max<int64_t>(1, (max_len + kRun - 1) / kRun);
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(runs, 2 * sms / std::max<int64_t>(1, blocks)));
+  const int64_t part = (runs + want - 1) / want * kRun;
+  return {(int)((runs * kRun + part - 1) / part), (int)part};
+}
+
+// Bytes of the (m, l) pairs and where the partial outputs start.
+WsLayout cross_workspace(int64_t total_queries, int num_heads, int head_dim, int parts) {
+  WsLayout w{};
+  w.parts = parts;
+  if (parts <= 1) return w;
+  const size_t rows = (size_t)total_queries * num_heads * parts;
+  w.ml_bytes = rows * sizeof(float2);
+  w.o_offset = (w.ml_bytes + 255) & ~size_t(255);
+  w.total = w.o_offset + rows * head_dim * sizeof(float);
+  return w;
+}
+
+bool cross_args_ok(const pkv_cache* c, int64_t total_queries, int num_seqs, int num_heads,
+                   int max_queries) {
+  return num_seqs >= 0 && num_seqs <= 65535 && num_heads >= 1 && max_queries >= 1 &&
+         total_queries >= 0 && total_queries <= INT32_MAX && c->num_kv_heads >= 1 &&
+         num_heads % c->num_kv_heads == 0;
+}
+
+}  // namespace
+
+size_t paged_attention_cross_workspace_bytes(const pkv_cache* cache, int64_t total_queries,
+                                             int32_t num_seqs, int32_t num_heads,
+                                             int32_t max_queries, int32_t max_enc_len) {
+  if (!cache || !cross_args_ok(cache, total_queries, num_seqs, num_heads, max_queries) ||
+      max_enc_len < 0)
+    return 0;
+  const CrossSplit sp = cross_split(cache, num_seqs, num_heads, max_queries, max_enc_len);
+  return cross_workspace(total_queries, num_heads, cache->head_dim, sp.parts).total;
+}
+
+int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_queries,
+                          const int32_t* query_starts, int32_t num_seqs, int32_t max_queries,
+                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                          const int32_t* enc_lens, int32_t max_enc_len, int32_t num_heads,
+                          float scale, void* out, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  rc = check_scales(cache);
+  if (rc) return rc;
+  if (num_heads < 1 || !decode_geometry_ok(cache, num_heads)) return PKV_ERR_GEOMETRY;
+  if (!cross_args_ok(cache, total_queries, num_seqs, num_heads, max_queries) ||
+      max_blocks_per_seq < 0 || !std::isfinite(scale))
+    return PKV_ERR_ARG;
+  if (num_seqs == 0 || total_queries == 0) return PKV_OK;
+  const int64_t cap = (int64_t)max_blocks_per_seq * cache->block_size;
+  if (max_enc_len < 0 || max_enc_len > cap || (max_enc_len ? max_enc_len : cap) > (1 << 30))
+    return PKV_ERR_ARG;
+  const int max_len = max_enc_len ? max_enc_len : (int)cap;
+  if (!q || !out || !query_starts || !enc_lens || (!block_tables && max_len > 0)) return PKV_ERR_NULL;
+  if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
+      (reinterpret_cast<uintptr_t>(enc_lens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(query_starts) & 3u))
+    return PKV_ERR_ALIGN;
+  const CrossSplit sp = cross_split(cache, num_seqs, num_heads, max_queries, max_len);
+  const WsLayout ws = cross_workspace(total_queries, num_heads, cache->head_dim, sp.parts);
+  if (ws.total > 0) {
+    if (!workspace || workspace_bytes < ws.total) return PKV_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return PKV_ERR_ALIGN;
+  }
+  unsigned* err = pkv_error_word();
+  if (!err) return PKV_ERR_CUDA;
+  pkv::CrossParams p{};
+  p.k_cache = cache->k_cache;
+  p.v_cache = cache->v_cache;
+  p.num_blocks = cache->num_blocks;
+  p.kv_heads = cache->num_kv_heads;
+  p.num_heads = num_heads;
+  p.group = num_heads / cache->num_kv_heads;
+  p.block_size = cache->block_size;
+  p.q = q;
+  p.out = out;
+  p.starts = query_starts;
+  p.total_queries = total_queries;
+  p.max_queries = max_queries;
+  p.tables = block_tables;
+  p.max_blocks = max_blocks_per_seq;
+  p.lens = enc_lens;
+  p.max_len = max_len;
+  p.qscale = scale * 1.4426950408889634f;  // log2(e): scores in base-2 units
+  p.parts = sp.parts;
+  p.part = sp.part;
+  p.ws_ml = ws.total ? static_cast<float2*>(workspace) : nullptr;
+  p.ws_o = ws.total ? reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.o_offset) : nullptr;
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.err = err;
+  return pkv_launch_cross(p, cache->dtype, cache->io_dtype, num_seqs, cache->head_dim, stream);
 }
 
 int paged_block_copy(const pkv_cache* cache, const int64_t* src_dst_pairs, int64_t num_pairs,

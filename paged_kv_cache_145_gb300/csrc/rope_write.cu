@@ -1,0 +1,326 @@
+// paged_rope_kv_write: rotary positions with several axes, fused with the
+// slot-mapped write of keys and values.
+//
+// The mathematics.  Frequency pair i of token t turns by
+// angle = pos[axis(i)][t] * inv_freq[i], and the elements of the pair
+// (x, y) become (x cos - y sin, y cos + x sin).  Angles of far positions need
+// more than float32 (position 2^20 at frequency 1 leaves 2^-4 radians): the
+// plan holds each frequency as turns per position in 64-bit fixed point, so
+// that position times frequency modulo one turn is one wrapping integer
+// product, exact to 2^-33 turns for any 32-bit position; its top 32 bits
+// are the reduced angle that sincospif takes.
+//
+// What bounds it: HBM traffic (q, k and v in, q and the pool rows out), and
+// latency for a decode step's few tokens.  The angles of a token serve all of
+// its query and key heads, so a thread block computes them once into shared
+// memory and then streams heads through 16-byte loads and stores, the first
+// of them issued before the angles are computed.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "common.cuh"
+
+namespace pkv {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 4;  // tokens per thread block, at most
+
+struct RopeParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;  // elements per token
+  void* k_cache;
+  void* v_cache;
+  const float* k_scale;   // FP8 pools
+  const float* v_scale;
+  const int32_t* positions;  // [axes][T]
+  const int64_t* slots;      // [T]
+  int64_t num_tokens;
+  int64_t num_blocks;
+  int block_size;
+  int heads, kv_heads, dim;
+  int tokens;             // tokens per thread block
+  int units;              // units per head
+  unsigned* err;
+  pkv_rotary rot;
+};
+
+// V consecutive elements as float.
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(const T* p, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = static_cast<float>(*p);
+  } else {
+    RowLoad<T, V>::load(p, f);
+  }
+}
+
+// V consecutive elements rounded once to the output type.
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
+  if constexpr (V == 1) {
+    *p = Elem<T>::from_f(f[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  } else {
+    uint4 u;
+    u.x = pack_pair<T>(f[0], f[1]);
+    u.y = pack_pair<T>(f[2], f[3]);
+    u.z = pack_pair<T>(f[4], f[5]);
+    u.w = pack_pair<T>(f[6], f[7]);
+    *reinterpret_cast<uint4*>(p) = u;
+  }
+}
+
+// V elements into an FP8 pool: e4m3(x / scale), saturating, from the rotated
+// float32 values (one rounding).
+template <int V>
+__device__ __forceinline__ void store_codes(unsigned char* p, const float (&f)[V], float scale) {
+  if constexpr (V == 1) {
+    *p = (unsigned char)__nv_cvt_float_to_fp8(f[0] / scale, __NV_SATFINITE, __NV_E4M3);
+  } else {
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+          make_float2(f[4 * j] / scale, f[4 * j + 1] / scale), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+          make_float2(f[4 * j + 2] / scale, f[4 * j + 3] / scale), __NV_SATFINITE, __NV_E4M3);
+      w[j] = lo | (hi << 16);
+    }
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  }
+}
+
+// TI: type of q, k, v and q_out.  FP8: the pool holds codes, else TI.
+// INTER: pairs are neighbours (2i, 2i + 1), else halves (i, i + R / 2).
+// V: elements per load.  A head's units are two vectors each: with halves,
+// unit u < R / 2 / V is the vectors u and u + R / 2 / V, which hold each
+// other's partners; all other vectors go two to a unit in order.
+template <typename TI, bool FP8, bool INTER, int V>
+__global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ float2 s_cs[kRopeTokens * 128];
+  __shared__ int64_t s_row[kRopeTokens];  // pool row of head 0, or -1
+  const int tid = threadIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
+  const int nt = (int)min((int64_t)p.tokens, p.num_tokens - t0);
+  const int D = p.dim, H = p.heads, Hk = p.kv_heads, HT = H + 2 * Hk;
+  const int pairs = p.rot.rotary_dim >> 1;
+  const int half_vecs = INTER ? 0 : pairs / V;  // vectors in each rotated half
+  const int vecs = D / V;
+  const int U = p.units;
+
+  // unit `u` of row `x` (token x / HT, head x % HT)
+  struct Unit {
+    float a[V], b[V];
+    int tok, head, va, vb;  // head counts through q, k, v; vb < 0: one vector
+  };
+  auto fetch = [&](int x, int u, Unit& w) {
+    w.tok = x / HT;
+    w.head = x - w.tok * HT;
+    const int64_t t = t0 + w.tok;
+    if (w.head < H + Hk && u < half_vecs) {
+      w.va = u;
+      w.vb = u + half_vecs;
+    } else {
+      w.va = 2 * u;
+      w.vb = 2 * u + 1 < vecs ? 2 * u + 1 : -1;
+    }
+    const TI* src;
+    if (w.head < H)
+      src = static_cast<const TI*>(p.q) + t * p.q_stride + (int64_t)w.head * D;
+    else if (w.head < H + Hk)
+      src = static_cast<const TI*>(p.k) + t * p.k_stride + (int64_t)(w.head - H) * D;
+    else
+      src = static_cast<const TI*>(p.v) + t * p.v_stride + (int64_t)(w.head - H - Hk) * D;
+    load_vec<TI, V>(src + w.va * V, w.a);
+    if (w.vb >= 0) load_vec<TI, V>(src + w.vb * V, w.b);
+  };
+
+  const int lanes = kRopeThreads / U;  // rows in flight
+  const int u = tid % U, lane_row = tid / U;
+  const int rows = nt * HT;
+  const int step = lanes * (int)gridDim.y;
+  int x = (int)blockIdx.y * lanes + lane_row;
+  bool live = lane_row < lanes && x < rows;
+  Unit cur;
+  if (live) fetch(x, u, cur);
+
+  // ---- angles and pool rows of this block's tokens ---------------------------
+  for (int e = tid; e < nt * pairs; e += kRopeThreads) {
+    const int tok = e / pairs, i = e - tok * pairs;
+    const int64_t pos = p.positions[(int64_t)p.rot.axis[i] * p.num_tokens + t0 + tok];
+    const uint64_t turns = (uint64_t)pos * p.rot.step[i];  // modulo one turn
+    const float half_turns = (float)(int32_t)(turns >> 32) * 0x1p-31f;
+    float s, c;
+    sincospif(half_turns, &s, &c);
+    s_cs[tok * pairs + i] = make_float2(c, s);
+  }
+  if (tid < nt) {
+    const int64_t slot = p.slots[t0 + tid];
+    int64_t row = -1;
+    if (slot >= 0) {
+      const int64_t blk = slot / p.block_size;
+      if (blk < p.num_blocks) row = blk * Hk * p.block_size + (slot - blk * p.block_size);
+      else if (blockIdx.y == 0) set_error(p.err, PKV_DEV_SLOT_RANGE);
+    }
+    s_row[tid] = row;
+  }
+  __syncthreads();
+
+  while (live) {
+    const float2* cs = s_cs + cur.tok * pairs;
+    if (cur.head < H + Hk) {
+      if constexpr (INTER) {
+        auto turn = [&](float (&f)[V], int vec) {
+#pragma unroll
+          for (int j = 0; j < V; j += 2) {
+            const int i = (vec * V + j) >> 1;
+            if (i < pairs) {
+              const float2 c = cs[i];
+              const float xx = f[j], yy = f[j + 1];
+              f[j] = xx * c.x - yy * c.y;
+              f[j + 1] = yy * c.x + xx * c.y;
+            }
+          }
+        };
+        turn(cur.a, cur.va);
+        if (cur.vb >= 0) turn(cur.b, cur.vb);
+      } else if (u < half_vecs) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float2 c = cs[u * V + j];
+          const float xx = cur.a[j], yy = cur.b[j];
+          cur.a[j] = xx * c.x - yy * c.y;
+          cur.b[j] = yy * c.x + xx * c.y;
+        }
+      }
+    }
+    if (cur.head < H) {
+      TI* dst = static_cast<TI*>(p.q_out) + (t0 + cur.tok) * p.q_out_stride + (int64_t)cur.head * D;
+      store_vec<TI, V>(dst + cur.va * V, cur.a);
+      if (cur.vb >= 0) store_vec<TI, V>(dst + cur.vb * V, cur.b);
+    } else if (s_row[cur.tok] >= 0) {
+      const bool key = cur.head < H + Hk;
+      const int h = cur.head - (key ? H : H + Hk);
+      const int64_t at = (s_row[cur.tok] + (int64_t)h * p.block_size) * D;
+      void* pool = key ? p.k_cache : p.v_cache;
+      if constexpr (FP8) {
+        const float sc = (key ? p.k_scale : p.v_scale)[h];
+        unsigned char* dst = static_cast<unsigned char*>(pool) + at;
+        store_codes<V>(dst + cur.va * V, cur.a, sc);
+        if (cur.vb >= 0) store_codes<V>(dst + cur.vb * V, cur.b, sc);
+      } else {
+        TI* dst = static_cast<TI*>(pool) + at;
+        store_vec<TI, V>(dst + cur.va * V, cur.a);
+        if (cur.vb >= 0) store_vec<TI, V>(dst + cur.vb * V, cur.b);
+      }
+    }
+    x += step;
+    live = x < rows;
+    if (live) fetch(x, u, cur);
+  }
+}
+
+template <typename TI, bool FP8>
+int launch_rope(RopeParams& p, cudaStream_t stream) {
+  constexpr int V = 16 / (int)sizeof(TI);
+  const int pairs = p.rot.rotary_dim / 2;
+  const bool inter = p.rot.interleaved != 0;
+  // Halves whose length is not a whole number of 16-byte vectors take one
+  // element at a time.
+  const bool single = !inter && pairs % V != 0;
+  const int vecs = single ? p.dim : p.dim / V;
+  p.units = (vecs + 1) / 2;
+  if (p.units > kRopeThreads) return PKV_ERR_GEOMETRY;
+  p.tokens = (int)std::min<int64_t>(kRopeTokens, std::max<int64_t>(1, p.num_tokens / 1024));
+  const int64_t blocks = (p.num_tokens + p.tokens - 1) / p.tokens;
+  dim3 grid((unsigned)blocks, 1);
+  if (blocks > INT32_MAX) return PKV_ERR_ARG;
+  if (single)
+    rope_write_kernel<TI, FP8, false, 1><<<grid, kRopeThreads, 0, stream>>>(p);
+  else if (inter)
+    rope_write_kernel<TI, FP8, true, V><<<grid, kRopeThreads, 0, stream>>>(p);
+  else
+    rope_write_kernel<TI, FP8, false, V><<<grid, kRopeThreads, 0, stream>>>(p);
+  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace pkv
+
+int pkv_launch_rope_write(const pkv_cache* c, const pkv_rotary* rot, const void* q,
+                          int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const int32_t* positions, const int64_t* slots,
+                          int64_t num_tokens, int num_heads, void* q_out, int64_t q_out_stride,
+                          cudaStream_t stream) {
+  pkv::RopeParams p;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_out = q_out;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out_stride = q_out_stride;
+  p.k_cache = c->k_cache;
+  p.v_cache = c->v_cache;
+  p.k_scale = c->k_scale;
+  p.v_scale = c->v_scale;
+  p.positions = positions;
+  p.slots = slots;
+  p.num_tokens = num_tokens;
+  p.num_blocks = c->num_blocks;
+  p.block_size = c->block_size;
+  p.heads = num_heads;
+  p.kv_heads = c->num_kv_heads;
+  p.dim = c->head_dim;
+  p.err = pkv_error_word();
+  p.rot = *rot;
+  switch (c->dtype) {
+    case PKV_F32: return pkv::launch_rope<float, false>(p, stream);
+    case PKV_F16: return pkv::launch_rope<__half, false>(p, stream);
+    case PKV_BF16: return pkv::launch_rope<__nv_bfloat16, false>(p, stream);
+    case PKV_FP8_E4M3:
+      return c->io_dtype == PKV_F16 ? pkv::launch_rope<__half, true>(p, stream)
+                                    : pkv::launch_rope<__nv_bfloat16, true>(p, stream);
+  }
+  return PKV_ERR_ARG;
+}
+
+extern "C" int paged_rotary_init(pkv_rotary* rotary, int32_t rotary_dim, int32_t num_axes,
+                                 const double* inv_freq, const int32_t* pair_axis,
+                                 int32_t interleaved) {
+  if (!rotary || !inv_freq) return PKV_ERR_NULL;
+  if (rotary_dim < 2 || rotary_dim > 2 * PKV_ROTARY_MAX_PAIRS || rotary_dim % 2 || num_axes < 1 ||
+      num_axes > PKV_ROTARY_MAX_AXES || (num_axes > 1 && !pair_axis))
+    return PKV_ERR_ARG;
+  pkv_rotary r;
+  std::memset(&r, 0, sizeof(r));
+  r.rotary_dim = rotary_dim;
+  r.num_axes = num_axes;
+  r.interleaved = interleaved != 0;
+  // Turns per position = inv_freq / (2 pi), modulo 1, in units of 2^-64: the
+  // product with 1 / (2 pi) as two doubles, its rounding error recovered by
+  // one fused multiply-add, split at 2^-32 so that every step is exact.
+  const double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi)
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double f = std::fabs(inv_freq[i]);
+    const int axis = pair_axis ? pair_axis[i] : 0;
+    if (!std::isfinite(f) || f > 1048576.0 || axis < 0 || axis >= num_axes)
+      return PKV_ERR_ARG;
+    volatile const double hi = f * kHi;  // rounded here: lo is what the rounding left
+    const double lo = std::fma(f, kHi, -hi) + f * kLo;
+    const double whole = std::floor(hi);
+    const double top = std::floor((hi - whole) * 0x1p32);     // < 2^32, exact
+    const double rest = ((hi - whole) * 0x1p32 - top) * 0x1p32;  // [0, 2^32), exact
+    const double low = std::nearbyint(rest + lo * 0x1p64);    // may be negative or >= 2^32
+    const uint64_t step = ((uint64_t)top << 32) + (uint64_t)(int64_t)low;
+    r.step[i] = inv_freq[i] < 0 ? 0 - step : step;
+    r.axis[i] = (uint8_t)axis;
+  }
+  *rotary = r;
+  return PKV_OK;
+}
