@@ -7,12 +7,18 @@
 #include <cstring>
 #include <mutex>
 
-#include "cross.cuh"
+#include "cross_tc.cuh"
 #include "decode_launch.cuh"
 #include "prefill.cuh"
 
 int pkv_launch_kv_write(const pkv_cache* c, const void* k, const void* v, const int64_t* slots,
                         int64_t num_tokens, size_t elem_bytes, cudaStream_t stream);
+int pkv_launch_cross_tc_f16(const pkv::CrossParams&, int, int, bool, const pkv::CrossMaps&,
+                            cudaStream_t);
+int pkv_launch_cross_tc_bf16(const pkv::CrossParams&, int, int, bool, const pkv::CrossMaps&,
+                             cudaStream_t);
+int pkv_launch_cross_tc_fp8(const pkv::CrossParams&, int, int, bool, const pkv::CrossMaps&,
+                            cudaStream_t);
 int pkv_launch_cross(const pkv::CrossParams& p, int dtype, int io_dtype, int num_seqs, int dim,
                      cudaStream_t stream);
 int pkv_launch_rope_write(const pkv_cache* c, const pkv_rotary* rot, const void* q,
@@ -520,28 +526,39 @@ int paged_attention_prefill(const pkv_cache* cache, const void* q, int64_t total
 
 namespace {
 
-// Split of cross attention's states: the longest parts that still give about
-// two thread blocks per SM, in whole 128-position runs.  rows: rows per
-// thread block.
-struct CrossSplit {
+// How cross attention runs: on tensor cores (16-bit pools, FP8 pools of
+// head_dim 128) in blocks of 256 rows, or of 128 rows two to an SM where a
+// sequence has no more than that, else on CUDA cores in blocks of 8 rows; and
+// the split of the states where the blocks would not fill the GPU: whole
+// runs of 128 positions, as few parts as give every SM its blocks.
+struct CrossPlan {
+  bool tc, wide;
   int parts, part;
 };
 
-CrossSplit cross_split(const pkv_cache* c, int num_seqs, int num_heads, int max_queries,
-                       int max_len) {
+CrossPlan cross_plan(const pkv_cache* c, int num_seqs, int num_heads, int max_queries,
+                     int max_len) {
+  CrossPlan pl{};
+  pl.tc = c->dtype == PKV_F16 || c->dtype == PKV_BF16 ||
+          (c->dtype == PKV_FP8_E4M3 && c->head_dim == 128);
+  const int64_t rows = (int64_t)max_queries * (num_heads / c->num_kv_heads);
+  pl.wide = rows > 128;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
     cudaGetLastError();
     sms = 1;
   }
-  const int64_t rows = (int64_t)max_queries * (num_heads / c->num_kv_heads);
-  const int64_t blocks = (int64_t)num_seqs * c->num_kv_heads * ((rows + pkv::kCrossRows - 1) / pkv::kCrossRows);
+  const int64_t per = !pl.tc ? pkv::kCrossRows : pl.wide ? 256 : 128;
+  const int64_t slots = (int64_t)sms * (pl.tc ? (pl.wide ? 1 : 2) : 8);
+  const int64_t blocks = std::max<int64_t>(1, (int64_t)num_seqs * c->num_kv_heads * ((rows + per - 1) / per));
   constexpr int kRun = 128;
-  const int64_t runs = std::max<int64_t>(1, (max_len + kRun - 1) / kRun);
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(runs, 2 * sms / std::max<int64_t>(1, blocks)));
+  const int64_t runs = std::max<int64_t>(1, ((int64_t)max_len + kRun - 1) / kRun);
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(runs, slots / blocks));
   const int64_t part = (runs + want - 1) / want * kRun;
-  return {(int)((runs * kRun + part - 1) / part), (int)part};
+  pl.part = (int)part;
+  pl.parts = (int)((runs * kRun + part - 1) / part);
+  return pl;
 }
 
 // Bytes of the (m, l) pairs and where the partial outputs start.
@@ -571,7 +588,7 @@ size_t paged_attention_cross_workspace_bytes(const pkv_cache* cache, int64_t tot
   if (!cache || !cross_args_ok(cache, total_queries, num_seqs, num_heads, max_queries) ||
       max_enc_len < 0)
     return 0;
-  const CrossSplit sp = cross_split(cache, num_seqs, num_heads, max_queries, max_enc_len);
+  const CrossPlan sp = cross_plan(cache, num_seqs, num_heads, max_queries, max_enc_len);
   return cross_workspace(total_queries, num_heads, cache->head_dim, sp.parts).total;
 }
 
@@ -599,7 +616,7 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
       (reinterpret_cast<uintptr_t>(enc_lens) & 3u) ||
       (reinterpret_cast<uintptr_t>(query_starts) & 3u))
     return PKV_ERR_ALIGN;
-  const CrossSplit sp = cross_split(cache, num_seqs, num_heads, max_queries, max_len);
+  const CrossPlan sp = cross_plan(cache, num_seqs, num_heads, max_queries, max_len);
   const WsLayout ws = cross_workspace(total_queries, num_heads, cache->head_dim, sp.parts);
   if (ws.total > 0) {
     if (!workspace || workspace_bytes < ws.total) return PKV_ERR_WORKSPACE;
@@ -632,7 +649,16 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
   p.k_scale = cache->k_scale;
   p.v_scale = cache->v_scale;
   p.err = err;
-  return pkv_launch_cross(p, cache->dtype, cache->io_dtype, num_seqs, cache->head_dim, stream);
+  if (!sp.tc)
+    return pkv_launch_cross(p, cache->dtype, cache->io_dtype, num_seqs, cache->head_dim, stream);
+  pkv::CrossMaps maps;
+  if (!encode_pool_map(&maps.k, cache, cache->k_cache) ||
+      !encode_pool_map(&maps.v, cache, cache->v_cache))
+    return PKV_ERR_CUDA;
+  if (cache->dtype == PKV_FP8_E4M3)
+    return pkv_launch_cross_tc_fp8(p, cache->io_dtype, num_seqs, sp.wide, maps, stream);
+  return (cache->dtype == PKV_F16 ? pkv_launch_cross_tc_f16 : pkv_launch_cross_tc_bf16)(
+      p, num_seqs, cache->head_dim, sp.wide, maps, stream);
 }
 
 int paged_block_copy(const pkv_cache* cache, const int64_t* src_dst_pairs, int64_t num_pairs,

@@ -15,23 +15,18 @@ int launch(const pkv::CrossParams& p, int num_seqs, cudaStream_t stream) {
   return pkv::launch_cross_merge<T, D>(p, num_seqs, stream);
 }
 
-template <typename T, typename TC>
-int launch_d(const pkv::CrossParams& p, int num_seqs, int dim, cudaStream_t stream) {
-  return dim == 64 ? launch<T, TC, 64>(p, num_seqs, stream) : launch<T, TC, 128>(p, num_seqs, stream);
-}
-
 }  // namespace
 
-// head_dim 64 or 128.
+// fp32 pools (head_dim 64 or 128) and FP8 pools of head_dim 64.
 int pkv_launch_cross(const pkv::CrossParams& p, int dtype, int io_dtype, int num_seqs, int dim,
                      cudaStream_t stream) {
   switch (dtype) {
-    case PKV_F32: return launch_d<float, float>(p, num_seqs, dim, stream);
-    case PKV_F16: return launch_d<__half, __half>(p, num_seqs, dim, stream);
-    case PKV_BF16: return launch_d<__nv_bfloat16, __nv_bfloat16>(p, num_seqs, dim, stream);
-    case PKV_FP8_E4M3:
-      return io_dtype == PKV_F16 ? launch_d<__half, __nv_fp8_e4m3>(p, num_seqs, dim, stream)
-                                 : launch_d<__nv_bfloat16, __nv_fp8_e4m3>(p, num_seqs, dim, stream);
+    case PKV_F32:
+      return dim == 64 ? launch<float, float, 64>(p, num_seqs, stream)
+                       : launch<float, float, 128>(p, num_seqs, stream);
+    case PKV_FP8_E4M3:  // (head_dim 64)
+      return io_dtype == PKV_F16 ? launch<__half, __nv_fp8_e4m3, 64>(p, num_seqs, stream)
+                                 : launch<__nv_bfloat16, __nv_fp8_e4m3, 64>(p, num_seqs, stream);
   }
   return PKV_ERR_ARG;
 }
