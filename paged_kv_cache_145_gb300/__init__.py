@@ -50,32 +50,23 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-class _on:
-    """Enters a tensor's device, and the stream that the call runs on, so that
-    what the call allocates belongs to that stream; gives the stream's
-    handle."""
+# The current stream's handle on a device (the raw accessor where torch has
+# it: a Stream object costs ten times as much to make).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    __slots__ = ("device", "stream", "inner")
 
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
-        self.device, self.stream, self.inner = device, stream, None
-
-    def __enter__(self):
-        if self.stream is not None:
-            self.inner = torch.cuda.stream(self.stream)  # enters the stream's device too
-            self.inner.__enter__()
-            return self.stream.cuda_stream
-        if torch.cuda.current_device() != self.device.index:
-            self.inner = torch.cuda.device(self.device)
-            self.inner.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.inner is not None:
-            self.inner.__exit__(*exc)
-        return False
+def _elsewhere(device, stream):
+    """The context to enter before a call whose tensors are on ``device``, so
+    that it launches there and its allocations belong to ``stream``; None
+    where the current device and stream are the ones."""
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return None
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+    return torch.cuda.stream(stream)
 
 
 def _need(t, name, dtype=None, device=None):
@@ -193,17 +184,17 @@ class RotaryAxes:
 
 
 def _need_rows(t, name, heads, dim, dtype, device):
-    """[T, heads, dim] whose heads are contiguous; tokens may be strided."""
+    """The token stride of ``t``: [T, heads, dim] whose heads are contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dtype != dtype or t.device != device:
         raise ValueError("%s must be %s on %s, got %s on %s" % (name, dtype, device, t.dtype, t.device))
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+    if t.dim() != 3 or t.shape[1:] != (heads, dim):
         raise ValueError("%s must be [num_tokens, %d, %d]" % (name, heads, dim))
-    s = t.stride()
-    if (dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim):
+    row, head, one = t.stride()
+    if one != 1 or (head != dim and heads > 1):
         raise ValueError("%s must have contiguous heads" % name)
-    return s[0]
+    return row
 
 
 def paged_rope_kv_write(cache, rotary, q, k, v, positions, slot_mapping, q_out=None, stream=None):
@@ -215,13 +206,13 @@ def paged_rope_kv_write(cache, rotary, q, k, v, positions, slot_mapping, q_out=N
     by a multiple of 16 bytes).  ``q_out`` may be ``q``; it is allocated when
     not given.  Returns ``q_out``.
     """
-    dev = cache.device
+    dev, io, dim = cache.device, cache.io_dtype, cache.head_dim
     if q.dim() != 3:
         raise ValueError("q must be [num_tokens, num_heads, head_dim]")
     n, heads = q.shape[0], q.shape[1]
-    qs = _need_rows(q, "q", heads, cache.head_dim, cache.io_dtype, dev)
-    ks = _need_rows(k, "k", cache.num_kv_heads, cache.head_dim, cache.io_dtype, dev)
-    vs = _need_rows(v, "v", cache.num_kv_heads, cache.head_dim, cache.io_dtype, dev)
+    qs = _need_rows(q, "q", heads, dim, io, dev)
+    ks = _need_rows(k, "k", cache.num_kv_heads, dim, io, dev)
+    vs = _need_rows(v, "v", cache.num_kv_heads, dim, io, dev)
     _need(positions, "positions", torch.int32, dev)
     _need(slot_mapping, "slot_mapping", torch.int64, dev)
     if k.shape[0] != n or v.shape[0] != n or slot_mapping.shape != (n,):
@@ -229,16 +220,23 @@ def paged_rope_kv_write(cache, rotary, q, k, v, positions, slot_mapping, q_out=N
     if positions.shape != (rotary.num_axes, n) and not (rotary.num_axes == 1 and
                                                         positions.shape == (n,)):
         raise ValueError("positions must be [num_axes, num_tokens]")
-    with _on(dev, stream) as st:
-        if q_out is None:
-            q_out = torch.empty((n, heads, cache.head_dim), dtype=cache.io_dtype, device=dev)
-        os = _need_rows(q_out, "q_out", heads, cache.head_dim, cache.io_dtype, dev)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return paged_rope_kv_write(cache, rotary, q, k, v, positions, slot_mapping, q_out)
+    if q_out is None:
+        q_out = torch.empty((n, heads, dim), dtype=io, device=dev)
+        os = heads * dim
+    else:
+        os = _need_rows(q_out, "q_out", heads, dim, io, dev)
         if q_out.shape[0] != n:
             raise ValueError("q_out must have q's shape")
-        _lib.check(_lib.lib().paged_rope_kv_write(
-            cache.ref, rotary.ref, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-            positions.data_ptr(), slot_mapping.data_ptr(), n, heads, q_out.data_ptr(), os, st),
-            "paged_rope_kv_write")
+    rc = _lib.lib().paged_rope_kv_write(
+        cache.ref, rotary.ref, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        positions.data_ptr(), slot_mapping.data_ptr(), n, heads, q_out.data_ptr(), os,
+        _raw_stream(dev.index))
+    if rc:
+        _lib.check(rc, "paged_rope_kv_write")
     return q_out
 
 
@@ -398,28 +396,34 @@ def paged_attention_cross(cache, q, query_starts, block_tables, enc_lens, scale,
             block_tables.dim() != 2 or block_tables.shape[0] != num_seqs:
         raise ValueError("enc_lens must be [S], query_starts [S + 1] and block_tables [S, max_blocks]")
     max_queries, max_enc_len = int(max_queries), int(max_enc_len)
-    lib = _lib.lib()
-    with _on(dev, stream) as st:
-        if out is None:
-            out = torch.empty_like(q)
-        else:
-            _need(out, "out", cache.io_dtype, dev)
-            if out.shape != q.shape:
-                raise ValueError("out must have q's shape")
-        if workspace is None:
-            bound = max_enc_len if max_enc_len else block_tables.shape[1] * cache.block_size
-            need = lib.paged_attention_cross_workspace_bytes(cache.ref, q.shape[0], num_seqs,
-                                                             q.shape[1], max_queries, bound)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        else:
-            _need(workspace, "workspace", None, dev)
-        ws, ws_len = (None, 0) if workspace is None else (
-            workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        _lib.check(lib.paged_attention_cross(
-            cache.ref, q.data_ptr(), q.shape[0], query_starts.data_ptr(), num_seqs, max_queries,
-            block_tables.data_ptr(), block_tables.shape[1], enc_lens.data_ptr(), max_enc_len,
-            q.shape[1], float(scale), out.data_ptr(), ws, ws_len, st), "paged_attention_cross")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return paged_attention_cross(cache, q, query_starts, block_tables, enc_lens, scale,
+                                         max_queries, max_enc_len, out, workspace)
+    lib, total, heads, width = _lib.lib(), q.shape[0], q.shape[1], block_tables.shape[1]
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", cache.io_dtype, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if workspace is None:
+        need = lib.paged_attention_cross_workspace_bytes(
+            cache.ref, total, num_seqs, heads, max_queries, max_enc_len or width * cache.block_size)
+        ws, ws_len = None, need
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws = workspace.data_ptr()
+    else:
+        _need(workspace, "workspace", None, dev)
+        ws, ws_len = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    rc = lib.paged_attention_cross(
+        cache.ref, q.data_ptr(), total, query_starts.data_ptr(), num_seqs, max_queries,
+        block_tables.data_ptr(), width, enc_lens.data_ptr(), max_enc_len, heads, scale,
+        out.data_ptr(), ws, ws_len, _raw_stream(dev.index))
+    if rc:
+        _lib.check(rc, "paged_attention_cross")
     return out
 
 
@@ -458,13 +462,13 @@ def paged_block_swap(cache, host_k, host_v, pairs, direction, stream=None):
                "paged_block_swap")
 
 
-def _output(t, name, shape, dtype, device):
+def _output(t, name, size, dtype, device):
     """``t`` checked against what the call writes, or a new tensor."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(size, dtype=dtype, device=device)
     _need(t, name, dtype, device)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    if t.shape != (size,):
+        raise ValueError("%s must be [%d], got %s" % (name, size, list(t.shape)))
     return t
 
 
@@ -501,18 +505,25 @@ def paged_build_tables(free_list, free_state, old_lens, new_lens, block_tables, 
     max_tokens = int(max_tokens)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
-    with _on(dev, stream) as st:
-        seq_lens = _output(seq_lens, "seq_lens", (n,), torch.int32, dev)
-        free_state_out = _output(free_state_out, "free_state_out", (2,), torch.int64, dev)
-        query_starts = _output(query_starts, "query_starts", (n + 1,), torch.int32, dev)
-        slot_mapping = _output(slot_mapping, "slot_mapping", (max_tokens,), torch.int64, dev)
-        positions = _output(positions, "positions", (max_tokens,), torch.int32, dev)
-        _lib.check(_lib.lib().paged_build_tables(
-            free_list.numel(), int(block_size), free_list.data_ptr(), free_state.data_ptr(),
-            old_lens.data_ptr(), new_lens.data_ptr(), n, block_tables.data_ptr(),
-            block_tables.shape[1], seq_lens.data_ptr(), free_state_out.data_ptr(),
-            query_starts.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), max_tokens,
-            st), "paged_build_tables")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return paged_build_tables(free_list, free_state, old_lens, new_lens, block_tables,
+                                      block_size, max_tokens, seq_lens, free_state_out, query_starts,
+                                      slot_mapping, positions)
+    seq_lens = _output(seq_lens, "seq_lens", n, torch.int32, dev)
+    free_state_out = _output(free_state_out, "free_state_out", 2, torch.int64, dev)
+    query_starts = _output(query_starts, "query_starts", n + 1, torch.int32, dev)
+    slot_mapping = _output(slot_mapping, "slot_mapping", max_tokens, torch.int64, dev)
+    positions = _output(positions, "positions", max_tokens, torch.int32, dev)
+    rc = _lib.lib().paged_build_tables(
+        free_list.numel(), block_size, free_list.data_ptr(), free_state.data_ptr(),
+        old_lens.data_ptr(), new_lens.data_ptr(), n, block_tables.data_ptr(),
+        block_tables.shape[1], seq_lens.data_ptr(), free_state_out.data_ptr(),
+        query_starts.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), max_tokens,
+        _raw_stream(dev.index))
+    if rc:
+        _lib.check(rc, "paged_build_tables")
     return seq_lens, free_state_out, query_starts, slot_mapping, positions
 
 

@@ -13,11 +13,11 @@
 
 int pkv_launch_kv_write(const pkv_cache* c, const void* k, const void* v, const int64_t* slots,
                         int64_t num_tokens, size_t elem_bytes, cudaStream_t stream);
-int pkv_launch_cross_tc_f16(const pkv::CrossParams&, int, int, bool, const pkv::CrossMaps&,
+int pkv_launch_cross_tc_f16(const pkv::CrossParams&, int, int, pkv::CrossRows, const pkv::CrossMaps&,
                             cudaStream_t);
-int pkv_launch_cross_tc_bf16(const pkv::CrossParams&, int, int, bool, const pkv::CrossMaps&,
+int pkv_launch_cross_tc_bf16(const pkv::CrossParams&, int, int, pkv::CrossRows, const pkv::CrossMaps&,
                              cudaStream_t);
-int pkv_launch_cross_tc_fp8(const pkv::CrossParams&, int, int, bool, const pkv::CrossMaps&,
+int pkv_launch_cross_tc_fp8(const pkv::CrossParams&, int, int, pkv::CrossRows, const pkv::CrossMaps&,
                             cudaStream_t);
 int pkv_launch_cross(const pkv::CrossParams& p, int dtype, int io_dtype, int num_seqs, int dim,
                      cudaStream_t stream);
@@ -527,12 +527,13 @@ int paged_attention_prefill(const pkv_cache* cache, const void* q, int64_t total
 namespace {
 
 // How cross attention runs: on tensor cores (16-bit pools, FP8 pools of
-// head_dim 128) in blocks of 256 rows, or of 128 rows two to an SM where a
-// sequence has no more than that, else on CUDA cores in blocks of 8 rows; and
-// the split of the states where the blocks would not fill the GPU: whole
+// head_dim 128) in blocks of 256 rows, or, where no sequence has more, of 128
+// or 32 rows two to an SM; else on CUDA cores in blocks of 8 rows; and the
+// split of the states where the blocks would not fill the GPU: whole
 // runs of 128 positions, as few parts as give every SM its blocks.
 struct CrossPlan {
-  bool tc, wide;
+  bool tc;
+  pkv::CrossRows rows;
   int parts, part;
 };
 
@@ -542,19 +543,23 @@ CrossPlan cross_plan(const pkv_cache* c, int num_seqs, int num_heads, int max_qu
   pl.tc = c->dtype == PKV_F16 || c->dtype == PKV_BF16 ||
           (c->dtype == PKV_FP8_E4M3 && c->head_dim == 128);
   const int64_t rows = (int64_t)max_queries * (num_heads / c->num_kv_heads);
-  pl.wide = rows > 128;
+  pl.rows = rows > 128  ? pkv::CrossRows::k256
+            : rows > 32 ? pkv::CrossRows::k128
+                        : pkv::CrossRows::k32;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
     cudaGetLastError();
     sms = 1;
   }
-  const int64_t per = !pl.tc ? pkv::kCrossRows : pl.wide ? 256 : 128;
-  const int64_t slots = (int64_t)sms * (pl.tc ? (pl.wide ? 1 : 2) : 8);
+  const bool wide = pl.rows == pkv::CrossRows::k256;
+  const int64_t per = !pl.tc ? pkv::kCrossRows : wide ? 256 : rows > 32 ? 128 : 32;
+  const int64_t slots = (int64_t)sms * (pl.tc ? (wide ? 1 : 2) : 8);
   const int64_t blocks = std::max<int64_t>(1, (int64_t)num_seqs * c->num_kv_heads * ((rows + per - 1) / per));
+  static const int mul = std::getenv("XMUL") ? std::atoi(std::getenv("XMUL")) : 1;  // EXPERIMENT
   constexpr int kRun = 128;
   const int64_t runs = std::max<int64_t>(1, ((int64_t)max_len + kRun - 1) / kRun);
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(runs, slots / blocks));
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(runs, slots * mul / blocks));
   const int64_t part = (runs + want - 1) / want * kRun;
   pl.part = (int)part;
   pl.parts = (int)((runs * kRun + part - 1) / part);
@@ -656,9 +661,9 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
       !encode_pool_map(&maps.v, cache, cache->v_cache))
     return PKV_ERR_CUDA;
   if (cache->dtype == PKV_FP8_E4M3)
-    return pkv_launch_cross_tc_fp8(p, cache->io_dtype, num_seqs, sp.wide, maps, stream);
+    return pkv_launch_cross_tc_fp8(p, cache->io_dtype, num_seqs, sp.rows, maps, stream);
   return (cache->dtype == PKV_F16 ? pkv_launch_cross_tc_f16 : pkv_launch_cross_tc_bf16)(
-      p, num_seqs, cache->head_dim, sp.wide, maps, stream);
+      p, num_seqs, cache->head_dim, sp.rows, maps, stream);
 }
 
 int paged_block_copy(const pkv_cache* cache, const int64_t* src_dst_pairs, int64_t num_pairs,

@@ -21,6 +21,8 @@
 // a few microseconds of one SM's store rate at most; the chain lengths ->
 // prefix sums -> ring entries -> stores is two dependent loads and one
 // barrier.
+#include <algorithm>
+
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -46,7 +48,8 @@ struct BuildParams {
   int max_blocks;
   int block_size;
   int share;                 // rows per thread block
-  bool fill;                 // this kernel writes the slot map too
+  bool fill;                 // build_tables_kernel writes the slot map too
+  bool vectors;              // slots and positions are 16-byte aligned
   unsigned* err;
 };
 
@@ -297,15 +300,74 @@ __global__ void __launch_bounds__(kBuildThreads) build_tables_kernel(const Build
   }
 }
 
+// The slot map and positions of a wide step, from the tables, lengths and
+// starts that build_tables_kernel left (whatever it decided): a thread takes
+// kFillTokens consecutive tokens, so that one search and mostly one table
+// entry serve them all and the stores are whole 16-byte vectors.
+constexpr int kFillThreads = 256;
+constexpr int kFillTokens = 4;
+constexpr int kFillRows = 8192;  // starts held in shared memory, at most
+
+__global__ void __launch_bounds__(kFillThreads) fill_slots_kernel(const BuildParams p) {
+  extern __shared__ int rows[];
+  const int S = p.num_seqs, b = p.block_size;
+  const int total = p.starts[S];
+  const int64_t t0 = ((int64_t)blockIdx.x * kFillThreads + threadIdx.x) * kFillTokens;
+  const int* starts = p.starts;
+  if ((int64_t)blockIdx.x * kFillThreads * kFillTokens < total && S <= kFillRows) {
+    for (int r = threadIdx.x; r < S; r += kFillThreads) rows[r] = p.starts[r];
+    starts = rows;
+    __syncthreads();
+  }
+  if (t0 >= p.max_tokens) return;
+  int64_t slot[kFillTokens];
+  int pos[kFillTokens];
+  int r = t0 < total ? find_row(starts, S, (int)t0) : 0, blk = -1, entry = 0;
+#pragma unroll
+  for (int i = 0; i < kFillTokens; ++i) {
+    slot[i] = -1;
+    pos[i] = 0;
+    const int64_t t = t0 + i;
+    if (t >= total) continue;
+    // the row of token t: the last with starts[r] <= t
+    while (r + 1 < S && starts[r + 1] <= t) {
+      ++r;
+      blk = -1;
+    }
+    const int next = r + 1 < S ? starts[r + 1] : total;
+    pos[i] = p.seq_lens[r] - next + (int)t;  // the row's last token is its last position
+    if (blk != pos[i] / b) {
+      blk = pos[i] / b;
+      entry = p.tables[(int64_t)r * p.max_blocks + blk];
+    }
+    slot[i] = (int64_t)entry * b + (pos[i] - blk * b);
+  }
+  if (p.vectors && t0 + kFillTokens <= p.max_tokens) {
+    reinterpret_cast<longlong2*>(p.slots + t0)[0] = make_longlong2(slot[0], slot[1]);
+    reinterpret_cast<longlong2*>(p.slots + t0)[1] = make_longlong2(slot[2], slot[3]);
+    *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kFillTokens; ++i)
+      if (t0 + i < p.max_tokens) {
+        p.slots[t0 + i] = slot[i];
+        p.positions[t0 + i] = pos[i];
+      }
+  }
+}
+
 }  // namespace pkv
 
 int pkv_launch_build_tables(pkv::BuildParams p, cudaStream_t stream) {
   using namespace pkv;
   p.err = pkv_error_word();
   if (!p.err) return PKV_ERR_CUDA;
-  p.fill = true;
-  const bool small = p.num_seqs <= kBuildThreads && p.max_tokens <= 2 * kBuildThreads;
-  const int cluster = small ? 1 : kBuildCluster;
+  // One block serves a step of few rows; more rows are shared by a cluster.
+  // Few tokens are written along; a wider slot map by a second kernel over the
+  // whole GPU.
+  const int cluster = p.num_seqs <= kBuildThreads ? 1 : kBuildCluster;
+  p.fill = p.max_tokens <= 2 * kBuildThreads;
+  p.vectors = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15u) == 0;
   p.share = (p.num_seqs + cluster - 1) / cluster;
   const size_t smem = (size_t)p.share * 5 * sizeof(int);
   if (smem > 48 * 1024 &&
@@ -323,7 +385,13 @@ int pkv_launch_build_tables(pkv::BuildParams p, cudaStream_t stream) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, build_tables_kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, build_tables_kernel, p) != cudaSuccess) return PKV_ERR_CUDA;
+  if (!p.fill) {
+    const int64_t per = kFillThreads * kFillTokens;
+    fill_slots_kernel<<<(unsigned)((p.max_tokens + per - 1) / per), kFillThreads,
+                        std::min(p.num_seqs, kFillRows) * sizeof(int), stream>>>(p);
+  }
+  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 extern "C" int paged_build_tables(int64_t num_blocks, int32_t block_size, int32_t* free_list,

@@ -31,12 +31,18 @@
 
 namespace pkv {
 
-// QT 2: 256 rows, one block per SM; QT 1: 128 rows, two blocks per SM.
-template <typename T, int D, int QT, bool KV8>
+// QT 2: 256 rows, one block per SM; QT 1: 128 rows, two blocks per SM.  SPLIT
+// (QT 1): 32 rows, each on four tensor-memory lanes, one per softmax warp,
+// which each take a quarter of every tile's keys with a maximum, a sum and an
+// O of their own, joined at the end: with few rows the softmax of one warp
+// would set the pace (64 sequences of 200-1500 states, 16 heads of 64:
+// 71 us without).
+template <typename T, int D, int QT, bool KV8, bool SPLIT>
 struct CrossTcCfg {
   static constexpr int kKeys = QT == 2 && !KV8 ? 128 : 64;
   static constexpr int kBufs = QT == 2 && !KV8 ? 1 : 2;     // S buffers (NS)
-  static constexpr int kRows = QT * 128;
+  static constexpr int kRows = SPLIT ? 32 : QT * 128;
+  static constexpr int kLaneKeys = SPLIT ? kKeys / 4 : kKeys;  // keys of a lane
   static constexpr int kHalves = D / 64;                    // 128-byte column blocks
   static constexpr int kHalfBytes = kKeys * 128;            // of a K or V tile
   static constexpr int kTileBytes = kHalves * kHalfBytes;
@@ -56,9 +62,14 @@ struct CrossTcCfg {
   static constexpr int kRingOff = QT * kQBytes;
   static constexpr int kRawOff = kRingOff + kSlots * kTileBytes;
   static constexpr int kBarOff = kRawOff + kRawSlots * kRawBytes;
-  static constexpr int kNumBars = 2 * kSlots + 2 * kRawSlots + QT * (2 * kBufs + 2) + 1;
+  static constexpr int kNumBars = 2 * kSlots + 2 * kRawSlots + QT * (2 * kBufs + 2) + 2;
   static constexpr int kTmemOff = kBarOff + kNumBars * 8;
+  static constexpr int kFlagOff = kTmemOff + 4;
   static constexpr int kSmemBytes = kTmemOff + 16;
+  // SPLIT, at the end: the lanes' (m, l) in Q's memory, their O in the ring's,
+  // rows padded by 16 bytes
+  static constexpr int kORow = D + 4;
+  static_assert(!SPLIT || (QT == 1 && 4 * 32 * kORow * 4 <= kBarOff - kRingOff), "O in the ring");
   static constexpr uint32_t kTileCols = 256;
   static constexpr uint32_t kTmemCols = QT * kTileCols;
   static constexpr uint32_t kOCol = kBufs * kKeys;
@@ -81,19 +92,33 @@ struct CrossMaps {
   CUtensorMap k, v;
 };
 
+// 16 consecutive 32-bit columns of this thread's lane, waited for.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void tmem_ld_row(uint32_t addr, uint32_t (&r)[N]) {
   if constexpr (N == 128) tmem_ld128(addr, r);
-  else tmem_ld64(addr, r);
+  else if constexpr (N == 64) tmem_ld64(addr, r);
+  else tmem_ld16(addr, r);
 }
 
-template <typename T, int D, int QT, bool KV8>
-__global__ void __launch_bounds__(CrossTcCfg<T, D, QT, KV8>::kThreads, QT == 2 ? 1 : 2)
+template <typename T, int D, int QT, bool KV8, bool SPLIT>
+__global__ void __launch_bounds__(CrossTcCfg<T, D, QT, KV8, SPLIT>::kThreads, QT == 2 ? 1 : 2)
 cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ CUtensorMap tmk,
                 const __grid_constant__ CUtensorMap tmv) {
-  using Cfg = CrossTcCfg<T, D, QT, KV8>;
+  using Cfg = CrossTcCfg<T, D, QT, KV8, SPLIT>;
   using Op = typename Cfg::Op;
   constexpr int KT = Cfg::kKeys, NS = Cfg::kBufs, SLOTS = Cfg::kSlots, RAW = Cfg::kRawSlots;
+  constexpr int LK = Cfg::kLaneKeys;
   extern __shared__ __align__(1024) unsigned char cross_smem[];
   unsigned char* const smem = cross_smem;
   const uint32_t sbase = smem_addr(smem);
@@ -125,29 +150,15 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
     return ((int64_t)(c.q0 + x / G) * H + kvh * G + x % G) * D;
   };
   const int nr = min(Cfg::kRows, rows - r0);
-  const int32_t* trow = p.tables + (int64_t)s * p.max_blocks;
-  int bad = 0;
-  const int nblk = c.L > 0 ? (c.L - 1) / b + 1 : 0;
-  for (int i = tid; i < nblk; i += Cfg::kThreads) {
-    const int e = trow[i];
-    bad |= e < 0 || (int64_t)e >= p.num_blocks;
-  }
-  bad = __syncthreads_or(bad);
-  const int lo = part * p.part, hi = min(c.L, lo + p.part);
-  if (bad || c.L == 0) {  // zero rows, or empty parts of them
-    if (bad && tid == 0) set_error(p.err, PKV_DEV_TABLE_RANGE);
-    for (int e = tid; e < nr * D; e += Cfg::kThreads) {
-      const int64_t at = row_at(e / D);
-      if (c.parts == 1) out[at + e % D] = Elem<T>::from_f(0.f);
-      else p.ws_o[(at / D * p.parts + part) * D + e % D] = 0.f;
-    }
-    if (c.parts > 1)
-      for (int r = tid; r < nr; r += Cfg::kThreads)
-        p.ws_ml[row_at(r) / D * p.parts + part] = make_float2(-INFINITY, 0.f);
+  if (c.L == 0) {
+    for (int e = tid; e < nr * D; e += Cfg::kThreads)
+      out[row_at(e / D) + e % D] = Elem<T>::from_f(0.f);
     return;
   }
+  const int32_t* trow = p.tables + (int64_t)s * p.max_blocks;
+  const int lo = part * p.part, hi = min(c.L, lo + p.part);
   const int n_tiles = (hi - lo + KT - 1) / KT;
-  const int row_n = nr > 128 ? 2 : 1;  // row tiles with rows
+  const int row_n = !SPLIT && nr > 128 ? 2 : 1;  // row tiles with rows
 
   // ---- barriers, tensor memory, Q ---------------------------------------------
   const uint32_t bar0 = sbase + Cfg::kBarOff;
@@ -162,8 +173,11 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
   // the last one
   auto o_done = [&](int t) { return bar0 + 8u * (B1 + 2 * QT * NS + t); };
   auto o_last = [&](int t) { return bar0 + 8u * (B1 + 2 * QT * NS + QT + t); };
-  const uint32_t drain = bar0 + 8u * (B1 + 2 * QT * NS + 2 * QT);
-  auto tile_warps = [&](int t) { return min(4, max(0, (nr - t * 128 + 31) / 32)); };
+  const uint32_t q_full = bar0 + 8u * (B1 + 2 * QT * NS + 2 * QT);
+  const uint32_t drain = q_full + 8u;
+  auto tile_warps = [&](int t) {  // softmax warps with rows of row tile t
+    return SPLIT ? 4 : min(4, max(0, (nr - t * 128 + 31) / 32));
+  };
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(full(i), KV8 ? Cfg::kConvThreads : 1);
@@ -181,20 +195,30 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       mbar_init(o_done(t), 1);
       mbar_init(o_last(t), 1);
     }
+    mbar_init(q_full, (tile_warps(0) + (QT > 1 ? tile_warps(QT - 1) : 0)) * 32);
     mbar_init(drain, 1);
     fence_mbar_init();
+    *reinterpret_cast<int*>(smem + Cfg::kFlagOff) = 0;
   }
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + Cfg::kTmemOff);
+  volatile int* bad_flag = reinterpret_cast<volatile int*>(smem + Cfg::kFlagOff);
   if (warp == Cfg::kMmaWarp) {
     tmem_alloc(smem_addr(slot), Cfg::kTmemCols);
     tmem_relinquish();
   }
-  // Softmax thread: row rr of row tile t.  It brings its Q row into the
-  // 128-byte-swizzled operand layout; the sign of the scale goes into Q
-  // (exact), so that the largest score has the largest product.
-  const int t = warp >> 2, rr = (warp & 3) * 32 + lane, r = t * 128 + rr;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  bool failed = false;
+  // Softmax thread: lane rr of row tile t, row r of the block.  It brings its
+  // Q row into the 128-byte-swizzled operand layout while the first tiles are
+  // on their way; the sign of the scale goes into Q (exact), so that the
+  // largest score has the largest product.
+  const int t = warp >> 2, rr = (warp & 3) * 32 + lane, r = SPLIT ? lane : t * 128 + rr;
+  const bool softmax = warp < Cfg::kSoftmaxWarps && (warp & 3) < tile_warps(t);
   float qscale = fabsf(p.qscale);
-  if (warp < Cfg::kSoftmaxWarps && (warp & 3) < tile_warps(t)) {
+  if (softmax) {
     unsigned char* qt = smem + t * Cfg::kQBytes;
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
                                                       row_at(min(r, nr - 1)));
@@ -242,12 +266,16 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
                                 (((i & 7) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     fence_proxy_async_smem();
+    mbar_arrive(q_full);
+    // Every block checks the whole table row, so that all parts agree.  A bad
+    // entry's pages are read as zeros and the rows are zeroed at the end.
+    const int nblk = (c.L - 1) / b + 1;
+    for (int i = tid; i < nblk; i += 32 * tile_warps(0)) {
+      if (tid >= 32 * tile_warps(0)) break;  // (the second row tile leaves it to the first)
+      const int e = trow[i];
+      if (e < 0 || (int64_t)e >= p.num_blocks) *bad_flag = 1;
+    }
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *slot;
-  bool failed = false;
   // Place of K and V tiles in the order of use: the first NS K tiles, then
   // V(j) and K(j + NS) in turn, then the V tiles that are left.
   const int pre = min(NS, n_tiles);
@@ -259,6 +287,18 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
     const uint64_t policy = row_tiles > 1 ? policy_evict_last() : policy_evict_first();
     const int rb = b < 16 ? b : 16;          // rows per box
     const int boxes = KT / rb;
+    // Table entries, a warp's worth of boxes at a time and one such group
+    // ahead, so that no copy waits for its own table load: lane x of group g
+    // holds the block of box x % boxes of tile g * per + x / boxes.  Values run
+    // at most two tiles behind keys, so the group before is kept for them.
+    const int per = 32 / boxes, shift = 31 - __clz(b);
+    const int oob = (int)p.num_blocks;  // reads as zeros (as do too large entries)
+    auto group = [&](int g) {
+      const int pos = lo + (g * 32 + lane) * rb;
+      const int e = pos < hi ? trow[pos >> shift] : oob;
+      return e < 0 ? oob : e;
+    };
+    int at = 0, before = oob, now = group(0), next = group(1);
     constexpr int N = KV8 ? RAW : SLOTS;
     constexpr int BYTES = KV8 ? Cfg::kRawBytes : Cfg::kTileBytes;
     const uint32_t ring = sbase + (KV8 ? Cfg::kRawOff : Cfg::kRingOff);
@@ -280,14 +320,15 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       }
       if (lane == 0) mbar_arrive_expect_tx(fb, BYTES);
       __syncwarp();
+      const int g = j / per;
+      if (g > at) {  // (keys lead)
+        before = now;
+        now = next;
+        next = group(++at + 1);
+      }
+      const int pb = __shfl_sync(kFullMask, g == at ? now : before, (j % per) * boxes + lane);
       if (lane < boxes) {
-        // boxes wholly past the states read an out-of-range block: zeros
-        const int pos = lo + j * KT + lane * rb;
-        int pb = (int)p.num_blocks, row = 0;
-        if (pos < hi) {
-          pb = trow[pos / b];
-          row = pos % b;
-        }
+        const int row = (lo + j * KT + lane * rb) & (b - 1);
         const uint32_t dst = ring + sl * BYTES + lane * rb * 128;
         const CUtensorMap* map = key ? &tmk : &tmv;
         if constexpr (KV8) {
@@ -324,7 +365,7 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
                   Cfg::kIdescS, kk > 0 ? 1u : 0u);
       tc_commit(s_full(tt, j % NS));
     };
-    bool ok = true;
+    bool ok = wait(q_full, 0);
     auto all_s = [&](int j) {  // S(j) of every row tile, outside the main loop
       const int i = seq_k(j);
       ok = ok && wait(full(i % SLOTS), i / SLOTS);
@@ -427,7 +468,7 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
         mbar_arrive(raw_empty(rs));
       }
     }
-  } else if (warp < Cfg::kSoftmaxWarps && (warp & 3) < tile_warps(t)) {
+  } else if (softmax) {
     // ---- softmax, row rr of row tile t ------------------------------------------
     const uint32_t base = tmem + t * Cfg::kTileCols + ((uint32_t)((warp & 3) * 32) << 16);
     float m = -INFINITY, l = 0.f;
@@ -440,17 +481,17 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       }
       tc_fence_after();
       const uint32_t sp = base + (j % NS) * KT;
-      uint32_t w[KT];
-      tmem_ld_row<KT>(sp, w);
-      const int valid = hi - lo - j * KT;
-      if (valid < KT) {
+      uint32_t w[LK];
+      tmem_ld_row<LK>(sp + (SPLIT ? warp * LK : 0), w);
+      const int valid = hi - lo - j * KT - (SPLIT ? warp * LK : 0);
+      if (valid < LK) {
 #pragma unroll
-        for (int k = 0; k < KT; ++k)
+        for (int k = 0; k < LK; ++k)
           if (k >= valid) w[k] = __float_as_uint(-INFINITY);
       }
       float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int k = 0; k < KT; k += 8)
+      for (int k = 0; k < LK; k += 8)
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           mq[u] = max3(mq[u], __uint_as_float(w[k + 2 * u]), __uint_as_float(w[k + 2 * u + 1]));
@@ -468,14 +509,16 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
           m = mx;
         }
       }
+      // A quarter whose keys so far all lie past the states has m = -inf.
+      const float ref = SPLIT && m == -INFINITY ? 0.f : m;
       // 2^(s * scale - m + bias) in pairs, its sum, and P over S's columns
       const float2 qs2 = make_float2(qscale, qscale);
-      const float2 nm2 = make_float2(Cfg::kBias - m, Cfg::kBias - m);
+      const float2 nm2 = make_float2(Cfg::kBias - ref, Cfg::kBias - ref);
       float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                         make_float2(0.f, 0.f)};
-      uint32_t pk[KT / 2];
+      uint32_t pk[LK / 2];
 #pragma unroll
-      for (int k = 0; k < KT; k += 2) {
+      for (int k = 0; k < LK; k += 2) {
         const float2 a = __ffma2_rn(make_float2(__uint_as_float(w[k]), __uint_as_float(w[k + 1])),
                                     qs2, nm2);
         const float2 e = make_float2(ex2(a.x), ex2(a.y));
@@ -485,8 +528,16 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       const float2 s01 = __fadd2_rn(sum2[0], sum2[1]), s23 = __fadd2_rn(sum2[2], sum2[3]);
       const float2 sx = __fadd2_rn(s01, s23);
       l += sx.x + sx.y;
-      if constexpr (KT == 128) tmem_st64(sp, pk);
-      else tmem_st32(sp, pk);
+      if constexpr (SPLIT) {  // zeros for the other quarters' keys
+        uint32_t row[KT / 2];
+#pragma unroll
+        for (int k = 0; k < KT / 2; ++k) row[k] = k / (LK / 2) == warp ? pk[k % (LK / 2)] : 0u;
+        tmem_st32(sp, row);
+      } else if constexpr (KT == 128) {
+        tmem_st64(sp, pk);
+      } else {
+        tmem_st32(sp, pk);
+      }
       // P.V(j - 1) has been added to O before O or its factor changes.  With
       // one S buffer it was, before S(j) was made; with two, every phase is
       // waited for in turn.
@@ -516,19 +567,84 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       ok = !__any_sync(kFullMask, !ok);
     }
     failed = !ok;
-    if (ok) {
+    // (every softmax warp is here: the table flag is complete after this)
+    named_bar_sync(1, 32 * (tile_warps(0) + (QT > 1 ? tile_warps(QT - 1) : 0)));
+    const bool bad = *bad_flag != 0;
+    if (bad && tid == 0) set_error(p.err, PKV_DEV_TABLE_RANGE);
+    const float vs = KV8 ? p.v_scale[kvh] : 1.f;
+    const bool whole = c.parts == 1;
+    if constexpr (SPLIT) {
+      // Joins the quarters: O * 2^(m - M) to shared memory, summed by row.
+      float2* ml = reinterpret_cast<float2*>(smem);
+      float* os = reinterpret_cast<float*>(smem + Cfg::kRingOff);
+      ml[tid] = make_float2(m, l);
+      named_bar_sync(1, 128);
+      float M = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) M = fmaxf(M, ml[q * 32 + lane].x);
+      const float f = m == -INFINITY ? 0.f : ex2(m - M);
+      if (ok) tc_fence_after();
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t w[32];
+        tmem_ld32(base + Cfg::kOCol + q * 32, w);
+        if (lane < nr) {
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            *reinterpret_cast<float4*>(os + tid * Cfg::kORow + q * 32 + v * 4) =
+                make_float4(__uint_as_float(w[4 * v]) * f, __uint_as_float(w[4 * v + 1]) * f,
+                            __uint_as_float(w[4 * v + 2]) * f, __uint_as_float(w[4 * v + 3]) * f);
+        }
+      }
+      named_bar_sync(1, 128);
+      for (int e = tid; e < nr * (D / 8); e += 128) {
+        const int row = e / (D / 8), d = e % (D / 8) * 8;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) top = fmaxf(top, ml[q * 32 + row].x);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 x = ml[q * 32 + row];
+          sum += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - top);
+        }
+        const float inv = bad ? 0.f : vs / sum;
+        float o[8] = {};
+#pragma unroll
+        for (int q = 0; q < 4 && !bad; ++q) {
+          const float4* x = reinterpret_cast<const float4*>(os + (q * 32 + row) * Cfg::kORow + d);
+          const float4 x0 = x[0], x1 = x[1];
+          o[0] += x0.x; o[1] += x0.y; o[2] += x0.z; o[3] += x0.w;
+          o[4] += x1.x; o[5] += x1.y; o[6] += x1.z; o[7] += x1.w;
+        }
+        const int64_t at = row_at(row);
+        if (ok && whole) {
+          uint4 u;
+          u.x = pack_pair<T>(o[0] * inv, o[1] * inv);
+          u.y = pack_pair<T>(o[2] * inv, o[3] * inv);
+          u.z = pack_pair<T>(o[4] * inv, o[5] * inv);
+          u.w = pack_pair<T>(o[6] * inv, o[7] * inv);
+          *reinterpret_cast<uint4*>(out + at + d) = u;
+        } else if (ok) {
+          const int64_t wrow = at / D * p.parts + part;
+          if (d == 0) p.ws_ml[wrow] = bad ? make_float2(-INFINITY, 0.f) : make_float2(top, sum);
+          float4* dst = reinterpret_cast<float4*>(p.ws_o + wrow * D + d);
+          dst[0] = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+          dst[1] = make_float4(o[4] * inv, o[5] * inv, o[6] * inv, o[7] * inv);
+        }
+      }
+    } else if (ok) {
       tc_fence_after();
-      const float inv = (KV8 ? p.v_scale[kvh] : 1.f) / l;
+      const float inv = vs / l;
       const int64_t at = row_at(min(r, nr - 1));
       const int64_t wrow = at / D * p.parts + part;
-      if (c.parts > 1 && r < nr) p.ws_ml[wrow] = make_float2(m, l);
+      if (!whole && r < nr) p.ws_ml[wrow] = bad ? make_float2(-INFINITY, 0.f) : make_float2(m, l);
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
         uint32_t w[32];
         tmem_ld32(base + Cfg::kOCol + q * 32, w);
-        auto o = [&](int d) { return __uint_as_float(w[d]) * inv; };
+        auto o = [&](int d) { return bad ? 0.f : __uint_as_float(w[d]) * inv; };
         if (r >= nr) continue;
-        if (c.parts == 1) {
+        if (whole) {
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint4 u;
@@ -555,10 +671,10 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
   if (warp == Cfg::kMmaWarp) tmem_dealloc(tmem, Cfg::kTmemCols);
 }
 
-template <typename T, int D, int QT, bool KV8>
+template <typename T, int D, int QT, bool KV8, bool SPLIT>
 int launch_cross_tc(const CrossParams& p, int num_seqs, const CrossMaps& maps, cudaStream_t stream) {
-  using Cfg = CrossTcCfg<T, D, QT, KV8>;
-  auto kern = cross_tc_kernel<T, D, QT, KV8>;
+  using Cfg = CrossTcCfg<T, D, QT, KV8, SPLIT>;
+  auto kern = cross_tc_kernel<T, D, QT, KV8, SPLIT>;
   static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use its shared memory
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
@@ -574,6 +690,20 @@ int launch_cross_tc(const CrossParams& p, int num_seqs, const CrossMaps& maps, c
   const dim3 grid((unsigned)(tiles * p.kv_heads), (unsigned)num_seqs, (unsigned)p.parts);
   kern<<<grid, Cfg::kThreads, Cfg::kSmemBytes, stream>>>(p, maps.k, maps.v);
   return launch_cross_merge<T, D>(p, num_seqs, stream);
+}
+
+// Rows of a thread block: 32 (each on four lanes), 128, or 256.
+enum class CrossRows { k32, k128, k256 };
+
+template <typename T, int D, bool KV8>
+int launch_cross_rows(const CrossParams& p, int num_seqs, CrossRows rows, const CrossMaps& maps,
+                      cudaStream_t stream) {
+  switch (rows) {
+    case CrossRows::k32: return launch_cross_tc<T, D, 1, KV8, true>(p, num_seqs, maps, stream);
+    case CrossRows::k128: return launch_cross_tc<T, D, 1, KV8, false>(p, num_seqs, maps, stream);
+    case CrossRows::k256: return launch_cross_tc<T, D, 2, KV8, false>(p, num_seqs, maps, stream);
+  }
+  return PKV_ERR_ARG;
 }
 
 }  // namespace pkv

@@ -18,13 +18,14 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 
 namespace pkv {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 4;  // tokens per thread block, at most
+constexpr int kRopeTokens = 4;  // tokens per chunk
 
 struct RopeParams {
   const void* q;
@@ -42,38 +43,35 @@ struct RopeParams {
   int64_t num_blocks;
   int block_size;
   int heads, kv_heads, dim;
-  int tokens;             // tokens per thread block
   int units;              // units per head
   unsigned* err;
   pkv_rotary rot;
 };
 
-// V consecutive elements as float.
+// A vector of V elements as it lies in memory, and as float.
 template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float (&f)[V]) {
-  if constexpr (V == 1) {
-    f[0] = static_cast<float>(*p);
-  } else {
-    RowLoad<T, V>::load(p, f);
+struct RopeVec {
+  static_assert(V == 1 || V * sizeof(T) == 16, "one element or 16 bytes");
+  typename std::conditional<V == 1, T, uint4>::type raw;
+  __device__ __forceinline__ void load(const T* p) {
+    raw = *reinterpret_cast<const decltype(raw)*>(p);
   }
-}
-
-// V consecutive elements rounded once to the output type.
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
-  if constexpr (V == 1) {
-    *p = Elem<T>::from_f(f[0]);
-  } else if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  } else {
-    uint4 u;
-    u.x = pack_pair<T>(f[0], f[1]);
-    u.y = pack_pair<T>(f[2], f[3]);
-    u.z = pack_pair<T>(f[4], f[5]);
-    u.w = pack_pair<T>(f[6], f[7]);
-    *reinterpret_cast<uint4*>(p) = u;
+  __device__ __forceinline__ void widen(float (&f)[V]) const {
+    if constexpr (V == 1) f[0] = static_cast<float>(raw);
+    else RowLoad<T, V>::load(reinterpret_cast<const T*>(&raw), f);
   }
-}
+  // Rounded once to the type.
+  __device__ __forceinline__ void narrow(const float (&f)[V]) {
+    if constexpr (V == 1) raw = Elem<T>::from_f(f[0]);
+    else if constexpr (sizeof(T) == 4)
+      raw = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                       __float_as_uint(f[3]));
+    else
+      raw = make_uint4(pack_pair<T>(f[0], f[1]), pack_pair<T>(f[2], f[3]),
+                       pack_pair<T>(f[4], f[5]), pack_pair<T>(f[6], f[7]));
+  }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<decltype(raw)*>(p) = raw; }
+};
 
 // V elements into an FP8 pool: e4m3(x / scale), saturating, from the rotated
 // float32 values (one rounding).
@@ -99,26 +97,32 @@ __device__ __forceinline__ void store_codes(unsigned char* p, const float (&f)[V
 // INTER: pairs are neighbours (2i, 2i + 1), else halves (i, i + R / 2).
 // V: elements per load.  A head's units are two vectors each: with halves,
 // unit u < R / 2 / V is the vectors u and u + R / 2 / V, which hold each
-// other's partners; all other vectors go two to a unit in order.
+// other's partners; all other units are the vectors 2u and 2u + 1.
+//
+// Block (x, y) takes the x-th run of tokens and, of each chunk of up to
+// kRopeTokens of them, the y-th share of the heads; it walks the chunks with
+// the next unit's loads in flight while it turns and stores one.
 template <typename TI, bool FP8, bool INTER, int V>
 __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ float2 s_cs[kRopeTokens * 128];
-  __shared__ int64_t s_row[kRopeTokens];  // pool row of head 0, or -1
+  __shared__ float2 s_cs[2][kRopeTokens * PKV_ROTARY_MAX_PAIRS];
+  __shared__ int64_t s_row[2][kRopeTokens];  // pool row of head 0, or -1
   const int tid = threadIdx.x;
-  const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
-  const int nt = (int)min((int64_t)p.tokens, p.num_tokens - t0);
   const int D = p.dim, H = p.heads, Hk = p.kv_heads, HT = H + 2 * Hk;
   const int pairs = p.rot.rotary_dim >> 1;
   const int half_vecs = INTER ? 0 : pairs / V;  // vectors in each rotated half
   const int vecs = D / V;
-  const int U = p.units;
+  const int64_t first = p.num_tokens * blockIdx.x / gridDim.x;
+  const int64_t last = p.num_tokens * (blockIdx.x + 1) / gridDim.x;
+  const int lanes = kRopeThreads / p.units;  // rows (head of a token) in flight
+  const int u = tid % p.units, lane_row = tid / p.units;
+  const int step = lanes * (int)gridDim.y;
+  const int x0 = lane_row < lanes ? (int)blockIdx.y * lanes + lane_row : INT32_MAX;
 
-  // unit `u` of row `x` (token x / HT, head x % HT)
   struct Unit {
-    float a[V], b[V];
+    RopeVec<TI, V> a, b;
     int tok, head, va, vb;  // head counts through q, k, v; vb < 0: one vector
   };
-  auto fetch = [&](int x, int u, Unit& w) {
+  auto fetch = [&](int64_t t0, int x, Unit& w) {
     w.tok = x / HT;
     w.head = x - w.tok * HT;
     const int64_t t = t0 + w.tok;
@@ -136,44 +140,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const __grid_c
       src = static_cast<const TI*>(p.k) + t * p.k_stride + (int64_t)(w.head - H) * D;
     else
       src = static_cast<const TI*>(p.v) + t * p.v_stride + (int64_t)(w.head - H - Hk) * D;
-    load_vec<TI, V>(src + w.va * V, w.a);
-    if (w.vb >= 0) load_vec<TI, V>(src + w.vb * V, w.b);
+    w.a.load(src + w.va * V);
+    if (w.vb >= 0) w.b.load(src + w.vb * V);
   };
-
-  const int lanes = kRopeThreads / U;  // rows in flight
-  const int u = tid % U, lane_row = tid / U;
-  const int rows = nt * HT;
-  const int step = lanes * (int)gridDim.y;
-  int x = (int)blockIdx.y * lanes + lane_row;
-  bool live = lane_row < lanes && x < rows;
-  Unit cur;
-  if (live) fetch(x, u, cur);
-
-  // ---- angles and pool rows of this block's tokens ---------------------------
-  for (int e = tid; e < nt * pairs; e += kRopeThreads) {
-    const int tok = e / pairs, i = e - tok * pairs;
-    const int64_t pos = p.positions[(int64_t)p.rot.axis[i] * p.num_tokens + t0 + tok];
-    const uint64_t turns = (uint64_t)pos * p.rot.step[i];  // modulo one turn
-    const float half_turns = (float)(int32_t)(turns >> 32) * 0x1p-31f;
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    s_cs[tok * pairs + i] = make_float2(c, s);
-  }
-  if (tid < nt) {
-    const int64_t slot = p.slots[t0 + tid];
-    int64_t row = -1;
-    if (slot >= 0) {
-      const int64_t blk = slot / p.block_size;
-      if (blk < p.num_blocks) row = blk * Hk * p.block_size + (slot - blk * p.block_size);
-      else if (blockIdx.y == 0) set_error(p.err, PKV_DEV_SLOT_RANGE);
-    }
-    s_row[tid] = row;
-  }
-  __syncthreads();
-
-  while (live) {
-    const float2* cs = s_cs + cur.tok * pairs;
-    if (cur.head < H + Hk) {
+  auto finish = [&](int64_t t0, Unit& w, const float2* cs, int64_t row) {
+    const bool key = w.head < H + Hk;
+    float a[V], b[V];
+    w.a.widen(a);
+    if (w.vb >= 0) w.b.widen(b);
+    bool turned = false;
+    if (key) {
       if constexpr (INTER) {
         auto turn = [&](float (&f)[V], int vec) {
 #pragma unroll
@@ -187,41 +163,85 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const __grid_c
             }
           }
         };
-        turn(cur.a, cur.va);
-        if (cur.vb >= 0) turn(cur.b, cur.vb);
+        turn(a, w.va);
+        if (w.vb >= 0) turn(b, w.vb);
+        turned = true;
       } else if (u < half_vecs) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const float2 c = cs[u * V + j];
-          const float xx = cur.a[j], yy = cur.b[j];
-          cur.a[j] = xx * c.x - yy * c.y;
-          cur.b[j] = yy * c.x + xx * c.y;
+          const float xx = a[j], yy = b[j];
+          a[j] = xx * c.x - yy * c.y;
+          b[j] = yy * c.x + xx * c.y;
         }
+        turned = true;
       }
     }
-    if (cur.head < H) {
-      TI* dst = static_cast<TI*>(p.q_out) + (t0 + cur.tok) * p.q_out_stride + (int64_t)cur.head * D;
-      store_vec<TI, V>(dst + cur.va * V, cur.a);
-      if (cur.vb >= 0) store_vec<TI, V>(dst + cur.vb * V, cur.b);
-    } else if (s_row[cur.tok] >= 0) {
-      const bool key = cur.head < H + Hk;
-      const int h = cur.head - (key ? H : H + Hk);
-      const int64_t at = (s_row[cur.tok] + (int64_t)h * p.block_size) * D;
-      void* pool = key ? p.k_cache : p.v_cache;
-      if constexpr (FP8) {
-        const float sc = (key ? p.k_scale : p.v_scale)[h];
-        unsigned char* dst = static_cast<unsigned char*>(pool) + at;
-        store_codes<V>(dst + cur.va * V, cur.a, sc);
-        if (cur.vb >= 0) store_codes<V>(dst + cur.vb * V, cur.b, sc);
-      } else {
-        TI* dst = static_cast<TI*>(pool) + at;
-        store_vec<TI, V>(dst + cur.va * V, cur.a);
-        if (cur.vb >= 0) store_vec<TI, V>(dst + cur.vb * V, cur.b);
-      }
+    const int h = w.head < H ? w.head : w.head - (key ? H : H + Hk);
+    const int64_t at = (row + (int64_t)h * p.block_size) * D;
+    if (FP8 && w.head >= H) {
+      if (row < 0) return;
+      const float sc = (key ? p.k_scale : p.v_scale)[h];
+      unsigned char* dst = static_cast<unsigned char*>(key ? p.k_cache : p.v_cache) + at;
+      store_codes<V>(dst + w.va * V, a, sc);
+      if (w.vb >= 0) store_codes<V>(dst + w.vb * V, b, sc);
+      return;
     }
-    x += step;
-    live = x < rows;
-    if (live) fetch(x, u, cur);
+    TI* dst;
+    if (w.head < H) {
+      dst = static_cast<TI*>(p.q_out) + (t0 + w.tok) * p.q_out_stride + (int64_t)h * D;
+    } else {
+      if (row < 0) return;
+      dst = static_cast<TI*>(key ? p.k_cache : p.v_cache) + at;
+    }
+    if (turned) {  // (what is not turned keeps its bits)
+      w.a.narrow(a);
+      if (w.vb >= 0) w.b.narrow(b);
+    }
+    w.a.store(dst + w.va * V);
+    if (w.vb >= 0) w.b.store(dst + w.vb * V);
+  };
+
+  Unit cur;
+  int64_t t0 = first;
+  int rows = (int)min((int64_t)kRopeTokens, last - t0) * HT;
+  if (t0 < last && x0 < rows) fetch(t0, x0, cur);
+  for (int buf = 0; t0 < last; buf ^= 1) {
+    // ---- angles and pool rows of this chunk's tokens -------------------------
+    const int nt = (int)min((int64_t)kRopeTokens, last - t0);
+    for (int e = tid; e < nt * pairs; e += kRopeThreads) {
+      const int tok = e / pairs, i = e - tok * pairs;
+      const int64_t pos = p.positions[(int64_t)p.rot.axis[i] * p.num_tokens + t0 + tok];
+      const uint64_t turns = (uint64_t)pos * p.rot.step[i];  // modulo one turn
+      const float half_turns = (float)(int32_t)(turns >> 32) * 0x1p-31f;
+      float s, c;
+      sincospif(half_turns, &s, &c);
+      s_cs[buf][e] = make_float2(c, s);
+    }
+    if (tid < nt) {
+      const int64_t slot = p.slots[t0 + tid];
+      int64_t row = -1;
+      if (slot >= 0) {
+        const int64_t blk = slot / p.block_size;
+        if (blk < p.num_blocks) row = blk * Hk * p.block_size + (slot - blk * p.block_size);
+        else if (blockIdx.y == 0) set_error(p.err, PKV_DEV_SLOT_RANGE);
+      }
+      s_row[buf][tid] = row;
+    }
+    // (the other buffer's readers are past this barrier's last use of it)
+    __syncthreads();
+    const int64_t t1 = t0 + nt;
+    const int rows1 = (int)min((int64_t)kRopeTokens, last - t1) * HT;
+    for (int x = x0; x < rows;) {
+      Unit nxt = cur;
+      x += step;
+      if (x < rows) fetch(t0, x, nxt);
+      else if (t1 < last && x0 < rows1) fetch(t1, x0, nxt);
+      finish(t0, cur, s_cs[buf] + cur.tok * pairs, s_row[buf][cur.tok]);
+      cur = nxt;
+    }
+    t0 = t1;
+    rows = rows1;
   }
 }
 
@@ -236,16 +256,23 @@ int launch_rope(RopeParams& p, cudaStream_t stream) {
   const int vecs = single ? p.dim : p.dim / V;
   p.units = (vecs + 1) / 2;
   if (p.units > kRopeThreads) return PKV_ERR_GEOMETRY;
-  p.tokens = (int)std::min<int64_t>(kRopeTokens, std::max<int64_t>(1, p.num_tokens / 1024));
-  const int64_t blocks = (p.num_tokens + p.tokens - 1) / p.tokens;
-  dim3 grid((unsigned)blocks, 1);
-  if (blocks > INT32_MAX) return PKV_ERR_ARG;
-  if (single)
-    rope_write_kernel<TI, FP8, false, 1><<<grid, kRopeThreads, 0, stream>>>(p);
-  else if (inter)
-    rope_write_kernel<TI, FP8, true, V><<<grid, kRopeThreads, 0, stream>>>(p);
-  else
-    rope_write_kernel<TI, FP8, false, V><<<grid, kRopeThreads, 0, stream>>>(p);
+  auto kern = single ? rope_write_kernel<TI, FP8, false, 1>
+              : inter ? rope_write_kernel<TI, FP8, true, V>
+                      : rope_write_kernel<TI, FP8, false, V>;
+  int dev = 0, sms = 0, per_sm = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kRopeThreads, 0) != cudaSuccess ||
+      sms < 1 || per_sm < 1)
+    return PKV_ERR_CUDA;
+  // One wave of blocks, each with an equal run of tokens; few tokens share
+  // their heads among the blocks that are left.
+  const int64_t slots = (int64_t)sms * per_sm;
+  const int64_t x = std::min<int64_t>(p.num_tokens, slots);
+  const int lanes = kRopeThreads / p.units;
+  const int64_t passes = (p.heads + 2 * (int64_t)p.kv_heads + lanes - 1) / lanes;  // of one token
+  const int64_t y = std::max<int64_t>(1, std::min<int64_t>(passes, slots / x));
+  kern<<<dim3((unsigned)x, (unsigned)std::min<int64_t>(y, 65535)), kRopeThreads, 0, stream>>>(p);
   return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
