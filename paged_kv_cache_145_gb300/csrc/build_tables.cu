@@ -31,6 +31,18 @@ namespace pkv {
 
 namespace cg = cooperative_groups;
 
+// Division by the block size for numbers below 2^31: q = n * mul / 2^(32 +
+// shift), mul = floor(2^(32 + shift) / d) + 1 with 2^shift < d <= 2^(shift + 1).
+// (mul exceeds 2^(32 + shift) / d by at most 1, so the quotient by less than
+// n / 2^(32 + shift) < 1 / d: no whole number lies between.)
+struct BlockDiv {
+  uint32_t d, mul, shift;
+  __device__ __forceinline__ int quot(int n) const {
+    return d == 1 ? n : (int)(__umulhi((uint32_t)n, mul) >> shift);
+  }
+  __device__ __forceinline__ int blocks(int len) const { return len > 0 ? quot(len - 1) + 1 : 0; }
+};
+
 struct BuildParams {
   int32_t* ring;             // [num_blocks]
   const int64_t* state;      // {head, count}
@@ -46,32 +58,34 @@ struct BuildParams {
   int64_t max_tokens;
   int num_seqs;
   int max_blocks;
-  int block_size;
+  BlockDiv b;                // positions per block
   int share;                 // rows per thread block
   bool fill;                 // build_tables_kernel writes the slot map too
   bool vectors;              // slots and positions are 16-byte aligned
   unsigned* err;
 };
 
-constexpr int kBuildThreads = 1024;
+constexpr int kBuildThreads = 512;
 constexpr int kBuildWarps = kBuildThreads / 32;
 constexpr int kBuildCluster = 8;  // the portable cluster size
 
 // Blocks taken, blocks given back and new tokens: of a row, of a run of
-// rows, or before a row.  64 bits: 65535 rows of up to 2^31 - 1 positions.
+// rows, or before a row.  Sums stop at kMany, above any count that passes
+// the checks (blocks and tokens are at most 2^30): min(a + b, kMany) is
+// associative, and 32 bits halve the scans.
+constexpr unsigned kMany = (1u << 30) + 1;
+
 struct Moves {
-  long long take, give, tokens;
+  unsigned take, give, tokens;
 };
 
 __device__ __forceinline__ Moves operator+(const Moves& a, const Moves& b) {
-  return {a.take + b.take, a.give + b.give, a.tokens + b.tokens};
+  return {min(a.take + b.take, kMany), min(a.give + b.give, kMany), min(a.tokens + b.tokens, kMany)};
 }
 
-__device__ __forceinline__ int blocks_of(int len, int b) { return len > 0 ? (len - 1) / b + 1 : 0; }
-
-__device__ __forceinline__ Moves moves_of(int o, int n, int b) {
-  const int d = blocks_of(n, b) - blocks_of(o, b);
-  return {d > 0 ? d : 0, d < 0 ? -d : 0, n > o ? (long long)n - o : 0};
+__device__ __forceinline__ Moves moves_of(int have, int want, int o, int n) {
+  return {(unsigned)max(want - have, 0), (unsigned)max(have - want, 0),
+          min((unsigned)max(n - o, 0), kMany)};
 }
 
 __device__ __forceinline__ Moves shfl_up(const Moves& a, int d) {
@@ -90,11 +104,33 @@ __device__ __forceinline__ int find_row(const int* pre, int n, int i) {
   return lo;
 }
 
+// Consecutive tokens that one thread places: one search and mostly one table
+// entry serve them, and the stores are whole 16-byte vectors.
+constexpr int kGroup = 4;
+
+// Stores tokens t0 .. t0 + kGroup - 1 as far as they lie in [lo, hi).
+__device__ __forceinline__ void store_tokens(const BuildParams& p, int64_t t0, int64_t lo, int64_t hi,
+                                             const int64_t (&slot)[kGroup], const int (&pos)[kGroup]) {
+  if (p.vectors && t0 >= lo && t0 + kGroup <= hi) {
+    reinterpret_cast<longlong2*>(p.slots + t0)[0] = make_longlong2(slot[0], slot[1]);
+    reinterpret_cast<longlong2*>(p.slots + t0)[1] = make_longlong2(slot[2], slot[3]);
+    *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < kGroup; ++k)
+    if (t0 + k >= lo && t0 + k < hi) {
+      p.slots[t0 + k] = slot[k];
+      p.positions[t0 + k] = pos[k];
+    }
+}
+
 __global__ void __launch_bounds__(kBuildThreads) build_tables_kernel(const BuildParams p) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), blocks = (int)cluster.num_blocks();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = p.block_size;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = (int)blockDim.x;
+  const BlockDiv b = p.b;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // fill_slots_kernel, if it follows
   // This block's rows: lengths and prefixes (over all rows before).
   extern __shared__ int rows[];
   int* const s_old = rows;
@@ -103,14 +139,14 @@ __global__ void __launch_bounds__(kBuildThreads) build_tables_kernel(const Build
   int* const s_give = rows + 3 * p.share;
   int* const s_tok = rows + 4 * p.share;
   __shared__ Moves s_warp[kBuildWarps];   // sums of the warps' rows
-  __shared__ Moves s_part[2];             // rows before this block's, and all rows
+  __shared__ Moves s_part[2][kBuildWarps];  // the rows before this block's, and after them
   __shared__ unsigned s_bits[kBuildCluster];
   const int first = min(rank * p.share, p.num_seqs);
   const int mine = min(p.share, p.num_seqs - first);
 
   // ---- sums of the rows of the blocks before and after this one ------------
   unsigned bits = 0;
-  const long long cap = min((long long)p.max_blocks * b, 0x7fffffffLL);
+  const int cap = (int)min((long long)p.max_blocks * b.d, 0x7fffffffLL);
   auto row = [&](int s, int& o, int& n) {
     o = p.old_lens[s];
     n = p.new_lens[s];
@@ -121,17 +157,17 @@ __global__ void __launch_bounds__(kBuildThreads) build_tables_kernel(const Build
   };
   Moves before{0, 0, 0}, after{0, 0, 0};
   if (blocks > 1) {
-    for (int s = tid; s < p.num_seqs; s += kBuildThreads) {
+    for (int s = tid; s < p.num_seqs; s += threads) {
       if (s >= first && s < first + mine) continue;
       int o, n;
       row(s, o, n);
-      const Moves m = moves_of(o, n, b);
+      const Moves m = moves_of(b.blocks(o), b.blocks(n), o, n);
       if (s < first) before = before + m;
       else after = after + m;
     }
   }
   // ---- this block's rows: `per` consecutive ones per thread -----------------
-  const int per = (mine + kBuildThreads - 1) / kBuildThreads;
+  const int per = (mine + threads - 1) / threads;
   const int r0 = min(tid * per, mine), r1 = min(r0 + per, mine);
   Moves sum{0, 0, 0};
   for (int r = r0; r < r1; ++r) {
@@ -139,7 +175,7 @@ __global__ void __launch_bounds__(kBuildThreads) build_tables_kernel(const Build
     row(first + r, o, n);
     s_old[r] = o;
     s_new[r] = n;
-    sum = sum + moves_of(o, n, b);
+    sum = sum + moves_of(b.blocks(o), b.blocks(n), o, n);
   }
   Moves scan = sum;
 #pragma unroll
@@ -148,19 +184,7 @@ __global__ void __launch_bounds__(kBuildThreads) build_tables_kernel(const Build
     if (lane >= d) scan = scan + up;
   }
   if (lane == 31) s_warp[warp] = scan;
-  if (tid < 2) s_part[tid] = Moves{0, 0, 0};
-  if (tid < kBuildCluster) s_bits[tid] = 0;
-  // Other blocks write s_bits[1..] once every block has cleared its own.
-  if (blocks > 1) cluster.barrier_arrive();
-  const int64_t head = p.state[0], count = p.state[1];
-  __syncthreads();
   if (blocks > 1) {
-    auto add = [&](Moves& to, const Moves& m) {
-      // three block-wide sums; integer additions commute
-      atomicAdd(reinterpret_cast<unsigned long long*>(&to.take), (unsigned long long)m.take);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&to.give), (unsigned long long)m.give);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&to.tokens), (unsigned long long)m.tokens);
-    };
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
       before = before + Moves{__shfl_xor_sync(kFullMask, before.take, d),
@@ -170,12 +194,17 @@ __global__ void __launch_bounds__(kBuildThreads) build_tables_kernel(const Build
                             __shfl_xor_sync(kFullMask, after.give, d),
                             __shfl_xor_sync(kFullMask, after.tokens, d)};
     }
-    if (lane == 0 && warp * 32 < p.num_seqs) {
-      add(s_part[0], before);
-      add(s_part[1], after);
+    if (lane == 0) {
+      s_part[0][warp] = before;
+      s_part[1][warp] = after;
     }
   }
-  Moves w = s_warp[lane], w_scan = w;
+  if (tid < kBuildCluster) s_bits[tid] = 0;
+  // Other blocks write s_bits[1..] once every block has cleared its own.
+  if (blocks > 1) cluster.barrier_arrive();
+  const int64_t head = p.state[0], count = p.state[1];
+  __syncthreads();
+  Moves w_scan = lane < threads / 32 ? s_warp[lane] : Moves{0, 0, 0};
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const Moves up = shfl_up(w_scan, d);
@@ -187,19 +216,23 @@ __global__ void __launch_bounds__(kBuildThreads) build_tables_kernel(const Build
   Moves base{__shfl_sync(kFullMask, w_scan.take, prev), __shfl_sync(kFullMask, w_scan.give, prev),
              __shfl_sync(kFullMask, w_scan.tokens, prev)};
   if (warp == 0) base = Moves{0, 0, 0};
-  __syncthreads();
-  before = s_part[0];
-  const Moves all = before + own + s_part[1];
+  if (blocks > 1) {
+    before = after = Moves{0, 0, 0};
+    for (int w = 0; w < threads / 32; ++w) {
+      before = before + s_part[0][w];
+      after = after + s_part[1][w];
+    }
+  }
+  const Moves all = before + own + after;
 
   // ---- checks ----------------------------------------------------------------
   if (head < 0 || head >= p.num_blocks || count < 0 || count > p.num_blocks ||
-      all.give > p.num_blocks - count)
+      (int64_t)all.give > p.num_blocks - count)
     bits |= PKV_DEV_FREE_LIST;
-  if (all.take > count) bits |= PKV_DEV_NOMEM;
-  if (all.tokens > p.max_tokens) bits |= PKV_DEV_TOKENS;
-  // Every sum fits 32 bits from here on (take <= count, give <= num_blocks,
-  // tokens <= max_tokens), in every block alike: the flags so far are taken
-  // over the whole block first, and the other blocks' through the cluster.
+  if ((int64_t)all.take > count) bits |= PKV_DEV_NOMEM;
+  if ((int64_t)all.tokens > p.max_tokens) bits |= PKV_DEV_TOKENS;
+  // Every block sees every row, so all of them agree on these flags; without
+  // one no sum has reached kMany.
   const bool sums_ok = !__syncthreads_or(bits != 0);
   auto ring_at = [&](int64_t i) {
     int64_t x = head + i;
@@ -207,28 +240,46 @@ __global__ void __launch_bounds__(kBuildThreads) build_tables_kernel(const Build
   };
   auto outside = [&](int e) { return e < 0 || (int64_t)e >= p.num_blocks; };
   if (sums_ok) {
-    Moves at = before + base + (scan + Moves{-sum.take, -sum.give, -sum.tokens});
+    Moves at = before + base + Moves{scan.take - sum.take, scan.give - sum.give, scan.tokens - sum.tokens};
     for (int r = r0; r < r1; ++r) {
       s_take[r] = (int)at.take;
       s_give[r] = (int)at.give;
       s_tok[r] = (int)at.tokens;
-      at = at + moves_of(s_old[r], s_new[r], b);
+      at = at + moves_of(b.blocks(s_old[r]), b.blocks(s_new[r]), s_old[r], s_new[r]);
       // the partly filled last block that the row's first new tokens go to
-      if (s_new[r] > s_old[r] && s_old[r] % b != 0 &&
-          outside(p.tables[(int64_t)(first + r) * p.max_blocks + s_old[r] / b]))
+      const int full = b.quot(s_old[r]);
+      if (s_new[r] > s_old[r] && full * (int)b.d != s_old[r] &&
+          outside(p.tables[(int64_t)(first + r) * p.max_blocks + full]))
         bits |= PKV_DEV_TABLE_RANGE;
     }
   }
   __syncthreads();
+  // The block's moves: flat items, blocks taken first, then blocks given
+  // back.  A move is one entry (checked) and the place it goes to.
   const int take0 = (int)before.take, give0 = (int)before.give;
-  if (sums_ok) {
-    for (int64_t i = tid; i < own.take; i += kBuildThreads)
-      if (outside(p.ring[ring_at(take0 + i)])) bits |= PKV_DEV_FREE_LIST;
-    for (int64_t i = tid; i < own.give; i += kBuildThreads) {
-      const int r = find_row(s_give, mine, (int)(give0 + i));
-      const int j = blocks_of(s_new[r], b) + (int)(give0 + i - s_give[r]);
-      if (outside(p.tables[(int64_t)(first + r) * p.max_blocks + j])) bits |= PKV_DEV_TABLE_RANGE;
+  const int64_t moves = sums_ok ? (int64_t)own.take + own.give : 0;
+  struct Move {
+    int32_t entry;
+    int32_t* to;
+  };
+  auto move = [&](int64_t i) {
+    Move m;
+    if (i < own.take) {
+      const int x = take0 + (int)i, r = find_row(s_take, mine, x);
+      m.to = p.tables + (int64_t)(first + r) * p.max_blocks + b.blocks(s_old[r]) + x - s_take[r];
+      m.entry = p.ring[ring_at(x)];
+    } else {
+      const int x = give0 + (int)(i - own.take), r = find_row(s_give, mine, x);
+      m.to = p.ring + ring_at(count + x);
+      m.entry = p.tables[(int64_t)(first + r) * p.max_blocks + b.blocks(s_new[r]) + x - s_give[r]];
     }
+    return m;
+  };
+  Move kept{0, nullptr};  // the thread's first, so that most need no second look
+  for (int64_t i = tid; i < moves; i += threads) {
+    const Move m = move(i);
+    if (outside(m.entry)) bits |= i < own.take ? PKV_DEV_FREE_LIST : PKV_DEV_TABLE_RANGE;
+    if (i == tid) kept = m;
   }
   bits = __reduce_or_sync(kFullMask, bits);
   if (lane == 0 && bits) atomicOr(&s_bits[0], bits);
@@ -253,107 +304,109 @@ __global__ void __launch_bounds__(kBuildThreads) build_tables_kernel(const Build
   if (!ok && tid == 0 && rank == 0) set_error(p.err, seen);
   if (rank == 0 && tid == 0) {
     p.state_out[0] = ok ? ring_at(all.take) : head;
-    p.state_out[1] = ok ? count - all.take + all.give : count;
+    p.state_out[1] = ok ? count - (int64_t)all.take + (int64_t)all.give : count;
     if (!ok || p.num_seqs == 0) p.starts[0] = 0;
   }
   if (ok) {
-    for (int r = tid; r < mine; r += kBuildThreads) {
+    if (kept.to) *kept.to = kept.entry;
+    for (int r = tid; r < mine; r += threads) {
       p.seq_lens[first + r] = s_new[r];
       p.starts[first + r] = s_tok[r];
     }
     if (first + mine == p.num_seqs && mine > 0 && tid == 0) p.starts[p.num_seqs] = (int)all.tokens;
-    for (int64_t i = tid; i < own.take; i += kBuildThreads) {
-      const int r = find_row(s_take, mine, (int)(take0 + i));
-      const int j = blocks_of(s_old[r], b) + (int)(take0 + i - s_take[r]);
-      p.tables[(int64_t)(first + r) * p.max_blocks + j] = p.ring[ring_at(take0 + i)];
-    }
-    for (int64_t i = tid; i < own.give; i += kBuildThreads) {
-      const int r = find_row(s_give, mine, (int)(give0 + i));
-      const int j = blocks_of(s_new[r], b) + (int)(give0 + i - s_give[r]);
-      p.ring[ring_at(count + give0 + i)] = p.tables[(int64_t)(first + r) * p.max_blocks + j];
+    // The other moves, and groups of kGroup tokens at multiples of kGroup (a
+    // group that other blocks share is written in part).
+    const int tok0 = (int)before.tokens, tok1 = tok0 + (int)own.tokens;
+    const int g0 = tok0 / kGroup, groups = p.fill && tok1 > tok0 ? (tok1 - 1) / kGroup + 1 - g0 : 0;
+    const int64_t rest = moves > threads ? moves - threads : 0;
+    for (int64_t i = tid; i < rest + groups; i += threads) {
+      if (i < rest) {
+        const Move m = move(threads + i);
+        *m.to = m.entry;
+        continue;
+      }
+      const int t0 = (g0 + (int)(i - rest)) * kGroup;
+      int r = find_row(s_tok, mine, max(t0, tok0)), at = -1, entry = 0;
+      int64_t slot[kGroup];
+      int pos[kGroup];
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k) {
+        const int t = t0 + k;
+        if (t < tok0 || t >= tok1) continue;
+        while (r + 1 < mine && s_tok[r + 1] <= t) {
+          ++r;
+          at = -1;
+        }
+        pos[k] = s_old[r] + t - s_tok[r];
+        const int blk = b.quot(pos[k]);
+        if (at != blk) {
+          at = blk;
+          const int have = b.blocks(s_old[r]);
+          entry = at < have ? p.tables[(int64_t)(first + r) * p.max_blocks + at]
+                            : p.ring[ring_at(s_take[r] + at - have)];
+        }
+        slot[k] = (int64_t)entry * b.d + (pos[k] - at * (int)b.d);
+      }
+      store_tokens(p, t0, tok0, tok1, slot, pos);
     }
   } else {
     // lengths as they were: a row with a bad length keeps that length
-    for (int r = tid; r < mine; r += kBuildThreads) {
+    for (int r = tid; r < mine; r += threads) {
       p.starts[first + r + 1] = 0;
       p.seq_lens[first + r] = p.old_lens[first + r];
     }
   }
   if (!p.fill) return;
-  const int tok0 = (int)before.tokens;
-  if (ok) {
-    for (int i = tid; i < own.tokens; i += kBuildThreads) {
-      const int t = tok0 + i;
-      const int r = find_row(s_tok, mine, t);
-      const int pos = s_old[r] + t - s_tok[r];
-      const int blk = pos / b, have = blocks_of(s_old[r], b);
-      const int e = blk < have ? p.tables[(int64_t)(first + r) * p.max_blocks + blk]
-                               : p.ring[ring_at(s_take[r] + blk - have)];
-      p.slots[t] = (int64_t)e * b + (pos - blk * b);
-      p.positions[t] = pos;
-    }
-  }
-  for (int64_t t = (ok ? all.tokens : 0) + rank * kBuildThreads + tid; t < p.max_tokens;
-       t += (int64_t)blocks * kBuildThreads) {
+  for (int64_t t = (ok ? (int64_t)all.tokens : 0) + rank * threads + tid; t < p.max_tokens;
+       t += (int64_t)blocks * threads) {
     p.slots[t] = -1;
     p.positions[t] = 0;
   }
 }
 
 // The slot map and positions of a wide step, from the tables, lengths and
-// starts that build_tables_kernel left (whatever it decided): a thread takes
-// kFillTokens consecutive tokens, so that one search and mostly one table
-// entry serve them all and the stores are whole 16-byte vectors.
+// starts that build_tables_kernel left (whatever it decided).  Launched
+// while that kernel runs; its set-up overlaps it.
 constexpr int kFillThreads = 256;
-constexpr int kFillTokens = 4;
 constexpr int kFillRows = 8192;  // starts held in shared memory, at most
 
 __global__ void __launch_bounds__(kFillThreads) fill_slots_kernel(const BuildParams p) {
   extern __shared__ int rows[];
-  const int S = p.num_seqs, b = p.block_size;
+  const int S = p.num_seqs;
+  const BlockDiv b = p.b;
+  const int64_t t0 = ((int64_t)blockIdx.x * kFillThreads + threadIdx.x) * kGroup;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int total = p.starts[S];
-  const int64_t t0 = ((int64_t)blockIdx.x * kFillThreads + threadIdx.x) * kFillTokens;
   const int* starts = p.starts;
-  if ((int64_t)blockIdx.x * kFillThreads * kFillTokens < total && S <= kFillRows) {
+  if ((int64_t)blockIdx.x * kFillThreads * kGroup < total && S <= kFillRows) {
     for (int r = threadIdx.x; r < S; r += kFillThreads) rows[r] = p.starts[r];
     starts = rows;
     __syncthreads();
   }
   if (t0 >= p.max_tokens) return;
-  int64_t slot[kFillTokens];
-  int pos[kFillTokens];
-  int r = t0 < total ? find_row(starts, S, (int)t0) : 0, blk = -1, entry = 0;
+  int64_t slot[kGroup];
+  int pos[kGroup];
+  int r = t0 < total ? find_row(starts, S, (int)t0) : 0, at = -1, entry = 0;
 #pragma unroll
-  for (int i = 0; i < kFillTokens; ++i) {
-    slot[i] = -1;
-    pos[i] = 0;
-    const int64_t t = t0 + i;
+  for (int k = 0; k < kGroup; ++k) {
+    slot[k] = -1;
+    pos[k] = 0;
+    const int64_t t = t0 + k;
     if (t >= total) continue;
-    // the row of token t: the last with starts[r] <= t
     while (r + 1 < S && starts[r + 1] <= t) {
       ++r;
-      blk = -1;
+      at = -1;
     }
     const int next = r + 1 < S ? starts[r + 1] : total;
-    pos[i] = p.seq_lens[r] - next + (int)t;  // the row's last token is its last position
-    if (blk != pos[i] / b) {
-      blk = pos[i] / b;
-      entry = p.tables[(int64_t)r * p.max_blocks + blk];
+    pos[k] = p.seq_lens[r] - next + (int)t;  // the row's last token is its last position
+    const int blk = b.quot(pos[k]);
+    if (at != blk) {
+      at = blk;
+      entry = p.tables[(int64_t)r * p.max_blocks + at];
     }
-    slot[i] = (int64_t)entry * b + (pos[i] - blk * b);
+    slot[k] = (int64_t)entry * b.d + (pos[k] - at * (int)b.d);
   }
-  if (p.vectors && t0 + kFillTokens <= p.max_tokens) {
-    reinterpret_cast<longlong2*>(p.slots + t0)[0] = make_longlong2(slot[0], slot[1]);
-    reinterpret_cast<longlong2*>(p.slots + t0)[1] = make_longlong2(slot[2], slot[3]);
-    *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kFillTokens; ++i)
-      if (t0 + i < p.max_tokens) {
-        p.slots[t0 + i] = slot[i];
-        p.positions[t0 + i] = pos[i];
-      }
-  }
+  store_tokens(p, t0, 0, p.max_tokens, slot, pos);
 }
 
 }  // namespace pkv
@@ -362,11 +415,13 @@ int pkv_launch_build_tables(pkv::BuildParams p, cudaStream_t stream) {
   using namespace pkv;
   p.err = pkv_error_word();
   if (!p.err) return PKV_ERR_CUDA;
-  // One block serves a step of few rows; more rows are shared by a cluster.
-  // Few tokens are written along; a wider slot map by a second kernel over the
-  // whole GPU.
-  const int cluster = p.num_seqs <= kBuildThreads ? 1 : kBuildCluster;
-  p.fill = p.max_tokens <= 2 * kBuildThreads;
+  // One small block serves a step of few rows and tokens (8 rows: 3.8 us; a
+  // cluster 5.4), a cluster the others.  Up to 16384 tokens are written along
+  // (256 rows, 16384 tokens: 10 us), a wider slot map by a second kernel over
+  // the whole GPU.
+  const bool small = p.num_seqs <= 256 && p.max_tokens <= 1024;
+  const int cluster = small ? 1 : kBuildCluster, threads = small ? 256 : kBuildThreads;
+  p.fill = p.max_tokens <= 16384;
   p.vectors = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15u) == 0;
   p.share = (p.num_seqs + cluster - 1) / cluster;
   const size_t smem = (size_t)p.share * 5 * sizeof(int);
@@ -376,7 +431,7 @@ int pkv_launch_build_tables(pkv::BuildParams p, cudaStream_t stream) {
     return PKV_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)cluster);
-  cfg.blockDim = dim3(kBuildThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
@@ -386,12 +441,14 @@ int pkv_launch_build_tables(pkv::BuildParams p, cudaStream_t stream) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, build_tables_kernel, p) != cudaSuccess) return PKV_ERR_CUDA;
-  if (!p.fill) {
-    const int64_t per = kFillThreads * kFillTokens;
-    fill_slots_kernel<<<(unsigned)((p.max_tokens + per - 1) / per), kFillThreads,
-                        std::min(p.num_seqs, kFillRows) * sizeof(int), stream>>>(p);
-  }
-  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  if (p.fill) return PKV_OK;
+  const int64_t per = kFillThreads * kGroup;
+  cfg.gridDim = dim3((unsigned)((p.max_tokens + per - 1) / per));
+  cfg.blockDim = dim3(kFillThreads);
+  cfg.dynamicSmemBytes = std::min(p.num_seqs, kFillRows) * sizeof(int);
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, fill_slots_kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 extern "C" int paged_build_tables(int64_t num_blocks, int32_t block_size, int32_t* free_list,
@@ -401,7 +458,7 @@ extern "C" int paged_build_tables(int64_t num_blocks, int32_t block_size, int32_
                                   int32_t* seq_lens, int64_t* free_state_out,
                                   int32_t* query_starts, int64_t* slot_mapping,
                                   int32_t* positions, int64_t max_tokens, cudaStream_t stream) {
-  if (num_blocks < 1 || num_blocks > INT32_MAX || block_size < 1 || num_seqs < 0 ||
+  if (num_blocks < 1 || num_blocks > (1 << 30) || block_size < 1 || num_seqs < 0 ||
       num_seqs > 65535 || max_blocks_per_seq < 1 || max_tokens < 0 || max_tokens > (1 << 30))
     return PKV_ERR_ARG;
   if (!free_list || !free_state || !free_state_out || !query_starts) return PKV_ERR_NULL;
@@ -427,6 +484,10 @@ extern "C" int paged_build_tables(int64_t num_blocks, int32_t block_size, int32_
   p.max_tokens = max_tokens;
   p.num_seqs = num_seqs;
   p.max_blocks = max_blocks_per_seq;
-  p.block_size = block_size;
+  p.b.d = (uint32_t)block_size;
+  if (block_size > 1) {
+    while ((2u << p.b.shift) < p.b.d) ++p.b.shift;
+    p.b.mul = (uint32_t)((1ull << (32 + p.b.shift)) / p.b.d + 1);
+  }
   return pkv_launch_build_tables(p, stream);
 }
