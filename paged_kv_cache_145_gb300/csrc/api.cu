@@ -7,7 +7,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "cross_tc.cuh"
+#include "cross_stream.cuh"
 #include "decode_launch.cuh"
 #include "prefill.cuh"
 
@@ -528,50 +528,86 @@ namespace {
 
 // How cross attention runs: on tensor cores (16-bit pools, FP8 pools of
 // head_dim 128) in blocks of 256 rows, or, where no sequence has more, of 128
-// or 32 rows two to an SM; else on CUDA cores in blocks of 8 rows; and the
-// split of the states where the blocks would not fill the GPU: whole
-// runs of 128 positions, as few parts as give every SM its blocks.
+// or 32 rows two to an SM; else on CUDA cores in blocks of 8 rows.  Where the
+// blocks would not fill the GPU the states are split in whole runs of 128
+// positions, as few parts as give every SM its blocks.  At most 32 rows run
+// as one stream of all states instead, unless the sequences are too many for
+// a block to hold their tile counts (there are blocks enough then).
 struct CrossPlan {
   bool tc;
   pkv::CrossRows rows;
-  int parts, part;
+  int parts, part;    // stream: blocks, rows of a workspace slot
+  int64_t ws_rows;    // workspace rows of head_dim floats and one (m, l) pair
 };
 
-CrossPlan cross_plan(const pkv_cache* c, int num_seqs, int num_heads, int max_queries,
-                     int max_len) {
+CrossPlan cross_plan(const pkv_cache* c, int64_t total_queries, int num_seqs, int num_heads,
+                     int max_queries, int max_len) {
   CrossPlan pl{};
   pl.tc = c->dtype == PKV_F16 || c->dtype == PKV_BF16 ||
           (c->dtype == PKV_FP8_E4M3 && c->head_dim == 128);
   const int64_t rows = (int64_t)max_queries * (num_heads / c->num_kv_heads);
-  pl.rows = rows > 128  ? pkv::CrossRows::k256
-            : rows > 32 ? pkv::CrossRows::k128
-                        : pkv::CrossRows::k32;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
     cudaGetLastError();
     sms = 1;
   }
+  const int64_t tiles = (int64_t)num_seqs * c->num_kv_heads * (((int64_t)max_len + 63) / 64);
+  if (pl.tc && rows <= 32 && num_seqs <= pkv::kStreamSeqs && tiles < INT32_MAX) {
+    pl.rows = pkv::CrossRows::kStream;
+    // at least about four tiles a block
+    pl.parts = (int)std::max<int64_t>(1, std::min<int64_t>(2 * sms, (tiles + (std::getenv("XD") ? std::atoi(std::getenv("XD")) : 4) - 1) / (std::getenv("XD") ? std::atoi(std::getenv("XD")) : 4)));
+    pl.part = (int)rows;
+    pl.ws_rows = pl.parts > 1 ? 2 * pl.parts * rows : 0;
+    return pl;
+  }
+  pl.rows = rows > 128  ? pkv::CrossRows::k256
+            : rows > 32 ? pkv::CrossRows::k128
+                        : pkv::CrossRows::k32;
   const bool wide = pl.rows == pkv::CrossRows::k256;
   const int64_t per = !pl.tc ? pkv::kCrossRows : wide ? 256 : rows > 32 ? 128 : 32;
   const int64_t slots = (int64_t)sms * (pl.tc ? (wide ? 1 : 2) : 8);
   const int64_t blocks = std::max<int64_t>(1, (int64_t)num_seqs * c->num_kv_heads * ((rows + per - 1) / per));
-  static const int mul = std::getenv("XMUL") ? std::atoi(std::getenv("XMUL")) : 1;  // EXPERIMENT
   constexpr int kRun = 128;
   const int64_t runs = std::max<int64_t>(1, ((int64_t)max_len + kRun - 1) / kRun);
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(runs, slots * mul / blocks));
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(runs, slots / blocks));
   const int64_t part = (runs + want - 1) / want * kRun;
   pl.part = (int)part;
   pl.parts = (int)((runs * kRun + part - 1) / part);
+  pl.ws_rows = pl.parts > 1 ? total_queries * num_heads * pl.parts : 0;
   return pl;
 }
 
+// Describes a pool to the cross attention kernels as pages of 8-row groups:
+// {128 bytes of a row, 8 rows, 128-byte column blocks, groups, N * Hk pages},
+// read in boxes of a page's rows (at most `keys`) with the 128-byte swizzle.
+// A box lands as its groups one after the other, each with its column blocks
+// of 8 x 128 bytes, the order in which the MMA operands are laid out.
+bool encode_page_map(CUtensorMap* map, const pkv_cache* c, void* base, int keys) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t elt = elem_bytes(c->dtype), row = c->head_dim * elt;
+  const cuuint64_t dims[5] = {128 / elt, 8, row / 128, (cuuint64_t)c->block_size / 8,
+                              (cuuint64_t)c->num_blocks * c->num_kv_heads};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, c->block_size * row};
+  const cuuint32_t box[5] = {(cuuint32_t)(128 / elt), 8, (cuuint32_t)(row / 128),
+                             (cuuint32_t)(std::min(c->block_size, keys) / 8), 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUtensorMapDataType ty =
+      c->dtype == PKV_FP8_E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+      : c->dtype == PKV_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(map, ty, 5, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Bytes of the (m, l) pairs and where the partial outputs start.
-WsLayout cross_workspace(int64_t total_queries, int num_heads, int head_dim, int parts) {
+WsLayout cross_workspace(const CrossPlan& pl, int head_dim) {
   WsLayout w{};
-  w.parts = parts;
-  if (parts <= 1) return w;
-  const size_t rows = (size_t)total_queries * num_heads * parts;
+  w.parts = pl.parts;
+  if (pl.ws_rows == 0) return w;
+  const size_t rows = (size_t)pl.ws_rows;
   w.ml_bytes = rows * sizeof(float2);
   w.o_offset = (w.ml_bytes + 255) & ~size_t(255);
   w.total = w.o_offset + rows * head_dim * sizeof(float);
@@ -593,8 +629,9 @@ size_t paged_attention_cross_workspace_bytes(const pkv_cache* cache, int64_t tot
   if (!cache || !cross_args_ok(cache, total_queries, num_seqs, num_heads, max_queries) ||
       max_enc_len < 0)
     return 0;
-  const CrossPlan sp = cross_plan(cache, num_seqs, num_heads, max_queries, max_enc_len);
-  return cross_workspace(total_queries, num_heads, cache->head_dim, sp.parts).total;
+  const CrossPlan sp =
+      cross_plan(cache, total_queries, num_seqs, num_heads, max_queries, max_enc_len);
+  return cross_workspace(sp, cache->head_dim).total;
 }
 
 int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_queries,
@@ -621,8 +658,9 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
       (reinterpret_cast<uintptr_t>(enc_lens) & 3u) ||
       (reinterpret_cast<uintptr_t>(query_starts) & 3u))
     return PKV_ERR_ALIGN;
-  const CrossPlan sp = cross_plan(cache, num_seqs, num_heads, max_queries, max_len);
-  const WsLayout ws = cross_workspace(total_queries, num_heads, cache->head_dim, sp.parts);
+  const CrossPlan sp =
+      cross_plan(cache, total_queries, num_seqs, num_heads, max_queries, max_len);
+  const WsLayout ws = cross_workspace(sp, cache->head_dim);
   if (ws.total > 0) {
     if (!workspace || workspace_bytes < ws.total) return PKV_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PKV_ERR_ALIGN;
@@ -645,6 +683,7 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
   p.tables = block_tables;
   p.max_blocks = max_blocks_per_seq;
   p.lens = enc_lens;
+  p.num_seqs = num_seqs;
   p.max_len = max_len;
   p.qscale = scale * 1.4426950408889634f;  // log2(e): scores in base-2 units
   p.parts = sp.parts;
@@ -656,9 +695,12 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
   p.err = err;
   if (!sp.tc)
     return pkv_launch_cross(p, cache->dtype, cache->io_dtype, num_seqs, cache->head_dim, stream);
+  // Pages are a 32-bit coordinate, and one past the last is used.
+  if (cache->num_blocks * cache->num_kv_heads >= INT32_MAX) return PKV_ERR_ARG;
+  const int keys = sp.rows == pkv::CrossRows::k256 && cache->dtype != PKV_FP8_E4M3 ? 128 : 64;
   pkv::CrossMaps maps;
-  if (!encode_pool_map(&maps.k, cache, cache->k_cache) ||
-      !encode_pool_map(&maps.v, cache, cache->v_cache))
+  if (!encode_page_map(&maps.k, cache, cache->k_cache, keys) ||
+      !encode_page_map(&maps.v, cache, cache->v_cache, keys))
     return PKV_ERR_CUDA;
   if (cache->dtype == PKV_FP8_E4M3)
     return pkv_launch_cross_tc_fp8(p, cache->io_dtype, num_seqs, sp.rows, maps, stream);

@@ -31,6 +31,7 @@ struct CrossParams {
   const int32_t* tables;    // [S][max_blocks]
   int max_blocks;
   const int32_t* lens;      // [S]
+  int num_seqs;
   int max_len;
   float qscale;             // scale * log2(e)
   int parts, part;          // parts of the states, positions in each

@@ -8,12 +8,17 @@
 // Roles:
 //   warps 0 .. 4 QT - 1  softmax, a thread per row (= tensor-memory lane): the
 //        S row to registers, running maximum and sum, P over S's own columns;
-//   producer warp        TMA boxes of the table's pages into one ring of K
-//        and V tiles, in the order of their use;
-//   MMA warp             S = Q.K^T and O += P.V (P from tensor memory), all
-//        tiles' products from one thread, so that they run in the order of
-//        issue: S(j + NS) is issued right behind P.V(j), whose P it overwrites;
-//   FP8 pools: four converter warps between raw codes and the ring.
+//   producer warps, one for K and one for V  the table's pages by TMA, a copy
+//        per page, into a ring each (a copy takes its thread about 90 cycles,
+//        and a tile has up to 8 pages of 16 rows);
+//   MMA warps, one per row tile  S = Q.K^T and O += P.V (P from tensor
+//        memory), all of a tile's products from one elected thread, so that
+//        they run in the order of issue: S(j + NS) is issued right behind
+//        P.V(j), whose P it overwrites.  The issuing thread's own chain of
+//        instructions is what limits it (about as long as the products), so
+//        each row tile has one, nothing in it is done by the whole warp, and
+//        ring slots and phases are counted along, not computed;
+//   FP8 pools: four converter warps between rings of codes and the others.
 // The running maximum is raised lazily (by more than 2^kSlack, so that O is
 // rescaled rarely); sums, maxima and O are float32.  P is rounded to the
 // operand type: bf16 for bf16 pools (2^-8 of each weight at most, the step
@@ -44,32 +49,40 @@ struct CrossTcCfg {
   static constexpr int kRows = SPLIT ? 32 : QT * 128;
   static constexpr int kLaneKeys = SPLIT ? kKeys / 4 : kKeys;  // keys of a lane
   static constexpr int kHalves = D / 64;                    // 128-byte column blocks
-  static constexpr int kHalfBytes = kKeys * 128;            // of a K or V tile
-  static constexpr int kTileBytes = kHalves * kHalfBytes;
+  // K and V tiles: groups of 8 keys, each with its 128-byte column blocks
+  // behind one another (1 KiB swizzle atoms).  The order is that of one copy
+  // per page: a page's box is {64 elements, 8 rows, column blocks, groups}.
+  static constexpr int kGroupBytes = kHalves * 1024;
+  static constexpr int kTileBytes = kKeys / 8 * kGroupBytes;
   static constexpr int kQHalfBytes = 128 * 128;
   static constexpr int kQBytes = kHalves * kQHalfBytes;     // one row tile
   static constexpr int kRawBytes = KV8 ? kKeys * D : 0;     // one tile of codes
-  static constexpr int kRawSlots = KV8 ? (QT == 2 ? 4 : 2) : 0;
-  // Ring slots: what one block (QT 1: two) leaves of an SM's shared memory.
-  static constexpr int kAvail = (QT == 2 ? 225 : 112) * 1024 - QT * kQBytes - kRawSlots * kRawBytes;
+  static constexpr int kRawSlots = KV8 ? 2 : 0;             // of K, and of V
+  // Ring slots of K and V: what one block (QT 1: two) leaves of an SM's shared
+  // memory, at most 8.  A V tile is held longer (until P.V).
+  static constexpr int kAvail =
+      (QT == 2 ? 225 : 112) * 1024 - QT * kQBytes - 2 * kRawSlots * kRawBytes;
   static constexpr int kSlots = kAvail / kTileBytes > 8 ? 8 : kAvail / kTileBytes;
+  static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;
   static constexpr int kSoftmaxWarps = 4 * QT;
-  static constexpr int kProducerWarp = kSoftmaxWarps;
-  static constexpr int kMmaWarp = kSoftmaxWarps + 1;
-  static constexpr int kConvWarp = kSoftmaxWarps + 2;
+  static constexpr int kKeyWarp = kSoftmaxWarps;            // producers
+  static constexpr int kValueWarp = kSoftmaxWarps + 1;
+  static constexpr int kMmaWarp = kSoftmaxWarps + 2;        // one per row tile
+  static constexpr int kConvWarp = kMmaWarp + QT;
   static constexpr int kConvThreads = KV8 ? 128 : 0;
   static constexpr int kThreads = kConvWarp * 32 + kConvThreads;
-  static constexpr int kRingOff = QT * kQBytes;
-  static constexpr int kRawOff = kRingOff + kSlots * kTileBytes;
-  static constexpr int kBarOff = kRawOff + kRawSlots * kRawBytes;
-  static constexpr int kNumBars = 2 * kSlots + 2 * kRawSlots + QT * (2 * kBufs + 2) + 2;
+  static constexpr int kKRingOff = QT * kQBytes;
+  static constexpr int kVRingOff = kKRingOff + kKSlots * kTileBytes;
+  static constexpr int kRawOff = kVRingOff + kVSlots * kTileBytes;  // K, then V
+  static constexpr int kBarOff = kRawOff + 2 * kRawSlots * kRawBytes;
+  static constexpr int kNumBars = 2 * kSlots + 4 * kRawSlots + QT * (2 * kBufs + 3) + 1;
   static constexpr int kTmemOff = kBarOff + kNumBars * 8;
   static constexpr int kFlagOff = kTmemOff + 4;
   static constexpr int kSmemBytes = kTmemOff + 16;
   // SPLIT, at the end: the lanes' (m, l) in Q's memory, their O in the ring's,
   // rows padded by 16 bytes
   static constexpr int kORow = D + 4;
-  static_assert(!SPLIT || (QT == 1 && 4 * 32 * kORow * 4 <= kBarOff - kRingOff), "O in the ring");
+  static_assert(!SPLIT || (QT == 1 && 4 * 32 * kORow * 4 <= kBarOff - kKRingOff), "O in the ring");
   static constexpr uint32_t kTileCols = 256;
   static constexpr uint32_t kTmemCols = QT * kTileCols;
   static constexpr uint32_t kOCol = kBufs * kKeys;
@@ -81,15 +94,178 @@ struct CrossTcCfg {
   // P stays at or below 2^(kSlack + kBias): 2^15 in fp16.
   static constexpr float kSlack = 8.f, kBias = kBf16 ? 0.f : 7.f;
   static_assert(kOCol + D <= kTileCols, "tensor memory");
-  static_assert(kSlots >= 4, "ring");
+  static_assert(kKSlots >= 1 && kVSlots >= 1, "rings");
   static_assert(kSmemBytes <= (QT == 2 ? 227 : 113) * 1024, "shared memory");
   // never more blocks on an SM than its 512 tensor-memory columns serve
   static_assert(QT == 1 || 2 * kSmemBytes > 228 * 1024, "blocks per SM");
   static_assert(QT == 2 || 3 * kSmemBytes > 228 * 1024, "blocks per SM");
 };
 
+// A thread's Q row, from global memory into row rr of a 128-row tile in the
+// 128-byte-swizzled operand layout; returns the factor that makes its
+// products scores in base-2 units (never negative: the sign of the scale goes
+// into Q, exactly, so that the largest score has the largest product).
+template <typename T, int D, bool KV8>
+__device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const T* row,
+                                           unsigned char* tile, int rr) {
+  const uint4* src = reinterpret_cast<const uint4*>(row);
+  bool neg = p.qscale < 0.f;
+  float shrink = 1.f, qscale = fabsf(p.qscale);
+  if constexpr (KV8) {
+    qscale *= fabsf(p.k_scale[kvh]);
+    neg = neg != (p.k_scale[kvh] < 0.f);
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      // bf16 rows enter as fp16; one that reaches 2^15 is first scaled by a
+      // power of two (exact), undone in the row's factor
+      float amax = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = src[i];
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[k] << 16)),
+                                   fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
+      }
+      if (amax >= 32768.f && amax <= 3.0e38f) {
+        int e = 0;
+        frexpf(amax, &e);
+        shrink = ldexpf(1.f, 15 - e);
+        qscale = ldexpf(qscale, e - 15);
+      }
+    }
+  }
+  // A zero scale becomes zero queries, so that hidden keys stay at -inf.
+  const bool none = qscale == 0.f;
+  if (none) qscale = 1.f;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {  // (all loads in flight)
+    const uint4 x = none ? make_uint4(0u, 0u, 0u, 0u) : src[i];
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (KV8 && std::is_same<T, __nv_bfloat16>::value)
+        w[k] = pack_pair<__half>(__uint_as_float(w[k] << 16) * shrink,
+                                 __uint_as_float(w[k] & 0xFFFF0000u) * shrink);
+      if (neg) w[k] ^= 0x80008000u;
+    }
+    *reinterpret_cast<uint4*>(tile + (i >> 3) * 128 * 128 + rr * 128 +
+                              (((i & 7) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return qscale;
+}
+
+// A tile of KEYS rows of 128 codes to fp16, both in the 128-byte-swizzled
+// layout, by THREADS threads; rows from `valid` on become zeros.
+template <int KEYS, int THREADS>
+__device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned char* dst, int valid,
+                                           int thread) {
+#pragma unroll
+  for (int u = 0; u < KEYS * 8 / THREADS; ++u) {
+    const int unit = thread + u * THREADS;
+    const int row = unit >> 3, ch = unit & 7;
+    uint4 a = make_uint4(0u, 0u, 0u, 0u), z = a;
+    if (row < valid) {
+      const uint4 x = *reinterpret_cast<const uint4*>(raw + row * 128 + ((ch ^ (row & 7)) << 4));
+      e4m3x4_to_f16x4(x.x, a.x, a.y);
+      e4m3x4_to_f16x4(x.y, a.z, a.w);
+      e4m3x4_to_f16x4(x.z, z.x, z.y);
+      e4m3x4_to_f16x4(x.w, z.z, z.w);
+    }
+    const int c2 = (ch & 3) * 2;
+    unsigned char* drow = dst + (row >> 3) * 2048 + (ch >> 2) * 1024 + (row & 7) * 128;
+    *reinterpret_cast<uint4*>(drow + ((c2 ^ (row & 7)) << 4)) = a;
+    *reinterpret_cast<uint4*>(drow + (((c2 + 1) ^ (row & 7)) << 4)) = z;
+  }
+}
+
 struct CrossMaps {
   CUtensorMap k, v;
+};
+
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
+// Place in a ring of N slots: the slot and the parity of its current phase.
+template <int N>
+struct RingPos {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Values past the states are anything, and NaN times a zero weight would
+// reach O: clears the rows of a value tile from `valid` to the end of their
+// page (pages wholly past the states came as zeros; block sizes are powers of
+// two, and a tile holds whole pages or lies inside one).
+template <int D, int KEYS>
+__device__ __forceinline__ void clear_tail(unsigned char* v, int valid, int block_size, int thread,
+                                           int threads) {
+  const int rb = min(block_size, KEYS), stop = (valid + rb - 1) & ~(rb - 1);
+  for (int e = thread; e < (stop - valid) * (D / 8); e += threads) {
+    const int row = valid + e / (D / 8), ch = e % (D / 8);
+    *reinterpret_cast<uint4*>(v + (row >> 3) * (D / 64 * 1024) + (ch >> 3) * 1024 +
+                              (row & 7) * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+}
+
+// One page (or the part of it in a tile) of a pool, see kGroupBytes: coordinates
+// are the first group of 8 rows and the page, block * kv_heads + kv_head.
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, int group,
+                                              int page, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(page), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+// The copies of a tile of KEYS positions, for one thread: the table entries
+// of its pages, read some tiles ahead (as they are: nothing waits for them
+// before they are used), and the copies.
+template <int KEYS>
+struct PageTile {
+  static constexpr int kMax = KEYS / 8;  // pages of a tile at most
+  int entry[kMax];
+
+  // Entries of positions pos .. pos + KEYS - 1 of a table row; positions from
+  // `end` on have none (-1).
+  __device__ __forceinline__ void look(const int32_t* trow, int pos, int end, int shift) {
+    const int step = min(1 << shift, KEYS);
+#pragma unroll
+    for (int x = 0; x < kMax; ++x) {
+      if (x * step >= KEYS) break;
+      const int at = pos + x * step;
+      entry[x] = -1;
+      if (at < end) entry[x] = trow[at >> shift];
+    }
+  }
+  // An entry out of range becomes a page past the pool, which reads as zeros.
+  __device__ __forceinline__ void copy(const CrossParams& p, uint32_t dst, const CUtensorMap* map,
+                                       int pos, int kvh, int shift, int group_bytes, uint32_t bar,
+                                       uint64_t policy) const {
+    const int step = min(1 << shift, KEYS), group = (pos & ((1 << shift) - 1)) >> 3;
+    const int blocks = (int)p.num_blocks;
+#pragma unroll
+    for (int x = 0; x < kMax; ++x) {
+      if (x * step >= KEYS) break;
+      const int page = (unsigned)entry[x] < (unsigned)blocks ? entry[x] * p.kv_heads + kvh
+                                                             : blocks * p.kv_heads;
+      tma_load_page(dst + x * (step >> 3) * group_bytes, map, group, page, bar, policy);
+    }
+  }
 };
 
 // 16 consecutive 32-bit columns of this thread's lane, waited for.
@@ -117,7 +293,8 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
                 const __grid_constant__ CUtensorMap tmv) {
   using Cfg = CrossTcCfg<T, D, QT, KV8, SPLIT>;
   using Op = typename Cfg::Op;
-  constexpr int KT = Cfg::kKeys, NS = Cfg::kBufs, SLOTS = Cfg::kSlots, RAW = Cfg::kRawSlots;
+  constexpr int KT = Cfg::kKeys, NS = Cfg::kBufs;
+  constexpr int NK = Cfg::kKSlots, NV = Cfg::kVSlots, RAW = Cfg::kRawSlots;
   constexpr int LK = Cfg::kLaneKeys;
   extern __shared__ __align__(1024) unsigned char cross_smem[];
   unsigned char* const smem = cross_smem;
@@ -162,11 +339,17 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
 
   // ---- barriers, tensor memory, Q ---------------------------------------------
   const uint32_t bar0 = sbase + Cfg::kBarOff;
-  auto full = [&](int i) { return bar0 + 8u * i; };                     // ring slot holds a tile
-  auto empty = [&](int i) { return bar0 + 8u * (SLOTS + i); };          // its products are done
-  auto raw_full = [&](int i) { return bar0 + 8u * (2 * SLOTS + i); };   // FP8: codes landed
-  auto raw_empty = [&](int i) { return bar0 + 8u * (2 * SLOTS + RAW + i); };
-  constexpr int B1 = 2 * SLOTS + 2 * RAW;
+  // Rings: a slot holds a tile; its products are done.
+  auto k_full = [&](int i) { return bar0 + 8u * i; };
+  auto k_empty = [&](int i) { return bar0 + 8u * (NK + i); };
+  auto v_full = [&](int i) { return bar0 + 8u * (2 * NK + i); };
+  auto v_empty = [&](int i) { return bar0 + 8u * (2 * NK + NV + i); };
+  // FP8: codes landed, codes widened; which: 0 keys, 1 values.
+  auto raw_full = [&](int which, int i) { return bar0 + 8u * (2 * NK + 2 * NV + which * RAW + i); };
+  auto raw_empty = [&](int which, int i) {
+    return bar0 + 8u * (2 * NK + 2 * NV + (2 + which) * RAW + i);
+  };
+  constexpr int B1 = 2 * NK + 2 * NV + 4 * RAW;
   auto s_full = [&](int t, int i) { return bar0 + 8u * (B1 + t * NS + i); };
   auto p_full = [&](int t, int i) { return bar0 + 8u * (B1 + QT * NS + t * NS + i); };
   // P.V(j) done, every j (two S buffers only: with one, S(j + 1) says so), and
@@ -174,18 +357,24 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
   auto o_done = [&](int t) { return bar0 + 8u * (B1 + 2 * QT * NS + t); };
   auto o_last = [&](int t) { return bar0 + 8u * (B1 + 2 * QT * NS + QT + t); };
   const uint32_t q_full = bar0 + 8u * (B1 + 2 * QT * NS + 2 * QT);
-  const uint32_t drain = q_full + 8u;
+  auto drain = [&](int t) { return q_full + 8u * (1 + t); };
   auto tile_warps = [&](int t) {  // softmax warps with rows of row tile t
     return SPLIT ? 4 : min(4, max(0, (nr - t * 128 + 31) / 32));
   };
   if (tid == 0) {
-    for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(full(i), KV8 ? Cfg::kConvThreads : 1);
-      mbar_init(empty(i), 1);
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(k_full(i), KV8 ? Cfg::kConvThreads : 1);
+      mbar_init(k_empty(i), row_n);
+    }
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(v_full(i), KV8 ? Cfg::kConvThreads : 1);
+      mbar_init(v_empty(i), row_n);
     }
     for (int i = 0; i < RAW; ++i) {
-      mbar_init(raw_full(i), 1);
-      mbar_init(raw_empty(i), Cfg::kConvThreads);
+      for (int which = 0; which < 2; ++which) {
+        mbar_init(raw_full(which, i), 1);
+        mbar_init(raw_empty(which, i), Cfg::kConvThreads);
+      }
     }
     for (int t = 0; t < QT; ++t) {
       for (int i = 0; i < NS; ++i) {
@@ -194,9 +383,9 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       }
       mbar_init(o_done(t), 1);
       mbar_init(o_last(t), 1);
+      mbar_init(drain(t), 1);
     }
     mbar_init(q_full, (tile_warps(0) + (QT > 1 ? tile_warps(QT - 1) : 0)) * 32);
-    mbar_init(drain, 1);
     fence_mbar_init();
     *reinterpret_cast<int*>(smem + Cfg::kFlagOff) = 0;
   }
@@ -212,59 +401,13 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
   const uint32_t tmem = *slot;
   bool failed = false;
   // Softmax thread: lane rr of row tile t, row r of the block.  It brings its
-  // Q row into the 128-byte-swizzled operand layout while the first tiles are
-  // on their way; the sign of the scale goes into Q (exact), so that the
-  // largest score has the largest product.
+  // Q row while the first tiles are on their way.
   const int t = warp >> 2, rr = (warp & 3) * 32 + lane, r = SPLIT ? lane : t * 128 + rr;
   const bool softmax = warp < Cfg::kSoftmaxWarps && (warp & 3) < tile_warps(t);
-  float qscale = fabsf(p.qscale);
+  float qscale = 1.f;
   if (softmax) {
     unsigned char* qt = smem + t * Cfg::kQBytes;
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
-                                                      row_at(min(r, nr - 1)));
-    bool neg = p.qscale < 0.f;
-    float shrink = 1.f;
-    if constexpr (KV8) {
-      qscale *= fabsf(p.k_scale[kvh]);
-      neg = neg != (p.k_scale[kvh] < 0.f);
-      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        // bf16 rows enter as fp16; one that reaches 2^15 is first scaled by
-        // a power of two (exact), undone in the row's factor
-        float amax = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = src[i];
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[k] << 16)),
-                                     fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
-        }
-        if (amax >= 32768.f && amax <= 3.0e38f) {
-          int e = 0;
-          frexpf(amax, &e);
-          shrink = ldexpf(1.f, 15 - e);
-          qscale = ldexpf(qscale, e - 15);
-        }
-      }
-    }
-    // A zero scale becomes zero queries, so that hidden keys stay at -inf.
-    const bool none = qscale == 0.f;
-    if (none) qscale = 1.f;
-#pragma unroll 8
-    for (int i = 0; i < D / 8; ++i) {
-      const uint4 x = none ? make_uint4(0u, 0u, 0u, 0u) : src[i];
-      uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if constexpr (KV8 && std::is_same<T, __nv_bfloat16>::value)
-          w[k] = pack_pair<__half>(__uint_as_float(w[k] << 16) * shrink,
-                                   __uint_as_float(w[k] & 0xFFFF0000u) * shrink);
-        if (neg) w[k] ^= 0x80008000u;
-      }
-      *reinterpret_cast<uint4*>(qt + (i >> 3) * Cfg::kQHalfBytes + rr * 128 +
-                                (((i & 7) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    qscale = bring_row<T, D, KV8>(p, kvh, static_cast<const T*>(p.q) + row_at(min(r, nr - 1)), qt, rr);
     fence_proxy_async_smem();
     mbar_arrive(q_full);
     // Every block checks the whole table row, so that all parts agree.  A bad
@@ -276,196 +419,148 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       if (e < 0 || (int64_t)e >= p.num_blocks) *bad_flag = 1;
     }
   }
-  // Place of K and V tiles in the order of use: the first NS K tiles, then
-  // V(j) and K(j + NS) in turn, then the V tiles that are left.
-  const int pre = min(NS, n_tiles);
-  auto seq_k = [&](int j) { return j < pre ? j : 2 * j - pre + 1; };
-  auto seq_v = [&](int j) { return j < n_tiles - pre ? pre + 2 * j : n_tiles + j; };
-
-  if (warp == Cfg::kProducerWarp) {
-    // ---- producer -----------------------------------------------------------
-    const uint64_t policy = row_tiles > 1 ? policy_evict_last() : policy_evict_first();
-    const int rb = b < 16 ? b : 16;          // rows per box
-    const int boxes = KT / rb;
-    // Table entries, a warp's worth of boxes at a time and one such group
-    // ahead, so that no copy waits for its own table load: lane x of group g
-    // holds the block of box x % boxes of tile g * per + x / boxes.  Values run
-    // at most two tiles behind keys, so the group before is kept for them.
-    const int per = 32 / boxes, shift = 31 - __clz(b);
-    const int oob = (int)p.num_blocks;  // reads as zeros (as do too large entries)
-    auto group = [&](int g) {
-      const int pos = lo + (g * 32 + lane) * rb;
-      const int e = pos < hi ? trow[pos >> shift] : oob;
-      return e < 0 ? oob : e;
-    };
-    int at = 0, before = oob, now = group(0), next = group(1);
-    constexpr int N = KV8 ? RAW : SLOTS;
-    constexpr int BYTES = KV8 ? Cfg::kRawBytes : Cfg::kTileBytes;
-    const uint32_t ring = sbase + (KV8 ? Cfg::kRawOff : Cfg::kRingOff);
-    int issued = 0;
-    for (int i = 0; i < 2 * n_tiles; ++i) {
-      // tile i of the order above
-      const bool key = i < pre || (i < 2 * n_tiles - pre && ((i - pre) & 1));
-      const int j = i < pre ? i
-                    : i < 2 * n_tiles - pre ? ((i - pre) >> 1) + (key ? pre : 0)
-                                            : i - n_tiles;
-      const int sl = i % N;
-      const uint32_t fb = KV8 ? raw_full(sl) : full(sl);
-      if (i >= N) {
-        const bool ok = mbar_wait(KV8 ? raw_empty(sl) : empty(sl), (uint32_t)((i / N - 1) & 1));
-        if (__any_sync(kFullMask, !ok)) {
+  if (warp == Cfg::kKeyWarp || warp == Cfg::kValueWarp) {
+    // ---- producers ----------------------------------------------------------
+    // One elected thread each: a copy's operands are uniform registers, and
+    // lanes that each issue one take turns at it.  The pages of two tiles
+    // ahead are read meanwhile.
+    if (elect_one()) {
+      const bool key = warp == Cfg::kKeyWarp;
+      const CUtensorMap* map = key ? &tmk : &tmv;
+      const uint64_t policy = row_tiles > 1 ? policy_evict_last() : policy_evict_first();
+      const int shift = 31 - __clz(b);
+      const int slots = KV8 ? RAW : key ? NK : NV;
+      constexpr int BYTES = KV8 ? Cfg::kRawBytes : Cfg::kTileBytes;
+      constexpr int GROUP = KV8 ? 1024 : Cfg::kGroupBytes;
+      const uint32_t ring = sbase + (KV8   ? Cfg::kRawOff + (key ? 0 : RAW * BYTES)
+                                     : key ? Cfg::kKRingOff
+                                           : Cfg::kVRingOff);
+      const uint32_t bars = KV8 ? raw_full(key ? 0 : 1, 0) : key ? k_full(0) : v_full(0);
+      const uint32_t frees = KV8 ? raw_empty(key ? 0 : 1, 0) : key ? k_empty(0) : v_empty(0);
+      PageTile<KT> now, next;
+      now.look(trow, lo, hi, shift);
+      next.look(trow, lo + KT, hi, shift);
+      int slot = 0, issued = 0;
+      uint32_t phase = 0;
+      for (; issued < n_tiles; ++issued) {
+        if (issued >= slots && !mbar_wait(frees + 8u * slot, phase ^ 1u)) {
           failed = true;
           break;
         }
-      }
-      if (lane == 0) mbar_arrive_expect_tx(fb, BYTES);
-      __syncwarp();
-      const int g = j / per;
-      if (g > at) {  // (keys lead)
-        before = now;
+        const uint32_t fb = bars + 8u * slot;
+        mbar_arrive_expect_tx(fb, BYTES);
+        now.copy(p, ring + slot * BYTES, map, lo + issued * KT, kvh, shift, GROUP, fb, policy);
         now = next;
-        next = group(++at + 1);
-      }
-      const int pb = __shfl_sync(kFullMask, g == at ? now : before, (j % per) * boxes + lane);
-      if (lane < boxes) {
-        const int row = (lo + j * KT + lane * rb) & (b - 1);
-        const uint32_t dst = ring + sl * BYTES + lane * rb * 128;
-        const CUtensorMap* map = key ? &tmk : &tmv;
-        if constexpr (KV8) {
-          tma_load_4d(dst, map, 0, row, kvh, pb, fb, policy);
-        } else {
-#pragma unroll
-          for (int h = 0; h < Cfg::kHalves; ++h)
-            tma_load_4d(dst + h * Cfg::kHalfBytes, map, h * 64, row, kvh, pb, fb, policy);
+        next.look(trow, lo + (issued + 2) * KT, hi, shift);
+        if (++slot == slots) {
+          slot = 0;
+          phase ^= 1u;
         }
       }
-      issued = i + 1;
+      // Copies that may not have been waited for (another role stopped).
+      for (int i = max(0, issued - slots); i < issued; ++i)
+        mbar_wait(bars + 8u * (i % slots), (uint32_t)((i / slots) & 1), kWaitLimitNs / 8);
+      if (failed) set_error(p.err, PKV_DEV_TIMEOUT);
+      failed = false;
     }
-    // Copies that may not have been waited for (another role stopped).
-    for (int i = max(0, issued - N); i < issued; ++i)
-      mbar_wait(KV8 ? raw_full(i % N) : full(i % N), (uint32_t)((i / N) & 1), kWaitLimitNs / 8);
-  } else if (warp == Cfg::kMmaWarp) {
-    // ---- MMA issuer -----------------------------------------------------------
-    auto wait = [&](uint32_t bar, int phase) {
-      const bool ok = mbar_wait(bar, (uint32_t)(phase & 1));
-      return !__any_sync(kFullMask, !ok);
-    };
-    const uint64_t kdesc = smem_desc_sw128(sbase + Cfg::kRingOff, 16, 1024);
-    const uint64_t vdesc =
-        smem_desc_sw128(sbase + Cfg::kRingOff, Cfg::kHalves > 1 ? Cfg::kHalfBytes : 1024, 1024);
-    const uint64_t qdesc = smem_desc_sw128(sbase, 16, 1024);
-    auto issue_s = [&](int tt, int j) {
-      const uint32_t d = tmem + tt * Cfg::kTileCols + (j % NS) * KT;
-      const uint64_t kb = kdesc + (uint64_t)(((seq_k(j) % SLOTS) * Cfg::kTileBytes) >> 4);
-      const uint64_t qb = qdesc + (uint64_t)((tt * Cfg::kQBytes) >> 4);
+    __syncwarp();
+  } else if (warp >= Cfg::kMmaWarp && warp < Cfg::kConvWarp) {
+    // ---- MMA issuers ----------------------------------------------------------
+    const int tt = warp - Cfg::kMmaWarp;
+    if (tt < row_n && elect_one()) {
+      const uint32_t base = tmem + tt * Cfg::kTileCols;
+      const uint64_t kdesc = smem_desc_sw128(sbase + Cfg::kKRingOff, 16, Cfg::kGroupBytes);
+      const uint64_t vdesc = smem_desc_sw128(sbase + Cfg::kVRingOff, 1024, Cfg::kGroupBytes);
+      const uint64_t qdesc = smem_desc_sw128(sbase + tt * Cfg::kQBytes, 16, 1024);
+      RingPos<NK> ka;
+      RingPos<NV> va;
+      bool ok = mbar_wait(q_full, 0);
+      auto scores = [&](int buf) {
+        ok = ok && mbar_wait(k_full(ka.slot), ka.phase);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t kb = kdesc + (uint64_t)((ka.slot * Cfg::kTileBytes) >> 4);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        tc_mma_ss(d, qb + (uint64_t)((((kk >> 2) * Cfg::kQHalfBytes) + (kk & 3) * 32) >> 4),
-                  kb + (uint64_t)((((kk >> 2) * Cfg::kHalfBytes) + (kk & 3) * 32) >> 4),
-                  Cfg::kIdescS, kk > 0 ? 1u : 0u);
-      tc_commit(s_full(tt, j % NS));
-    };
-    bool ok = wait(q_full, 0);
-    auto all_s = [&](int j) {  // S(j) of every row tile, outside the main loop
-      const int i = seq_k(j);
-      ok = ok && wait(full(i % SLOTS), i / SLOTS);
-      if (!ok) return;
-      tc_fence_after();
-      if (lane == 0) {
-        for (int tt = 0; tt < row_n; ++tt) issue_s(tt, j);
-        tc_commit(empty(i % SLOTS));
-      }
-      __syncwarp();
-    };
-    for (int j = 0; j < pre; ++j) all_s(j);
-    for (int j = 0; j < n_tiles && ok; ++j) {
-      const int vi = seq_v(j);
-      const bool more = j + NS < n_tiles;
-      const int ki = more ? seq_k(j + NS) : 0;
-      ok = wait(full(vi % SLOTS), vi / SLOTS);
-      if (!ok) break;
-      if constexpr (!KV8) {
-        // Values past the states are anything (NaN times a zero weight would
-        // reach O): the rows up to the end of their box are cleared here.
-        const int valid = hi - lo - j * KT;
-        if (valid < KT) {
-          const int rb = b < 16 ? b : 16, end = (valid + rb - 1) / rb * rb;
-          unsigned char* v = smem + Cfg::kRingOff + (vi % SLOTS) * Cfg::kTileBytes;
-          for (int e = lane; e < (end - valid) * 8 * Cfg::kHalves; e += 32) {
-            const int row = valid + e / (8 * Cfg::kHalves), rest = e % (8 * Cfg::kHalves);
-            *reinterpret_cast<uint4*>(v + (rest >> 3) * Cfg::kHalfBytes + row * 128 +
-                                      (rest & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-      }
-      for (int tt = 0; tt < row_n && ok; ++tt) {
-        ok = wait(p_full(tt, j % NS), j / NS);
-        if (ok && more && tt == 0) ok = wait(full(ki % SLOTS), ki / SLOTS);
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_ss(base + buf * KT,
+                    qdesc + (uint64_t)((((kk >> 2) * Cfg::kQHalfBytes) + (kk & 3) * 32) >> 4),
+                    kb + (uint64_t)((((kk >> 2) * 1024) + (kk & 3) * 32) >> 4),
+                    Cfg::kIdescS, kk > 0 ? 1u : 0u);
+        tc_commit(s_full(tt, buf));
+        tc_commit(k_empty(ka.slot));
+        ka.next();
+      };
+      for (int j = 0; j < min(NS, n_tiles); ++j) scores(j);
+      int buf = 0;
+      uint32_t pphase = 0;
+      for (int j = 0; j < n_tiles && ok; ++j) {
+        ok = mbar_wait(v_full(va.slot), va.phase) && mbar_wait(p_full(tt, buf), pphase);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t base = tmem + tt * Cfg::kTileCols;
-          const uint32_t pa = base + (j % NS) * KT;
-          const uint64_t vb = vdesc + (uint64_t)(((vi % SLOTS) * Cfg::kTileBytes) >> 4);
+        const uint64_t vb = vdesc + (uint64_t)((va.slot * Cfg::kTileBytes) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            tc_mma_ts(base + Cfg::kOCol, pa + 8 * kk, vb + 128 * kk, Cfg::kIdescPV,
-                      (j > 0 || kk > 0) ? 1u : 0u);
-          if (NS > 1) tc_commit(o_done(tt));
-          if (j == n_tiles - 1) tc_commit(o_last(tt));
-          if (tt == row_n - 1) tc_commit(empty(vi % SLOTS));
-          if (more) {
-            issue_s(tt, j + NS);
-            if (tt == row_n - 1) tc_commit(empty(ki % SLOTS));
-          }
+        for (int kk = 0; kk < KT / 16; ++kk)
+          tc_mma_ts(base + Cfg::kOCol, base + buf * KT + 8 * kk, vb + (2 * Cfg::kGroupBytes >> 4) * kk, Cfg::kIdescPV,
+                    (j > 0 || kk > 0) ? 1u : 0u);
+        if (NS > 1) tc_commit(o_done(tt));
+        if (j == n_tiles - 1) tc_commit(o_last(tt));
+        tc_commit(v_empty(va.slot));
+        va.next();
+        if (j + NS < n_tiles) scores(buf);
+        if (++buf == NS) {
+          buf = 0;
+          pphase ^= 1u;
         }
-        __syncwarp();
       }
+      failed = !ok;
+      // every MMA has completed before the tensor memory is released
+      tc_commit(drain(tt));
+      mbar_wait(drain(tt), 0);
+      if (failed) set_error(p.err, PKV_DEV_TIMEOUT);
+      failed = false;
     }
-    failed = !ok;
-    // every MMA has completed before the tensor memory is released
-    if (lane == 0) tc_commit(drain);
     __syncwarp();
-    mbar_wait(drain, 0);
   } else if (KV8 && warp >= Cfg::kConvWarp) {
     // ---- converters: codes to fp16, one slot of the ring at a time --------------
     if constexpr (KV8) {
       const int ct = tid - Cfg::kConvWarp * 32;
-      for (int i = 0; i < 2 * n_tiles; ++i) {
-        const int rs = i % RAW, sl = i % SLOTS;
-        bool ok = mbar_wait(raw_full(rs), (uint32_t)((i / RAW) & 1));
-        if (ok && i >= SLOTS) ok = mbar_wait(empty(sl), (uint32_t)((i / SLOTS - 1) & 1));
+      // In the order of use: the first NS K tiles, then V(j) and K(j + NS).
+      RingPos<RAW> kr, vr;
+      RingPos<NK> ka;
+      RingPos<NV> va;
+      for (int kj = 0, vj = 0; vj < n_tiles;) {
+        const bool key = kj < n_tiles && kj < vj + NS;
+        bool ok;
+        if (key) {
+          ok = mbar_wait(raw_full(0, kr.slot), kr.phase);
+          if (ok && kj >= NK) ok = mbar_wait(k_empty(ka.slot), ka.phase ^ 1u);
+        } else {
+          ok = mbar_wait(raw_full(1, vr.slot), vr.phase);
+          if (ok && vj >= NV) ok = mbar_wait(v_empty(va.slot), va.phase ^ 1u);
+        }
         if (__any_sync(kFullMask, !ok)) {
           failed = true;
           break;
         }
-        const bool key = i < pre || (i < 2 * n_tiles - pre && ((i - pre) & 1));
-        const int j = i < 2 * n_tiles - pre ? (i - pre) >> 1 : i - n_tiles;  // (values)
-        const int valid = key ? KT : hi - lo - j * KT;
-        const unsigned char* raw = smem + Cfg::kRawOff + rs * Cfg::kRawBytes;
-        unsigned char* dst = smem + Cfg::kRingOff + sl * Cfg::kTileBytes;
-#pragma unroll
-        for (int u = 0; u < KT * 8 / Cfg::kConvThreads; ++u) {
-          const int unit = ct + u * Cfg::kConvThreads;
-          const int row = unit >> 3, ch = unit & 7;
-          uint4 a = make_uint4(0u, 0u, 0u, 0u), z = a;
-          if (row < valid) {
-            const uint4 x = *reinterpret_cast<const uint4*>(raw + row * 128 + ((ch ^ (row & 7)) << 4));
-            e4m3x4_to_f16x4(x.x, a.x, a.y);
-            e4m3x4_to_f16x4(x.y, a.z, a.w);
-            e4m3x4_to_f16x4(x.z, z.x, z.y);
-            e4m3x4_to_f16x4(x.w, z.z, z.w);
-          }
-          const int c2 = (ch & 3) * 2;
-          unsigned char* drow = dst + (ch >> 2) * Cfg::kHalfBytes + row * 128;
-          *reinterpret_cast<uint4*>(drow + ((c2 ^ (row & 7)) << 4)) = a;
-          *reinterpret_cast<uint4*>(drow + (((c2 + 1) ^ (row & 7)) << 4)) = z;
-        }
+        const unsigned char* raw =
+            smem + Cfg::kRawOff + (key ? kr.slot : RAW + vr.slot) * Cfg::kRawBytes;
+        unsigned char* dst = smem + (key ? Cfg::kKRingOff + ka.slot * Cfg::kTileBytes
+                                         : Cfg::kVRingOff + va.slot * Cfg::kTileBytes);
+        widen_tile<KT, Cfg::kConvThreads>(raw, dst, key ? KT : hi - lo - vj * KT, ct);
         fence_proxy_async_smem();
-        mbar_arrive(full(sl));
-        mbar_arrive(raw_empty(rs));
+        if (key) {
+          mbar_arrive(k_full(ka.slot));
+          mbar_arrive(raw_empty(0, kr.slot));
+          kr.next();
+          ka.next();
+          ++kj;
+        } else {
+          mbar_arrive(v_full(va.slot));
+          mbar_arrive(raw_empty(1, vr.slot));
+          vr.next();
+          va.next();
+          ++vj;
+        }
       }
     }
   } else if (softmax) {
@@ -538,6 +633,16 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       } else {
         tmem_st32(sp, pk);
       }
+      if (!KV8 && hi - lo - j * KT < KT) {  // (the last tile)
+        ok = mbar_wait(v_full(j % NV), (uint32_t)((j / NV) & 1));
+        if (__any_sync(kFullMask, !ok)) {
+          ok = false;
+          break;
+        }
+        // (both row tiles do it: the same zeros)
+        clear_tail<D, KT>(smem + Cfg::kVRingOff + (j % NV) * Cfg::kTileBytes, hi - lo - j * KT, b, rr,
+                          32 * tile_warps(t));
+      }
       // P.V(j - 1) has been added to O before O or its factor changes.  With
       // one S buffer it was, before S(j) was made; with two, every phase is
       // waited for in turn.
@@ -576,7 +681,7 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
     if constexpr (SPLIT) {
       // Joins the quarters: O * 2^(m - M) to shared memory, summed by row.
       float2* ml = reinterpret_cast<float2*>(smem);
-      float* os = reinterpret_cast<float*>(smem + Cfg::kRingOff);
+      float* os = reinterpret_cast<float*>(smem + Cfg::kKRingOff);
       ml[tid] = make_float2(m, l);
       named_bar_sync(1, 128);
       float M = -INFINITY;
@@ -692,18 +797,8 @@ int launch_cross_tc(const CrossParams& p, int num_seqs, const CrossMaps& maps, c
   return launch_cross_merge<T, D>(p, num_seqs, stream);
 }
 
-// Rows of a thread block: 32 (each on four lanes), 128, or 256.
-enum class CrossRows { k32, k128, k256 };
-
-template <typename T, int D, bool KV8>
-int launch_cross_rows(const CrossParams& p, int num_seqs, CrossRows rows, const CrossMaps& maps,
-                      cudaStream_t stream) {
-  switch (rows) {
-    case CrossRows::k32: return launch_cross_tc<T, D, 1, KV8, true>(p, num_seqs, maps, stream);
-    case CrossRows::k128: return launch_cross_tc<T, D, 1, KV8, false>(p, num_seqs, maps, stream);
-    case CrossRows::k256: return launch_cross_tc<T, D, 2, KV8, false>(p, num_seqs, maps, stream);
-  }
-  return PKV_ERR_ARG;
-}
+// Rows of a thread block: 32 (each on four lanes), 128, or 256; or 32 in one
+// balanced stream over all sequences (cross_stream.cuh).
+enum class CrossRows { kStream, k32, k128, k256 };
 
 }  // namespace pkv

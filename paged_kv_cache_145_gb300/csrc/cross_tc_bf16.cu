@@ -1,5 +1,5 @@
 // Cross attention on tensor cores: instantiations for bf16 pools.
-#include "cross_tc.cuh"
+#include "cross_stream.cuh"
 
 int pkv_launch_cross_tc_bf16(const pkv::CrossParams& p, int num_seqs, int dim, pkv::CrossRows rows,
                            const pkv::CrossMaps& maps, cudaStream_t stream) {

@@ -1,6 +1,6 @@
 // Cross attention on tensor cores: instantiations for FP8 pools (head_dim
 // 128), q and out in fp16 or bf16.
-#include "cross_tc.cuh"
+#include "cross_stream.cuh"
 
 int pkv_launch_cross_tc_fp8(const pkv::CrossParams& p, int io_dtype, int num_seqs,
                             pkv::CrossRows rows, const pkv::CrossMaps& maps, cudaStream_t stream) {

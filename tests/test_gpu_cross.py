@@ -351,3 +351,21 @@ def test_no_sequences_and_no_queries():
                                     torch.zeros(1, dtype=torch.int32, device="cuda"), 0.1, 3)
     assert (out == 0).all()
     assert pkv.paged_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,D,G", [(BF16, 128, 4), (F16, 64, 1), (FP8, 128, 8)])
+@pytest.mark.parametrize("seqs,longest,seed", [(1, 64, 0), (2, 65, 1), (7, 700, 2), (40, 3000, 3),
+                                               (400, 130, 4), (1024, 90, 5), (1100, 70, 6)])
+def test_streams_of_ragged_sequences(dtype, D, G, seqs, longest, seed):
+    """Few rows: boundaries between blocks fall anywhere in and between
+    sequences, some without states, some without queries; many sequences."""
+    rng = np.random.default_rng(seed)
+    lens = [int(x) for x in rng.integers(0, longest + 1, seqs)]
+    lens[0] = longest
+    top = max(1, 32 // G)
+    qlens = [int(x) for x in rng.integers(0, top + 1, seqs)]
+    qlens[-1] = top
+    c = Case(qlens, lens, 2 * G, 2, D, dtype, BF16 if dtype == FP8 else None, seed=seed + 20)
+    some = sorted({0, seqs - 1, *(int(x) for x in rng.integers(0, seqs, 40))})
+    c.check(c.call(max_queries=top), some)
+    assert pkv.paged_get_device_error() == 0
