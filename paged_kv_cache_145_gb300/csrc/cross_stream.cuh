@@ -32,10 +32,11 @@ struct CrossStreamCfg {
   static constexpr int kQBytes = Tc::kQBytes;
   static constexpr int kRawBytes = Tc::kRawBytes;
   static constexpr int kRawSlots = KV8 ? 2 : 0;             // of K, and of V
-  static constexpr int kKSlots = KV8 ? 1 : D == 64 ? 4 : 2, kVSlots = kKSlots;
+  static constexpr int kKSlots = KV8 ? 1 : D == 64 ? 5 : 2, kVSlots = kKSlots;
   static constexpr int kRound = KV8 ? 2 : 4;                // rows joined at a time
   static constexpr int kKeyWarp = 4, kValueWarp = 5, kMmaWarp = 6, kConvWarp = 7;
-  static constexpr int kThreads = 224 + Tc::kConvThreads;
+  static constexpr int kCheckWarp = 7 + (KV8 ? 4 : 0);
+  static constexpr int kThreads = (kCheckWarp + 1) * 32;
   static constexpr int kKRingOff = kQBytes;
   static constexpr int kVRingOff = kKRingOff + kKSlots * kTileBytes;
   static constexpr int kRawOff = kVRingOff + kVSlots * kTileBytes;  // K, then V
@@ -46,7 +47,7 @@ struct CrossStreamCfg {
   static constexpr int kLenOff = kCumOff + (kStreamSeqs + 1) * 4;
   static constexpr int kBadOff = kLenOff + kStreamSeqs * 4;        // a bit per sequence
   static constexpr int kBarOff = kBadOff + kStreamSeqs / 8 + 4;
-  static constexpr int kNumBars = 2 * kKSlots + 2 * kVSlots + 4 * kRawSlots + 2 * kBufs + 3;
+  static constexpr int kNumBars = 2 * kKSlots + 2 * kVSlots + 4 * kRawSlots + 2 * kBufs + 4;
   static constexpr int kTmemOff = kBarOff + kNumBars * 8;
   static constexpr int kFlagOff = kTmemOff + 4;  // a wait ran out
   static constexpr int kSmemBytes = kTmemOff + 16;
@@ -85,6 +86,13 @@ cross_stream_kernel(const __grid_constant__ CrossParams p, const __grid_constant
   const int c = blockIdx.x, C = (int)gridDim.x, S = p.num_seqs;
   const int H = p.num_heads, Hk = p.kv_heads, G = p.group, b = p.block_size;
   T* const out = static_cast<T*>(p.out);
+  // Small tables are on their way to L2 while the lengths are read.
+  {
+    const int64_t bytes = (int64_t)S * p.max_blocks * 4;
+    const int64_t at = ((int64_t)c * Cfg::kThreads + tid) * 128;
+    if (bytes <= (1 << 20) && at < bytes)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(p.tables) + at));
+  }
 
   // ---- barriers, tensor memory, tile counts --------------------------------------
   const uint32_t bar0 = sbase + Cfg::kBarOff;
@@ -100,7 +108,7 @@ cross_stream_kernel(const __grid_constant__ CrossParams p, const __grid_constant
   auto s_full = [&](int i) { return bar0 + 8u * (B1 + i); };
   auto p_full = [&](int i) { return bar0 + 8u * (B1 + NS + i); };
   const uint32_t o_done = bar0 + 8u * (B1 + 2 * NS);
-  const uint32_t q_full = o_done + 8u, drain = o_done + 16u;
+  const uint32_t q_full = o_done + 8u, drain = o_done + 16u, checked = o_done + 24u;
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) {
       mbar_init(k_full(i), KV8 ? Tc::kConvThreads : 1);
@@ -123,6 +131,7 @@ cross_stream_kernel(const __grid_constant__ CrossParams p, const __grid_constant
     mbar_init(o_done, 1);
     mbar_init(q_full, 128);
     mbar_init(drain, 1);
+    mbar_init(checked, 32);
     fence_mbar_init();
     *reinterpret_cast<int*>(smem + Cfg::kFlagOff) = 0;
   }
@@ -322,6 +331,14 @@ cross_stream_kernel(const __grid_constant__ CrossParams p, const __grid_constant
       mbar_wait(drain, 0);
     }
     __syncwarp();
+  } else if (warp == Cfg::kCheckWarp) {
+    // ---- whole table rows of the stretch's sequences, so that every block agrees ----
+    for (int s = run_at(0).s, last = run_at(n_tiles - 1).s; s <= last; ++s) {
+      const int nblk = cum[s + 1] > cum[s] ? (len[s] - 1) / b + 1 : 0;
+      if (table_row_bad(p, p.tables + (int64_t)s * p.max_blocks, nblk, lane))
+        atomicOr(bad_bits + s / 32, 1u << (s % 32));
+    }
+    mbar_arrive(checked);
   } else if (KV8 && warp >= Cfg::kConvWarp) {
     // ---- converters: codes to fp16 -------------------------------------------------
     if constexpr (KV8) {
@@ -390,15 +407,6 @@ cross_stream_kernel(const __grid_constant__ CrossParams p, const __grid_constant
     float qscale = bring(q, r.kvh);
     fence_proxy_async_smem();
     mbar_arrive(q_full);
-    // Whole table rows of the stretch's sequences, so that every block agrees.
-    for (int s = r.s, last = run_at(n_tiles - 1).s; s <= last; ++s) {
-      const int nblk = cum[s + 1] > cum[s] ? (len[s] - 1) / b + 1 : 0;
-      const int32_t* trow = p.tables + (int64_t)s * p.max_blocks;
-      for (int e = tid; e < nblk; e += 128) {
-        const int x = trow[e];
-        if (x < 0 || (int64_t)x >= p.num_blocks) atomicOr(bad_bits + s / 32, 1u << (s % 32));
-      }
-    }
     for (int i = 0; i < n_tiles && ok;) {
       const int nr = q.Q * G, end = i + r.n;
       // The next pair, looked up while this one's tiles are worked on.
@@ -407,6 +415,9 @@ cross_stream_kernel(const __grid_constant__ CrossParams p, const __grid_constant
       if (end < n_tiles) {
         nx = run_at(end);
         nq = cross_seq(p, nx.s);
+        const T* row = static_cast<const T*>(p.q) + row_at(nq, nx.kvh, min(lane, nq.Q * G - 1));
+#pragma unroll
+        for (int k = 0; k < D; k += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + k));
       }
       float m = -INFINITY, l = 0.f;
       for (int j = i; j < end; ++j) {
@@ -497,7 +508,11 @@ cross_stream_kernel(const __grid_constant__ CrossParams p, const __grid_constant
         ok = mbar_wait(o_done, (uint32_t)((end - 1) & 1));
         ok = !__any_sync(kFullMask, !ok);
       }
-      // The four warps go on, or stop, together; and the table bits are complete.
+      if (ok) {
+        ok = mbar_wait(checked, 0);  // the table bits are complete
+        ok = !__any_sync(kFullMask, !ok);
+      }
+      // The four warps go on, or stop, together.
       if (!ok) *stop_flag = 1;
       named_bar_sync(1, 128);
       const bool bad = (bad_bits[r.s / 32] >> (r.s % 32)) & 1u;

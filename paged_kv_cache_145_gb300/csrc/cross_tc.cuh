@@ -57,7 +57,7 @@ struct CrossTcCfg {
   static constexpr int kQHalfBytes = 128 * 128;
   static constexpr int kQBytes = kHalves * kQHalfBytes;     // one row tile
   static constexpr int kRawBytes = KV8 ? kKeys * D : 0;     // one tile of codes
-  static constexpr int kRawSlots = KV8 ? 2 : 0;             // of K, and of V
+  static constexpr int kRawSlots = KV8 ? (QT == 2 ? 4 : 2) : 0;  // of K, and of V
   // Ring slots of K and V: what one block (QT 1: two) leaves of an SM's shared
   // memory, at most 8.  A V tile is held longer (until P.V).
   static constexpr int kAvail =
@@ -75,7 +75,7 @@ struct CrossTcCfg {
   static constexpr int kVRingOff = kKRingOff + kKSlots * kTileBytes;
   static constexpr int kRawOff = kVRingOff + kVSlots * kTileBytes;  // K, then V
   static constexpr int kBarOff = kRawOff + 2 * kRawSlots * kRawBytes;
-  static constexpr int kNumBars = 2 * kSlots + 4 * kRawSlots + QT * (2 * kBufs + 3) + 1;
+  static constexpr int kNumBars = 2 * kSlots + 4 * kRawSlots + QT * (2 * kBufs + 3) + 2;
   static constexpr int kTmemOff = kBarOff + kNumBars * 8;
   static constexpr int kFlagOff = kTmemOff + 4;
   static constexpr int kSmemBytes = kTmemOff + 16;
@@ -100,6 +100,21 @@ struct CrossTcCfg {
   static_assert(QT == 1 || 2 * kSmemBytes > 228 * 1024, "blocks per SM");
   static_assert(QT == 2 || 3 * kSmemBytes > 228 * 1024, "blocks per SM");
 };
+
+// Whether any of the first n entries of a table row is out of range, in lane's
+// share of them (a warp reads the row, eight entries a lane in flight).
+__device__ __forceinline__ bool table_row_bad(const CrossParams& p, const int32_t* trow, int n,
+                                              int lane) {
+  bool bad = false;
+  for (int i0 = lane; i0 < n; i0 += 256) {
+    int e[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = i0 + 32 * k < n ? trow[i0 + 32 * k] : 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bad |= e[k] < 0 || (int64_t)e[k] >= p.num_blocks;
+  }
+  return bad;
+}
 
 // A thread's Q row, from global memory into row rr of a 128-row tile in the
 // 128-byte-swizzled operand layout; returns the factor that makes its
@@ -358,6 +373,7 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
   auto o_last = [&](int t) { return bar0 + 8u * (B1 + 2 * QT * NS + QT + t); };
   const uint32_t q_full = bar0 + 8u * (B1 + 2 * QT * NS + 2 * QT);
   auto drain = [&](int t) { return q_full + 8u * (1 + t); };
+  const uint32_t checked = q_full + 8u * (1 + QT);  // the table row
   auto tile_warps = [&](int t) {  // softmax warps with rows of row tile t
     return SPLIT ? 4 : min(4, max(0, (nr - t * 128 + 31) / 32));
   };
@@ -386,6 +402,7 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       mbar_init(drain(t), 1);
     }
     mbar_init(q_full, (tile_warps(0) + (QT > 1 ? tile_warps(QT - 1) : 0)) * 32);
+    mbar_init(checked, 32);
     fence_mbar_init();
     *reinterpret_cast<int*>(smem + Cfg::kFlagOff) = 0;
   }
@@ -410,14 +427,6 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
     qscale = bring_row<T, D, KV8>(p, kvh, static_cast<const T*>(p.q) + row_at(min(r, nr - 1)), qt, rr);
     fence_proxy_async_smem();
     mbar_arrive(q_full);
-    // Every block checks the whole table row, so that all parts agree.  A bad
-    // entry's pages are read as zeros and the rows are zeroed at the end.
-    const int nblk = (c.L - 1) / b + 1;
-    for (int i = tid; i < nblk; i += 32 * tile_warps(0)) {
-      if (tid >= 32 * tile_warps(0)) break;  // (the second row tile leaves it to the first)
-      const int e = trow[i];
-      if (e < 0 || (int64_t)e >= p.num_blocks) *bad_flag = 1;
-    }
   }
   if (warp == Cfg::kKeyWarp || warp == Cfg::kValueWarp) {
     // ---- producers ----------------------------------------------------------
@@ -464,6 +473,13 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       failed = false;
     }
     __syncwarp();
+    if (warp == Cfg::kKeyWarp) {
+      // All copies are under way: the whole table row is checked by every
+      // block, so that all parts agree.  (A bad entry's page was read as
+      // zeros, and the rows are zeroed at the end.)
+      if (table_row_bad(p, trow, (c.L - 1) / b + 1, lane)) *bad_flag = 1;
+      mbar_arrive(checked);
+    }
   } else if (warp >= Cfg::kMmaWarp && warp < Cfg::kConvWarp) {
     // ---- MMA issuers ----------------------------------------------------------
     const int tt = warp - Cfg::kMmaWarp;
@@ -671,9 +687,11 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       ok = mbar_wait(o_last(t), 0);
       ok = !__any_sync(kFullMask, !ok);
     }
+    if (ok) {
+      ok = mbar_wait(checked, 0);
+      ok = !__any_sync(kFullMask, !ok);
+    }
     failed = !ok;
-    // (every softmax warp is here: the table flag is complete after this)
-    named_bar_sync(1, 32 * (tile_warps(0) + (QT > 1 ? tile_warps(QT - 1) : 0)));
     const bool bad = *bad_flag != 0;
     if (bad && tid == 0) set_error(p.err, PKV_DEV_TABLE_RANGE);
     const float vs = KV8 ? p.v_scale[kvh] : 1.f;
