@@ -499,10 +499,9 @@ def paged_build_tables(free_list, free_state, old_lens, new_lens, block_tables, 
     n = old_lens.numel()
     if free_list.dim() != 1 or free_state.shape != (2,):
         raise ValueError("free_list must be [num_blocks] and free_state [2]")
-    if old_lens.shape != (n,) or new_lens.shape != (n,) or block_tables.dim() != 2 or \
-            block_tables.shape[0] != n:
+    width = block_tables.shape
+    if len(width) != 2 or width[0] != n or old_lens.dim() != 1 or new_lens.shape != (n,):
         raise ValueError("old_lens and new_lens must be [S] and block_tables [S, max_blocks]")
-    max_tokens = int(max_tokens)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
     there = _elsewhere(dev, stream)
@@ -519,9 +518,8 @@ def paged_build_tables(free_list, free_state, old_lens, new_lens, block_tables, 
     rc = _lib.lib().paged_build_tables(
         free_list.numel(), block_size, free_list.data_ptr(), free_state.data_ptr(),
         old_lens.data_ptr(), new_lens.data_ptr(), n, block_tables.data_ptr(),
-        block_tables.shape[1], seq_lens.data_ptr(), free_state_out.data_ptr(),
-        query_starts.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), max_tokens,
-        _raw_stream(dev.index))
+        width[1], seq_lens.data_ptr(), free_state_out.data_ptr(), query_starts.data_ptr(),
+        slot_mapping.data_ptr(), positions.data_ptr(), max_tokens, _raw_stream(dev.index))
     if rc:
         _lib.check(rc, "paged_build_tables")
     return seq_lens, free_state_out, query_starts, slot_mapping, positions

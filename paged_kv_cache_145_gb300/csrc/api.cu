@@ -556,7 +556,7 @@ CrossPlan cross_plan(const pkv_cache* c, int64_t total_queries, int num_seqs, in
   if (pl.tc && rows <= 32 && num_seqs <= pkv::kStreamSeqs && tiles < INT32_MAX) {
     pl.rows = pkv::CrossRows::kStream;
     // at least about four tiles a block
-    pl.parts = (int)std::max<int64_t>(1, std::min<int64_t>(2 * sms, (tiles + (std::getenv("XD") ? std::atoi(std::getenv("XD")) : 4) - 1) / (std::getenv("XD") ? std::atoi(std::getenv("XD")) : 4)));
+    pl.parts = (int)std::max<int64_t>(1, std::min<int64_t>(2 * sms, (tiles + 3) / 4));
     pl.part = (int)rows;
     pl.ws_rows = pl.parts > 1 ? 2 * pl.parts * rows : 0;
     return pl;

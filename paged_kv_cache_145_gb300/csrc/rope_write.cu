@@ -111,101 +111,109 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const __grid_c
   const int pairs = p.rot.rotary_dim >> 1;
   const int half_vecs = INTER ? 0 : pairs / V;  // vectors in each rotated half
   const int vecs = D / V;
+  // The cosines and sines of a token lie with a vector's j-th pair at
+  // j * groups + vector, so that the lanes of a head read neighbours.
+  constexpr int P = INTER ? V / 2 : V;  // pairs that a vector (INTER) or two hold
+  const int groups = (pairs + P - 1) / P;
   const int64_t first = p.num_tokens * blockIdx.x / gridDim.x;
   const int64_t last = p.num_tokens * (blockIdx.x + 1) / gridDim.x;
   const int lanes = kRopeThreads / p.units;  // rows (head of a token) in flight
   const int u = tid % p.units, lane_row = tid / p.units;
   const int step = lanes * (int)gridDim.y;
   const int x0 = lane_row < lanes ? (int)blockIdx.y * lanes + lane_row : INT32_MAX;
+  // This unit's vectors in query and key heads; in value heads 2u and 2u + 1.
+  const bool half = u < half_vecs;
+  const int va = half ? u : 2 * u, vb = half ? u + half_vecs : 2 * u + 1;
 
   struct Unit {
     RopeVec<TI, V> a, b;
-    int tok, head, va, vb;  // head counts through q, k, v; vb < 0: one vector
   };
-  auto fetch = [&](int64_t t0, int x, Unit& w) {
-    w.tok = x / HT;
-    w.head = x - w.tok * HT;
-    const int64_t t = t0 + w.tok;
-    if (w.head < H + Hk && u < half_vecs) {
-      w.va = u;
-      w.vb = u + half_vecs;
-    } else {
-      w.va = 2 * u;
-      w.vb = 2 * u + 1 < vecs ? 2 * u + 1 : -1;
+  // A place in a chunk: token and head (counted through queries, keys, values).
+  struct Place {
+    int tok, head;
+  };
+  auto settle = [&](Place& at) {
+    while (at.head >= HT) {
+      at.head -= HT;
+      ++at.tok;
     }
-    const TI* src;
-    if (w.head < H)
-      src = static_cast<const TI*>(p.q) + t * p.q_stride + (int64_t)w.head * D;
-    else if (w.head < H + Hk)
-      src = static_cast<const TI*>(p.k) + t * p.k_stride + (int64_t)(w.head - H) * D;
-    else
-      src = static_cast<const TI*>(p.v) + t * p.v_stride + (int64_t)(w.head - H - Hk) * D;
-    w.a.load(src + w.va * V);
-    if (w.vb >= 0) w.b.load(src + w.vb * V);
   };
-  auto finish = [&](int64_t t0, Unit& w, const float2* cs, int64_t row) {
-    const bool key = w.head < H + Hk;
+  auto fetch = [&](int64_t t0, const Place& at, Unit& w) {
+    const int64_t t = t0 + at.tok;
+    const bool key = at.head < H + Hk;
+    const TI* src;
+    if (at.head < H)
+      src = static_cast<const TI*>(p.q) + t * p.q_stride + (int64_t)at.head * D;
+    else if (key)
+      src = static_cast<const TI*>(p.k) + t * p.k_stride + (int64_t)(at.head - H) * D;
+    else
+      src = static_cast<const TI*>(p.v) + t * p.v_stride + (int64_t)(at.head - H - Hk) * D;
+    const int a = key ? va : 2 * u, b = key ? vb : 2 * u + 1;
+    w.a.load(src + a * V);
+    if (b < vecs) w.b.load(src + b * V);
+  };
+  auto finish = [&](int64_t t0, const Place& at, Unit& w, const float2* cs, int64_t row) {
+    const bool query = at.head < H, key = at.head < H + Hk;
+    const int fa = key ? va : 2 * u, fb = key ? vb : 2 * u + 1;
+    const int h = query ? at.head : at.head - (key ? H : H + Hk);
+    if (!query && row < 0) return;  // padding
     float a[V], b[V];
-    w.a.widen(a);
-    if (w.vb >= 0) w.b.widen(b);
-    bool turned = false;
-    if (key) {
+    const bool turned = key && (INTER || half);
+    if (turned || (FP8 && !query)) {
+      w.a.widen(a);
+      w.b.widen(b);
+    }
+    if (turned) {
       if constexpr (INTER) {
         auto turn = [&](float (&f)[V], int vec) {
 #pragma unroll
           for (int j = 0; j < V; j += 2) {
-            const int i = (vec * V + j) >> 1;
-            if (i < pairs) {
-              const float2 c = cs[i];
+            if (((vec * V + j) >> 1) < pairs) {
+              const float2 c = cs[(j >> 1) * groups + vec];
               const float xx = f[j], yy = f[j + 1];
               f[j] = xx * c.x - yy * c.y;
               f[j + 1] = yy * c.x + xx * c.y;
             }
           }
         };
-        turn(a, w.va);
-        if (w.vb >= 0) turn(b, w.vb);
-        turned = true;
-      } else if (u < half_vecs) {
+        turn(a, fa);
+        if (fb < vecs) turn(b, fb);
+      } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float2 c = cs[u * V + j];
+          const float2 c = cs[j * groups + u];
           const float xx = a[j], yy = b[j];
           a[j] = xx * c.x - yy * c.y;
           b[j] = yy * c.x + xx * c.y;
         }
-        turned = true;
       }
     }
-    const int h = w.head < H ? w.head : w.head - (key ? H : H + Hk);
-    const int64_t at = (row + (int64_t)h * p.block_size) * D;
-    if (FP8 && w.head >= H) {
-      if (row < 0) return;
+    if (FP8 && !query) {
       const float sc = (key ? p.k_scale : p.v_scale)[h];
-      unsigned char* dst = static_cast<unsigned char*>(key ? p.k_cache : p.v_cache) + at;
-      store_codes<V>(dst + w.va * V, a, sc);
-      if (w.vb >= 0) store_codes<V>(dst + w.vb * V, b, sc);
+      unsigned char* dst = static_cast<unsigned char*>(key ? p.k_cache : p.v_cache) +
+                           (row + (int64_t)h * p.block_size) * D;
+      store_codes<V>(dst + fa * V, a, sc);
+      if (fb < vecs) store_codes<V>(dst + fb * V, b, sc);
       return;
-    }
-    TI* dst;
-    if (w.head < H) {
-      dst = static_cast<TI*>(p.q_out) + (t0 + w.tok) * p.q_out_stride + (int64_t)h * D;
-    } else {
-      if (row < 0) return;
-      dst = static_cast<TI*>(key ? p.k_cache : p.v_cache) + at;
     }
     if (turned) {  // (what is not turned keeps its bits)
       w.a.narrow(a);
-      if (w.vb >= 0) w.b.narrow(b);
+      w.b.narrow(b);
     }
-    w.a.store(dst + w.va * V);
-    if (w.vb >= 0) w.b.store(dst + w.vb * V);
+    TI* dst = query ? static_cast<TI*>(p.q_out) + (t0 + at.tok) * p.q_out_stride + (int64_t)h * D
+                    : static_cast<TI*>(key ? p.k_cache : p.v_cache) +
+                          (row + (int64_t)h * p.block_size) * D;
+    w.a.store(dst + fa * V);
+    if (fb < vecs) w.b.store(dst + fb * V);
   };
 
   Unit cur;
   int64_t t0 = first;
-  int rows = (int)min((int64_t)kRopeTokens, last - t0) * HT;
-  if (t0 < last && x0 < rows) fetch(t0, x0, cur);
+  Place start{0, x0 < INT32_MAX ? x0 : 0}, at;
+  settle(start);
+  if (x0 == INT32_MAX) start.tok = INT32_MAX;  // no unit for this thread
+  at = start;
+  if (t0 + at.tok < last && at.tok < kRopeTokens) fetch(t0, at, cur);
   for (int buf = 0; t0 < last; buf ^= 1) {
     // ---- angles and pool rows of this chunk's tokens -------------------------
     const int nt = (int)min((int64_t)kRopeTokens, last - t0);
@@ -216,7 +224,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const __grid_c
       const float half_turns = (float)(int32_t)(turns >> 32) * 0x1p-31f;
       float s, c;
       sincospif(half_turns, &s, &c);
-      s_cs[buf][e] = make_float2(c, s);
+      s_cs[buf][tok * groups * P + i % P * groups + i / P] = make_float2(c, s);
     }
     if (tid < nt) {
       const int64_t slot = p.slots[t0 + tid];
@@ -231,17 +239,18 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const __grid_c
     // (the other buffer's readers are past this barrier's last use of it)
     __syncthreads();
     const int64_t t1 = t0 + nt;
-    const int rows1 = (int)min((int64_t)kRopeTokens, last - t1) * HT;
-    for (int x = x0; x < rows;) {
+    while (at.tok < nt) {
+      Place then{at.tok, at.head + step};
+      settle(then);
       Unit nxt = cur;
-      x += step;
-      if (x < rows) fetch(t0, x, nxt);
-      else if (t1 < last && x0 < rows1) fetch(t1, x0, nxt);
-      finish(t0, cur, s_cs[buf] + cur.tok * pairs, s_row[buf][cur.tok]);
+      if (then.tok < nt) fetch(t0, then, nxt);
+      else if (start.tok < kRopeTokens && t1 + start.tok < last) fetch(t1, start, nxt);
+      finish(t0, at, cur, s_cs[buf] + at.tok * groups * P, s_row[buf][at.tok]);
       cur = nxt;
+      at = then;
     }
     t0 = t1;
-    rows = rows1;
+    at = start;
   }
 }
 
