@@ -7,17 +7,15 @@
 #include <cstring>
 #include <mutex>
 
-#include "cross_stream.cuh"
+#include "cross_tc.cuh"
 #include "decode_launch.cuh"
 #include "prefill.cuh"
 
 int pkv_launch_kv_write(const pkv_cache* c, const void* k, const void* v, const int64_t* slots,
                         int64_t num_tokens, size_t elem_bytes, cudaStream_t stream);
-int pkv_launch_cross_tc_f16(const pkv::CrossParams&, int, int, pkv::CrossRows, const pkv::CrossMaps&,
-                            cudaStream_t);
-int pkv_launch_cross_tc_bf16(const pkv::CrossParams&, int, int, pkv::CrossRows, const pkv::CrossMaps&,
-                             cudaStream_t);
-int pkv_launch_cross_tc_fp8(const pkv::CrossParams&, int, int, pkv::CrossRows, const pkv::CrossMaps&,
+int pkv_launch_cross_tc_f16(const pkv::CrossParams&, int, int, const pkv::CrossMaps&, cudaStream_t);
+int pkv_launch_cross_tc_bf16(const pkv::CrossParams&, int, int, const pkv::CrossMaps&, cudaStream_t);
+int pkv_launch_cross_tc_fp8(const pkv::CrossParams&, int, int, bool, const pkv::CrossMaps&,
                             cudaStream_t);
 int pkv_launch_cross(const pkv::CrossParams& p, int dtype, int io_dtype, int num_seqs, int dim,
                      cudaStream_t stream);
@@ -527,63 +525,49 @@ int paged_attention_prefill(const pkv_cache* cache, const void* q, int64_t total
 namespace {
 
 // How cross attention runs: on tensor cores (16-bit pools, FP8 pools of
-// head_dim 128) in blocks of 256 rows, or, where no sequence has more, of 128
-// or 32 rows two to an SM; else on CUDA cores in blocks of 8 rows.  Where the
-// blocks would not fill the GPU the states are split in whole runs of 128
-// positions, as few parts as give every SM its blocks.  At most 32 rows run
-// as one stream of all states instead, unless the sequences are too many for
-// a block to hold their tile counts (there are blocks enough then).
+// head_dim 128) in blocks of 128 rows, two to an SM, or, for FP8 pools where a
+// sequence has more rows than that, of 256; else on CUDA cores in blocks of
+// 8 rows.  Where the blocks would not fill the GPU the states are split in
+// whole runs of 128 positions, into as many parts as there are free places
+// (one token of four sequences over 5200-6400 states: 23.9 us; twice and four
+// times as many parts: 29.2 and 34.5).
 struct CrossPlan {
-  bool tc;
-  pkv::CrossRows rows;
-  int parts, part;    // stream: blocks, rows of a workspace slot
-  int64_t ws_rows;    // workspace rows of head_dim floats and one (m, l) pair
+  bool tc, wide;
+  int parts, part;
 };
 
-CrossPlan cross_plan(const pkv_cache* c, int64_t total_queries, int num_seqs, int num_heads,
-                     int max_queries, int max_len) {
+CrossPlan cross_plan(const pkv_cache* c, int num_seqs, int num_heads, int max_queries,
+                     int max_len) {
   CrossPlan pl{};
   pl.tc = c->dtype == PKV_F16 || c->dtype == PKV_BF16 ||
           (c->dtype == PKV_FP8_E4M3 && c->head_dim == 128);
   const int64_t rows = (int64_t)max_queries * (num_heads / c->num_kv_heads);
+  pl.wide = c->dtype == PKV_FP8_E4M3 && rows > 128;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
     cudaGetLastError();
     sms = 1;
   }
-  const int64_t tiles = (int64_t)num_seqs * c->num_kv_heads * (((int64_t)max_len + 63) / 64);
-  if (pl.tc && rows <= 32 && num_seqs <= pkv::kStreamSeqs && tiles < INT32_MAX) {
-    pl.rows = pkv::CrossRows::kStream;
-    // at least about four tiles a block
-    pl.parts = (int)std::max<int64_t>(1, std::min<int64_t>(2 * sms, (tiles + 3) / 4));
-    pl.part = (int)rows;
-    pl.ws_rows = pl.parts > 1 ? 2 * pl.parts * rows : 0;
-    return pl;
-  }
-  pl.rows = rows > 128  ? pkv::CrossRows::k256
-            : rows > 32 ? pkv::CrossRows::k128
-                        : pkv::CrossRows::k32;
-  const bool wide = pl.rows == pkv::CrossRows::k256;
-  const int64_t per = !pl.tc ? pkv::kCrossRows : wide ? 256 : rows > 32 ? 128 : 32;
-  const int64_t slots = (int64_t)sms * (pl.tc ? (wide ? 1 : 2) : 8);
-  const int64_t blocks = std::max<int64_t>(1, (int64_t)num_seqs * c->num_kv_heads * ((rows + per - 1) / per));
+  const int64_t per = !pl.tc ? pkv::kCrossRows : pl.wide ? 256 : 128;
+  const int64_t places = (int64_t)sms * (!pl.tc ? 8 : pl.wide ? 1 : 2);
+  const int64_t blocks =
+      std::max<int64_t>(1, (int64_t)num_seqs * c->num_kv_heads * ((rows + per - 1) / per));
   constexpr int kRun = 128;
   const int64_t runs = std::max<int64_t>(1, ((int64_t)max_len + kRun - 1) / kRun);
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(runs, slots / blocks));
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(runs, places / blocks));
   const int64_t part = (runs + want - 1) / want * kRun;
   pl.part = (int)part;
   pl.parts = (int)((runs * kRun + part - 1) / part);
-  pl.ws_rows = pl.parts > 1 ? total_queries * num_heads * pl.parts : 0;
   return pl;
 }
 
 // Describes a pool to the cross attention kernels as pages of 8-row groups:
 // {128 bytes of a row, 8 rows, 128-byte column blocks, groups, N * Hk pages},
-// read in boxes of a page's rows (at most `keys`) with the 128-byte swizzle.
+// read a page at a time with the 128-byte swizzle.
 // A box lands as its groups one after the other, each with its column blocks
 // of 8 x 128 bytes, the order in which the MMA operands are laid out.
-bool encode_page_map(CUtensorMap* map, const pkv_cache* c, void* base, int keys) {
+bool encode_page_map(CUtensorMap* map, const pkv_cache* c, void* base) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t elt = elem_bytes(c->dtype), row = c->head_dim * elt;
@@ -591,7 +575,7 @@ bool encode_page_map(CUtensorMap* map, const pkv_cache* c, void* base, int keys)
                               (cuuint64_t)c->num_blocks * c->num_kv_heads};
   const cuuint64_t strides[4] = {row, 128, 8 * row, c->block_size * row};
   const cuuint32_t box[5] = {(cuuint32_t)(128 / elt), 8, (cuuint32_t)(row / 128),
-                             (cuuint32_t)(std::min(c->block_size, keys) / 8), 1};
+                             (cuuint32_t)c->block_size / 8, 1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUtensorMapDataType ty =
       c->dtype == PKV_FP8_E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
@@ -603,11 +587,11 @@ bool encode_page_map(CUtensorMap* map, const pkv_cache* c, void* base, int keys)
 }
 
 // Bytes of the (m, l) pairs and where the partial outputs start.
-WsLayout cross_workspace(const CrossPlan& pl, int head_dim) {
+WsLayout cross_workspace(int64_t total_queries, int num_heads, int head_dim, int parts) {
   WsLayout w{};
-  w.parts = pl.parts;
-  if (pl.ws_rows == 0) return w;
-  const size_t rows = (size_t)pl.ws_rows;
+  w.parts = parts;
+  if (parts <= 1) return w;
+  const size_t rows = (size_t)total_queries * num_heads * parts;
   w.ml_bytes = rows * sizeof(float2);
   w.o_offset = (w.ml_bytes + 255) & ~size_t(255);
   w.total = w.o_offset + rows * head_dim * sizeof(float);
@@ -629,9 +613,8 @@ size_t paged_attention_cross_workspace_bytes(const pkv_cache* cache, int64_t tot
   if (!cache || !cross_args_ok(cache, total_queries, num_seqs, num_heads, max_queries) ||
       max_enc_len < 0)
     return 0;
-  const CrossPlan sp =
-      cross_plan(cache, total_queries, num_seqs, num_heads, max_queries, max_enc_len);
-  return cross_workspace(sp, cache->head_dim).total;
+  const CrossPlan sp = cross_plan(cache, num_seqs, num_heads, max_queries, max_enc_len);
+  return cross_workspace(total_queries, num_heads, cache->head_dim, sp.parts).total;
 }
 
 int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_queries,
@@ -658,9 +641,8 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
       (reinterpret_cast<uintptr_t>(enc_lens) & 3u) ||
       (reinterpret_cast<uintptr_t>(query_starts) & 3u))
     return PKV_ERR_ALIGN;
-  const CrossPlan sp =
-      cross_plan(cache, total_queries, num_seqs, num_heads, max_queries, max_len);
-  const WsLayout ws = cross_workspace(sp, cache->head_dim);
+  const CrossPlan sp = cross_plan(cache, num_seqs, num_heads, max_queries, max_len);
+  const WsLayout ws = cross_workspace(total_queries, num_heads, cache->head_dim, sp.parts);
   if (ws.total > 0) {
     if (!workspace || workspace_bytes < ws.total) return PKV_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PKV_ERR_ALIGN;
@@ -683,7 +665,6 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
   p.tables = block_tables;
   p.max_blocks = max_blocks_per_seq;
   p.lens = enc_lens;
-  p.num_seqs = num_seqs;
   p.max_len = max_len;
   p.qscale = scale * 1.4426950408889634f;  // log2(e): scores in base-2 units
   p.parts = sp.parts;
@@ -697,15 +678,14 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
     return pkv_launch_cross(p, cache->dtype, cache->io_dtype, num_seqs, cache->head_dim, stream);
   // Pages are a 32-bit coordinate, and one past the last is used.
   if (cache->num_blocks * cache->num_kv_heads >= INT32_MAX) return PKV_ERR_ARG;
-  const int keys = sp.rows == pkv::CrossRows::k256 && cache->dtype != PKV_FP8_E4M3 ? 128 : 64;
   pkv::CrossMaps maps;
-  if (!encode_page_map(&maps.k, cache, cache->k_cache, keys) ||
-      !encode_page_map(&maps.v, cache, cache->v_cache, keys))
+  if (!encode_page_map(&maps.k, cache, cache->k_cache) ||
+      !encode_page_map(&maps.v, cache, cache->v_cache))
     return PKV_ERR_CUDA;
   if (cache->dtype == PKV_FP8_E4M3)
-    return pkv_launch_cross_tc_fp8(p, cache->io_dtype, num_seqs, sp.rows, maps, stream);
+    return pkv_launch_cross_tc_fp8(p, cache->io_dtype, num_seqs, sp.wide, maps, stream);
   return (cache->dtype == PKV_F16 ? pkv_launch_cross_tc_f16 : pkv_launch_cross_tc_bf16)(
-      p, num_seqs, cache->head_dim, sp.rows, maps, stream);
+      p, num_seqs, cache->head_dim, maps, stream);
 }
 
 int paged_block_copy(const pkv_cache* cache, const int64_t* src_dst_pairs, int64_t num_pairs,

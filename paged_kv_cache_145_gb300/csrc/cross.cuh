@@ -31,7 +31,6 @@ struct CrossParams {
   const int32_t* tables;    // [S][max_blocks]
   int max_blocks;
   const int32_t* lens;      // [S]
-  int num_seqs;
   int max_len;
   float qscale;             // scale * log2(e)
   int parts, part;          // parts of the states, positions in each
@@ -73,6 +72,7 @@ constexpr int kCrossMergeWarps = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(kCrossMergeWarps * 32) cross_merge_kernel(const CrossParams p) {
   const CrossSeq c = cross_seq(p, blockIdx.y);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the parts are computed
   if (c.parts <= 1) return;  // written directly
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * kCrossMergeWarps + (threadIdx.x >> 5);  // query * H + head
@@ -93,14 +93,22 @@ __global__ void __launch_bounds__(kCrossMergeWarps * 32) cross_merge_kernel(cons
       w = x.y > 0.f || x.y != x.y ? x.y * ex2(x.x - M) : 0.f;  // an empty part weighs nothing
     }
     const int n = min(32, c.parts - base);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float wi = __shfl_sync(kFullMask, w, i);
-      float f[E];
-      RowLoad<float, E>::load(o + (int64_t)(base + i) * D + lane * E, f);
-      sum += wi;
+    for (int i0 = 0; i0 < n; i0 += 8) {  // eight parts' loads in flight
+      float f[8][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += wi != 0.f ? wi * f[e] : 0.f;
+      for (int i = 0; i < 8; ++i) {
+        const float wi = __shfl_sync(kFullMask, w, i0 + i);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[i][e] = 0.f;
+        if (wi != 0.f) RowLoad<float, E>::load(o + (int64_t)(base + i0 + i) * D + lane * E, f[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float wi = __shfl_sync(kFullMask, w, i0 + i);
+        sum += wi;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += wi * f[i][e];
+      }
     }
   }
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
@@ -256,8 +264,16 @@ template <typename T, int D>
 int launch_cross_merge(const CrossParams& p, int num_seqs, cudaStream_t stream) {
   if (p.parts > 1) {
     const int64_t rows = (int64_t)p.max_queries * p.num_heads;
-    const dim3 grid((unsigned)((rows + kCrossMergeWarps - 1) / kCrossMergeWarps), (unsigned)num_seqs);
-    cross_merge_kernel<T, D><<<grid, kCrossMergeWarps * 32, 0, stream>>>(p);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((rows + kCrossMergeWarps - 1) / kCrossMergeWarps), (unsigned)num_seqs);
+    cfg.blockDim = dim3(kCrossMergeWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, cross_merge_kernel<T, D>, p) != cudaSuccess) return PKV_ERR_CUDA;
   }
   return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

@@ -3,30 +3,43 @@
 //
 // One thread block holds QT tiles of 128 rows (queries of the grouped heads
 // of one KV head, stacked) and walks one part of the sequence's states in
-// tiles of KT keys.  No mask falls between queries and states, so only the
+// tiles of 64 keys.  No mask falls between queries and states, so only the
 // last tile has keys to hide, and they are the same ones for every row.
 // Roles:
-//   warps 0 .. 4 QT - 1  softmax, a thread per row (= tensor-memory lane): the
-//        S row to registers, running maximum and sum, P over S's own columns;
+//   softmax warps, four per row tile  a thread per row (= tensor-memory lane):
+//        the S row to registers, running maximum and sum, P over S's columns;
 //   producer warps, one for K and one for V  the table's pages by TMA, a copy
-//        per page, into a ring each (a copy takes its thread about 90 cycles,
-//        and a tile has up to 8 pages of 16 rows);
+//        per page, into a ring each;
 //   MMA warps, one per row tile  S = Q.K^T and O += P.V (P from tensor
-//        memory), all of a tile's products from one elected thread, so that
-//        they run in the order of issue: S(j + NS) is issued right behind
-//        P.V(j), whose P it overwrites.  The issuing thread's own chain of
-//        instructions is what limits it (about as long as the products), so
-//        each row tile has one, nothing in it is done by the whole warp, and
-//        ring slots and phases are counted along, not computed;
+//        memory), all of a tile's products from one thread, so that they run
+//        in the order of issue: S(j + 2) is issued right behind P.V(j), whose
+//        P it overwrites;
 //   FP8 pools: four converter warps between rings of codes and the others.
-// The running maximum is raised lazily (by more than 2^kSlack, so that O is
+// Two S buffers: S(j + 1) is made while the softmax works on S(j).  The
+// running maximum is raised lazily (by more than 2^kSlack, so that O is
 // rescaled rarely); sums, maxima and O are float32.  P is rounded to the
 // operand type: bf16 for bf16 pools (2^-8 of each weight at most, the step
 // of the output itself), fp16 else, scaled by 2^kBias to keep small weights
 // out of fp16's subnormals.
 //
-// Tensor memory per row tile: NS buffers of S (KT columns, P in the first
-// KT / 2 of them), then O (D columns).  Every wait is bounded.
+// What bounds it.  Many rows: each tile's chain softmax -> P.V -> next S, and
+// the special function unit (an exponential takes a warp about 7 cycles); two
+// blocks of 128 rows per SM hide one another's chains better than one block
+// of 256 rows, although that reads each K and V tile half as often.  Measured
+// (8 sequences of 2048 queries over 2000-6400 states, bf16, 32/8 heads of 128):
+// 783 us (1495 TFLOP/s) with two blocks of 128 rows; one block of 256 rows with
+// 128-key tiles and one S buffer 883.  Few rows: HBM, and below some
+// megabytes per SM the fixed costs of a block (4 us from launch to first tile
+// and last tile to end).  Copies and MMAs are issued by one elected thread
+// each: an operand in a uniform register costs several instructions to fill,
+// and lanes that each issue one do it one after the other (a copy costs its
+// thread about 90 cycles; the same four copies from four lanes took 1000).
+// FP8 pools keep 256 rows where a sequence has more than 128: widening each
+// tile costs more than the chain (8 x 300-512 queries over 1000-4000 states:
+// 194 us, 241 with 128 rows).
+//
+// Tensor memory per row tile: two buffers of S (64 columns each, P in the first
+// 32), then O (D columns).  Every wait is bounded.
 #pragma once
 
 #include <atomic>
@@ -36,18 +49,12 @@
 
 namespace pkv {
 
-// QT 2: 256 rows, one block per SM; QT 1: 128 rows, two blocks per SM.  SPLIT
-// (QT 1): 32 rows, each on four tensor-memory lanes, one per softmax warp,
-// which each take a quarter of every tile's keys with a maximum, a sum and an
-// O of their own, joined at the end: with few rows the softmax of one warp
-// would set the pace (64 sequences of 200-1500 states, 16 heads of 64:
-// 71 us without).
-template <typename T, int D, int QT, bool KV8, bool SPLIT>
+// QT 2: 256 rows, one block per SM; QT 1: 128 rows, two blocks per SM.
+template <typename T, int D, int QT, bool KV8>
 struct CrossTcCfg {
-  static constexpr int kKeys = QT == 2 && !KV8 ? 128 : 64;
-  static constexpr int kBufs = QT == 2 && !KV8 ? 1 : 2;     // S buffers (NS)
-  static constexpr int kRows = SPLIT ? 32 : QT * 128;
-  static constexpr int kLaneKeys = SPLIT ? kKeys / 4 : kKeys;  // keys of a lane
+  static constexpr int kKeys = 64;
+  static constexpr int kBufs = 2;                           // S buffers
+  static constexpr int kRows = QT * 128;
   static constexpr int kHalves = D / 64;                    // 128-byte column blocks
   // K and V tiles: groups of 8 keys, each with its 128-byte column blocks
   // behind one another (1 KiB swizzle atoms).  The order is that of one copy
@@ -79,10 +86,6 @@ struct CrossTcCfg {
   static constexpr int kTmemOff = kBarOff + kNumBars * 8;
   static constexpr int kFlagOff = kTmemOff + 4;
   static constexpr int kSmemBytes = kTmemOff + 16;
-  // SPLIT, at the end: the lanes' (m, l) in Q's memory, their O in the ring's,
-  // rows padded by 16 bytes
-  static constexpr int kORow = D + 4;
-  static_assert(!SPLIT || (QT == 1 && 4 * 32 * kORow * 4 <= kBarOff - kKRingOff), "O in the ring");
   static constexpr uint32_t kTileCols = 256;
   static constexpr uint32_t kTmemCols = QT * kTileCols;
   static constexpr uint32_t kOCol = kBufs * kKeys;
@@ -283,34 +286,14 @@ struct PageTile {
   }
 };
 
-// 16 consecutive 32-bit columns of this thread's lane, waited for.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void tmem_ld_row(uint32_t addr, uint32_t (&r)[N]) {
-  if constexpr (N == 128) tmem_ld128(addr, r);
-  else if constexpr (N == 64) tmem_ld64(addr, r);
-  else tmem_ld16(addr, r);
-}
-
-template <typename T, int D, int QT, bool KV8, bool SPLIT>
-__global__ void __launch_bounds__(CrossTcCfg<T, D, QT, KV8, SPLIT>::kThreads, QT == 2 ? 1 : 2)
+template <typename T, int D, int QT, bool KV8>
+__global__ void __launch_bounds__(CrossTcCfg<T, D, QT, KV8>::kThreads, QT == 2 ? 1 : 2)
 cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ CUtensorMap tmk,
                 const __grid_constant__ CUtensorMap tmv) {
-  using Cfg = CrossTcCfg<T, D, QT, KV8, SPLIT>;
+  using Cfg = CrossTcCfg<T, D, QT, KV8>;
   using Op = typename Cfg::Op;
   constexpr int KT = Cfg::kKeys, NS = Cfg::kBufs;
   constexpr int NK = Cfg::kKSlots, NV = Cfg::kVSlots, RAW = Cfg::kRawSlots;
-  constexpr int LK = Cfg::kLaneKeys;
   extern __shared__ __align__(1024) unsigned char cross_smem[];
   unsigned char* const smem = cross_smem;
   const uint32_t sbase = smem_addr(smem);
@@ -324,6 +307,7 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
   const int row_tiles = (int)gridDim.x / p.kv_heads;
   const int kvh = blockIdx.x / row_tiles, tile = blockIdx.x % row_tiles;
   const int H = p.num_heads, G = p.group, b = p.block_size;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge's set-up
   const CrossSeq c = cross_seq(p, s);
   T* const out = static_cast<T*>(p.out);
   if (c.bits) {
@@ -350,7 +334,7 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
   const int32_t* trow = p.tables + (int64_t)s * p.max_blocks;
   const int lo = part * p.part, hi = min(c.L, lo + p.part);
   const int n_tiles = (hi - lo + KT - 1) / KT;
-  const int row_n = !SPLIT && nr > 128 ? 2 : 1;  // row tiles with rows
+  const int row_n = nr > 128 ? 2 : 1;  // row tiles with rows
 
   // ---- barriers, tensor memory, Q ---------------------------------------------
   const uint32_t bar0 = sbase + Cfg::kBarOff;
@@ -367,15 +351,14 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
   constexpr int B1 = 2 * NK + 2 * NV + 4 * RAW;
   auto s_full = [&](int t, int i) { return bar0 + 8u * (B1 + t * NS + i); };
   auto p_full = [&](int t, int i) { return bar0 + 8u * (B1 + QT * NS + t * NS + i); };
-  // P.V(j) done, every j (two S buffers only: with one, S(j + 1) says so), and
-  // the last one
+  // P.V(j) done, every j, and the last one
   auto o_done = [&](int t) { return bar0 + 8u * (B1 + 2 * QT * NS + t); };
   auto o_last = [&](int t) { return bar0 + 8u * (B1 + 2 * QT * NS + QT + t); };
   const uint32_t q_full = bar0 + 8u * (B1 + 2 * QT * NS + 2 * QT);
   auto drain = [&](int t) { return q_full + 8u * (1 + t); };
   const uint32_t checked = q_full + 8u * (1 + QT);  // the table row
   auto tile_warps = [&](int t) {  // softmax warps with rows of row tile t
-    return SPLIT ? 4 : min(4, max(0, (nr - t * 128 + 31) / 32));
+    return min(4, max(0, (nr - t * 128 + 31) / 32));
   };
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) {
@@ -419,7 +402,7 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
   bool failed = false;
   // Softmax thread: lane rr of row tile t, row r of the block.  It brings its
   // Q row while the first tiles are on their way.
-  const int t = warp >> 2, rr = (warp & 3) * 32 + lane, r = SPLIT ? lane : t * 128 + rr;
+  const int t = warp >> 2, rr = (warp & 3) * 32 + lane, r = t * 128 + rr;
   const bool softmax = warp < Cfg::kSoftmaxWarps && (warp & 3) < tile_warps(t);
   float qscale = 1.f;
   if (softmax) {
@@ -518,7 +501,7 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
         for (int kk = 0; kk < KT / 16; ++kk)
           tc_mma_ts(base + Cfg::kOCol, base + buf * KT + 8 * kk, vb + (2 * Cfg::kGroupBytes >> 4) * kk, Cfg::kIdescPV,
                     (j > 0 || kk > 0) ? 1u : 0u);
-        if (NS > 1) tc_commit(o_done(tt));
+        tc_commit(o_done(tt));
         if (j == n_tiles - 1) tc_commit(o_last(tt));
         tc_commit(v_empty(va.slot));
         va.next();
@@ -592,17 +575,17 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       }
       tc_fence_after();
       const uint32_t sp = base + (j % NS) * KT;
-      uint32_t w[LK];
-      tmem_ld_row<LK>(sp + (SPLIT ? warp * LK : 0), w);
-      const int valid = hi - lo - j * KT - (SPLIT ? warp * LK : 0);
-      if (valid < LK) {
+      uint32_t w[KT];
+      tmem_ld64(sp, w);
+      const int valid = hi - lo - j * KT;
+      if (valid < KT) {
 #pragma unroll
-        for (int k = 0; k < LK; ++k)
+        for (int k = 0; k < KT; ++k)
           if (k >= valid) w[k] = __float_as_uint(-INFINITY);
       }
       float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int k = 0; k < LK; k += 8)
+      for (int k = 0; k < KT; k += 8)
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           mq[u] = max3(mq[u], __uint_as_float(w[k + 2 * u]), __uint_as_float(w[k + 2 * u + 1]));
@@ -620,16 +603,14 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
           m = mx;
         }
       }
-      // A quarter whose keys so far all lie past the states has m = -inf.
-      const float ref = SPLIT && m == -INFINITY ? 0.f : m;
       // 2^(s * scale - m + bias) in pairs, its sum, and P over S's columns
       const float2 qs2 = make_float2(qscale, qscale);
-      const float2 nm2 = make_float2(Cfg::kBias - ref, Cfg::kBias - ref);
+      const float2 nm2 = make_float2(Cfg::kBias - m, Cfg::kBias - m);
       float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                         make_float2(0.f, 0.f)};
-      uint32_t pk[LK / 2];
+      uint32_t pk[KT / 2];
 #pragma unroll
-      for (int k = 0; k < LK; k += 2) {
+      for (int k = 0; k < KT; k += 2) {
         const float2 a = __ffma2_rn(make_float2(__uint_as_float(w[k]), __uint_as_float(w[k + 1])),
                                     qs2, nm2);
         const float2 e = make_float2(ex2(a.x), ex2(a.y));
@@ -639,16 +620,7 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       const float2 s01 = __fadd2_rn(sum2[0], sum2[1]), s23 = __fadd2_rn(sum2[2], sum2[3]);
       const float2 sx = __fadd2_rn(s01, s23);
       l += sx.x + sx.y;
-      if constexpr (SPLIT) {  // zeros for the other quarters' keys
-        uint32_t row[KT / 2];
-#pragma unroll
-        for (int k = 0; k < KT / 2; ++k) row[k] = k / (LK / 2) == warp ? pk[k % (LK / 2)] : 0u;
-        tmem_st32(sp, row);
-      } else if constexpr (KT == 128) {
-        tmem_st64(sp, pk);
-      } else {
-        tmem_st32(sp, pk);
-      }
+      tmem_st32(sp, pk);
       if (!KV8 && hi - lo - j * KT < KT) {  // (the last tile)
         ok = mbar_wait(v_full(j % NV), (uint32_t)((j / NV) & 1));
         if (__any_sync(kFullMask, !ok)) {
@@ -659,10 +631,9 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
         clear_tail<D, KT>(smem + Cfg::kVRingOff + (j % NV) * Cfg::kTileBytes, hi - lo - j * KT, b, rr,
                           32 * tile_warps(t));
       }
-      // P.V(j - 1) has been added to O before O or its factor changes.  With
-      // one S buffer it was, before S(j) was made; with two, every phase is
-      // waited for in turn.
-      if (NS > 1 && j > 0) {
+      // P.V(j - 1) has been added to O before O or its factor changes (and
+      // every phase of its barrier is waited for in turn).
+      if (j > 0) {
         ok = mbar_wait(o_done(t), (uint32_t)((j - 1) & 1));
         if (__any_sync(kFullMask, !ok)) {
           ok = false;
@@ -696,66 +667,7 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
     if (bad && tid == 0) set_error(p.err, PKV_DEV_TABLE_RANGE);
     const float vs = KV8 ? p.v_scale[kvh] : 1.f;
     const bool whole = c.parts == 1;
-    if constexpr (SPLIT) {
-      // Joins the quarters: O * 2^(m - M) to shared memory, summed by row.
-      float2* ml = reinterpret_cast<float2*>(smem);
-      float* os = reinterpret_cast<float*>(smem + Cfg::kKRingOff);
-      ml[tid] = make_float2(m, l);
-      named_bar_sync(1, 128);
-      float M = -INFINITY;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) M = fmaxf(M, ml[q * 32 + lane].x);
-      const float f = m == -INFINITY ? 0.f : ex2(m - M);
-      if (ok) tc_fence_after();
-#pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t w[32];
-        tmem_ld32(base + Cfg::kOCol + q * 32, w);
-        if (lane < nr) {
-#pragma unroll
-          for (int v = 0; v < 8; ++v)
-            *reinterpret_cast<float4*>(os + tid * Cfg::kORow + q * 32 + v * 4) =
-                make_float4(__uint_as_float(w[4 * v]) * f, __uint_as_float(w[4 * v + 1]) * f,
-                            __uint_as_float(w[4 * v + 2]) * f, __uint_as_float(w[4 * v + 3]) * f);
-        }
-      }
-      named_bar_sync(1, 128);
-      for (int e = tid; e < nr * (D / 8); e += 128) {
-        const int row = e / (D / 8), d = e % (D / 8) * 8;
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) top = fmaxf(top, ml[q * 32 + row].x);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 x = ml[q * 32 + row];
-          sum += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - top);
-        }
-        const float inv = bad ? 0.f : vs / sum;
-        float o[8] = {};
-#pragma unroll
-        for (int q = 0; q < 4 && !bad; ++q) {
-          const float4* x = reinterpret_cast<const float4*>(os + (q * 32 + row) * Cfg::kORow + d);
-          const float4 x0 = x[0], x1 = x[1];
-          o[0] += x0.x; o[1] += x0.y; o[2] += x0.z; o[3] += x0.w;
-          o[4] += x1.x; o[5] += x1.y; o[6] += x1.z; o[7] += x1.w;
-        }
-        const int64_t at = row_at(row);
-        if (ok && whole) {
-          uint4 u;
-          u.x = pack_pair<T>(o[0] * inv, o[1] * inv);
-          u.y = pack_pair<T>(o[2] * inv, o[3] * inv);
-          u.z = pack_pair<T>(o[4] * inv, o[5] * inv);
-          u.w = pack_pair<T>(o[6] * inv, o[7] * inv);
-          *reinterpret_cast<uint4*>(out + at + d) = u;
-        } else if (ok) {
-          const int64_t wrow = at / D * p.parts + part;
-          if (d == 0) p.ws_ml[wrow] = bad ? make_float2(-INFINITY, 0.f) : make_float2(top, sum);
-          float4* dst = reinterpret_cast<float4*>(p.ws_o + wrow * D + d);
-          dst[0] = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-          dst[1] = make_float4(o[4] * inv, o[5] * inv, o[6] * inv, o[7] * inv);
-        }
-      }
-    } else if (ok) {
+    if (ok) {
       tc_fence_after();
       const float inv = vs / l;
       const int64_t at = row_at(min(r, nr - 1));
@@ -766,8 +678,7 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
         uint32_t w[32];
         tmem_ld32(base + Cfg::kOCol + q * 32, w);
         auto o = [&](int d) { return bad ? 0.f : __uint_as_float(w[d]) * inv; };
-        if (r >= nr) continue;
-        if (whole) {
+        if (r < nr && whole) {
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint4 u;
@@ -777,7 +688,7 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
             u.w = pack_pair<T>(o(8 * v + 6), o(8 * v + 7));
             reinterpret_cast<uint4*>(out + at)[q * 4 + v] = u;
           }
-        } else {
+        } else if (r < nr) {
 #pragma unroll
           for (int v = 0; v < 8; ++v)
             reinterpret_cast<float4*>(p.ws_o + wrow * D)[q * 8 + v] =
@@ -794,10 +705,10 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
   if (warp == Cfg::kMmaWarp) tmem_dealloc(tmem, Cfg::kTmemCols);
 }
 
-template <typename T, int D, int QT, bool KV8, bool SPLIT>
+template <typename T, int D, int QT, bool KV8>
 int launch_cross_tc(const CrossParams& p, int num_seqs, const CrossMaps& maps, cudaStream_t stream) {
-  using Cfg = CrossTcCfg<T, D, QT, KV8, SPLIT>;
-  auto kern = cross_tc_kernel<T, D, QT, KV8, SPLIT>;
+  using Cfg = CrossTcCfg<T, D, QT, KV8>;
+  auto kern = cross_tc_kernel<T, D, QT, KV8>;
   static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use its shared memory
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
@@ -814,9 +725,5 @@ int launch_cross_tc(const CrossParams& p, int num_seqs, const CrossMaps& maps, c
   kern<<<grid, Cfg::kThreads, Cfg::kSmemBytes, stream>>>(p, maps.k, maps.v);
   return launch_cross_merge<T, D>(p, num_seqs, stream);
 }
-
-// Rows of a thread block: 32 (each on four lanes), 128, or 256; or 32 in one
-// balanced stream over all sequences (cross_stream.cuh).
-enum class CrossRows { kStream, k32, k128, k256 };
 
 }  // namespace pkv

@@ -356,9 +356,9 @@ def test_no_sequences_and_no_queries():
 @pytest.mark.parametrize("dtype,D,G", [(BF16, 128, 4), (F16, 64, 1), (FP8, 128, 8)])
 @pytest.mark.parametrize("seqs,longest,seed", [(1, 64, 0), (2, 65, 1), (7, 700, 2), (40, 3000, 3),
                                                (400, 130, 4), (1024, 90, 5), (1100, 70, 6)])
-def test_streams_of_ragged_sequences(dtype, D, G, seqs, longest, seed):
-    """Few rows: boundaries between blocks fall anywhere in and between
-    sequences, some without states, some without queries; many sequences."""
+def test_ragged_batches_of_few_rows(dtype, D, G, seqs, longest, seed):
+    """Few rows per sequence, some sequences without states, some without
+    queries; few long ones (split states) and many short ones."""
     rng = np.random.default_rng(seed)
     lens = [int(x) for x in rng.integers(0, longest + 1, seqs)]
     lens[0] = longest
