@@ -348,8 +348,8 @@ int paged_attention_prefill(const pkv_cache* cache, const void* q, int64_t total
  *                 most 2^30
  *   workspace     device, >= paged_attention_cross_workspace_bytes(...) with
  *                 the same arguments (max_enc_len there is the bound itself,
- *                 not 0), 16-byte aligned; may be NULL when that is 0.  Calls
- *                 that may overlap need one each.
+ *                 not 0) on the same device, 16-byte aligned; may be NULL
+ *                 when that is 0.  Calls that may overlap need one each.
  *
  * A sequence with Q > max_queries or L outside [0, max_enc_len] gets zero
  * rows and PKV_DEV_SEQ_LEN, one whose used table entries leave
@@ -542,6 +542,7 @@ int paged_block_swap(const pkv_cache* cache, void* host_k, void* host_v, int64_t
  * ring and tables stay as they were, query_starts is all zeros and every
  * token is padding.
  *
+ *   num_blocks      1 .. 2^30
  *   free_list       device, int32[num_blocks]: a ring of block ids; updated
  *                   in place (only behind the tail)
  *   free_state      device, int64[2] {head, count}: the free blocks are

@@ -510,8 +510,10 @@ def paged_build_tables(free_list, free_state, old_lens, new_lens, block_tables, 
             return paged_build_tables(free_list, free_state, old_lens, new_lens, block_tables,
                                       block_size, max_tokens, seq_lens, free_state_out, query_starts,
                                       slot_mapping, positions)
-    seq_lens = _output(seq_lens, "seq_lens", n, torch.int32, dev)
-    free_state_out = _output(free_state_out, "free_state_out", 2, torch.int64, dev)
+    seq_lens = torch.empty_like(old_lens) if seq_lens is None else \
+        _output(seq_lens, "seq_lens", n, torch.int32, dev)
+    free_state_out = torch.empty_like(free_state) if free_state_out is None else \
+        _output(free_state_out, "free_state_out", 2, torch.int64, dev)
     query_starts = _output(query_starts, "query_starts", n + 1, torch.int32, dev)
     slot_mapping = _output(slot_mapping, "slot_mapping", max_tokens, torch.int64, dev)
     positions = _output(positions, "positions", max_tokens, torch.int32, dev)

@@ -3,6 +3,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -543,9 +544,15 @@ CrossPlan cross_plan(const pkv_cache* c, int num_seqs, int num_heads, int max_qu
           (c->dtype == PKV_FP8_E4M3 && c->head_dim == 128);
   const int64_t rows = (int64_t)max_queries * (num_heads / c->num_kv_heads);
   pl.wide = c->dtype == PKV_FP8_E4M3 && rows > 128;
+  static std::atomic<int> sm_count[kMaxDevices];  // looked up once per device
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) {
+    sms = sm_count[dev].load();
+    if (sms == 0 &&
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && sms > 0)
+      sm_count[dev].store(sms);
+  }
+  if (sms < 1) {  // without a device nothing is split
     cudaGetLastError();
     sms = 1;
   }

@@ -18,9 +18,11 @@
 // replace the inputs (seq_lens over old_lens, the ring's state in place).
 //
 // What bounds it: latency.  The bytes (12 per token, 4 per moved block) are
-// a few microseconds of one SM's store rate at most; the chain lengths ->
-// prefix sums -> ring entries -> stores is two dependent loads and one
-// barrier.
+// nothing; the chain is lengths -> prefix sums -> ring entries -> barrier ->
+// stores, and the instructions on it count (32-bit saturating sums and
+// division by multiplication took 8 rows from 4.8 to 3.7 us).  Measured, in a
+// graph: 8 rows of one token 3.7 us; 256 rows with arrivals and releases, slot
+// map of 16384, 8.6 us; 1024 prompts of 262144 tokens 13.4 us.
 #include <algorithm>
 
 #include <cooperative_groups.h>

@@ -13,9 +13,14 @@
 // What bounds it: HBM traffic (q, k and v in, q and the pool rows out), and
 // latency for a decode step's few tokens.  The angles of a token serve all of
 // its query and key heads, so a thread block computes them once into shared
-// memory and then streams heads through 16-byte loads and stores, the first
-// of them issued before the angles are computed.
+// memory and then streams heads through 16-byte loads and stores.  One wave of
+// persistent blocks walks runs of tokens with the next unit's loads always in
+// flight.  Measured (bf16, 32/8 heads of 128, three axes, 8192 tokens, 201 MB):
+// 36 us, 5.6 TB/s, 82% of the copy rate; the instructions per unit and the
+// registers (64: four blocks per SM) set it.  With 72 registers and places
+// divided out it took 38.6 us, without the loads in flight 47.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <type_traits>
@@ -268,15 +273,23 @@ int launch_rope(RopeParams& p, cudaStream_t stream) {
   auto kern = single ? rope_write_kernel<TI, FP8, false, 1>
               : inter ? rope_write_kernel<TI, FP8, true, V>
                       : rope_write_kernel<TI, FP8, false, V>;
-  int dev = 0, sms = 0, per_sm = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kRopeThreads, 0) != cudaSuccess ||
-      sms < 1 || per_sm < 1)
-    return PKV_ERR_CUDA;
+  // Blocks that run at a time, per device and variant (looked up once).
+  static std::atomic<int> running[64][3];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+  std::atomic<int>& known = running[dev & 63][single ? 0 : inter ? 1 : 2];
+  int slots = known.load();
+  if (slots == 0) {
+    int sms = 0, per_sm = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kRopeThreads, 0) != cudaSuccess ||
+        sms < 1 || per_sm < 1)
+      return PKV_ERR_CUDA;
+    slots = sms * per_sm;
+    known.store(slots);
+  }
   // One wave of blocks, each with an equal run of tokens; few tokens share
   // their heads among the blocks that are left.
-  const int64_t slots = (int64_t)sms * per_sm;
   const int64_t x = std::min<int64_t>(p.num_tokens, slots);
   const int lanes = kRopeThreads / p.units;
   const int64_t passes = (p.heads + 2 * (int64_t)p.kv_heads + lanes - 1) / lanes;  // of one token
