@@ -441,13 +441,14 @@ int pkv_launch_build_tables(pkv::BuildParams p, cudaStream_t stream) {
   attr.val.clusterDim.x = (unsigned)cluster;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, build_tables_kernel, p) != cudaSuccess) return PKV_ERR_CUDA;
   if (p.fill) return PKV_OK;
   const int64_t per = kFillThreads * kGroup;
   cfg.gridDim = dim3((unsigned)((p.max_tokens + per - 1) / per));
   cfg.blockDim = dim3(kFillThreads);
   cfg.dynamicSmemBytes = std::min(p.num_seqs, kFillRows) * sizeof(int);
+  cfg.numAttrs = 1;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   return cudaLaunchKernelEx(&cfg, fill_slots_kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
