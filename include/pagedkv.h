@@ -334,7 +334,11 @@ int paged_attention_prefill(const pkv_cache* cache, const void* q, int64_t total
  * fp16, bf16, fp32 and FP8 pools; head_dim, block_size and head grouping as
  * for paged_attention_decode.  fp16 and bf16 pools, and FP8 pools of
  * head_dim 128, run on tensor cores, where probabilities are rounded to the
- * 16-bit operand type (bf16 pools: bf16; others: fp16) and sums are not.
+ * 16-bit operand type (bf16 pools: bf16; others: fp16) and sums are not
+ * (num_blocks * num_kv_heads must be below 2^31 - 1 there).  A NaN or an
+ * infinity among a sequence's states reaches every query of the sequence, as
+ * in the formula; what lies behind the states, in their last block too, does
+ * not count.
  *
  *   q, out        device, [total_queries][num_heads][head_dim], cache dtype
  *                 (io_dtype for FP8 pools)

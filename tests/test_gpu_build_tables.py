@@ -79,7 +79,8 @@ def same(m, d, got, want):
 
 @pytest.mark.parametrize("rows,b,longest,steps,in_place", [
     (1, 16, 70, 12, True), (3, 8, 40, 20, False), (13, 1, 9, 12, True), (64, 16, 300, 8, True),
-    (257, 32, 200, 6, False), (1025, 16, 50, 4, True), (3000, 8, 30, 4, True)])
+    (257, 32, 200, 6, False), (1025, 16, 50, 4, True), (3000, 8, 30, 4, True),
+    (40, 7, 100, 8, True), (300, 1000, 5000, 4, False), (5, 33, 400, 10, True)])
 def test_random_steps(rows, b, longest, steps, in_place):
     """Rows grow, shrink, start and end in one call; the ring wraps."""
     rng = np.random.default_rng(rows * 31 + b)

@@ -194,6 +194,48 @@ def test_large_batches():
     assert pkv.paged_get_device_error() == 0
 
 
+def test_largest_batch():
+    """65535 sequences of one query each over 0 to 3 states."""
+    n = 65535
+    lens = [int(x) for x in np.random.default_rng(2).integers(0, 4, n)]
+    c = Case([1] * n, lens, 2, 1, 64, F16, b=8, seed=30)
+    out = c.call()
+    c.check(out, [*range(0, 40), *range(n - 40, n)])
+    empty = torch.tensor(lens) == 0
+    assert (out.cpu()[empty] == 0).all() and (out.cpu()[~empty].abs().amax((1, 2)) > 0).all()
+    assert pkv.paged_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (F16, 64), (FP8, 128), (F32, 64)])
+def test_infinite_states_stay_in_their_sequence(dtype, D):
+    """An infinity or a NaN among one sequence's states reaches its own rows
+    and no other's, though they share blocks of the GPU and pages of the pool."""
+    c = Case([5, 5, 5], [70, 130, 40], 4, 2, D, dtype, F16 if dtype == FP8 else None, seed=31)
+    blk = int(c.tables[1, 2])
+    c.kv[1].view({1: torch.uint8, 2: torch.int16, 4: torch.int32}[c.kv[1].element_size()])[
+        blk, :, 3] = {F32: 0x7FC00000, F16: 0x7E00, BF16: 0x7FC0, FP8: 0x7F}[dtype]
+    out = c.call()
+    c.check(out, [0, 2])
+    assert torch.isnan(out[5:10]).all()
+
+
+def test_queries_in_any_order_of_calls():
+    """A second call with other lengths on the same buffers leaves nothing of
+    the first behind (workspace, outputs)."""
+    c = Case([2, 1], [5000, 3000], 8, 2, 128, BF16, seed=32)
+    cache = c.cache()
+    need = pkv.paged_attention_cross_workspace_bytes(cache, 3, 2, 8, 2, c.width * 16)
+    ws, out = torch.full((need,), 255, dtype=torch.uint8, device="cuda"), torch.empty_like(c.q).cuda()
+    c.check(c.call(cache, workspace=ws, out=out))
+    full = c.lens
+    for lens in ([1000, 0], [0, 3000], [64, 1], [4999, 2999]):
+        c.lens = lens
+        c.check(c.call(cache, workspace=ws, out=out))
+    c.lens = full
+    c.check(c.call(cache, workspace=ws, out=out))
+    assert pkv.paged_get_device_error() == 0
+
+
 @pytest.mark.parametrize("dtype,D", [(BF16, 128), (F32, 64), (FP8, 128)])
 def test_rows_behind_the_last_sequence_stay(dtype, D):
     c = Case([3, 4], [50, 60], 4, 2, D, dtype, BF16 if dtype == FP8 else None, seed=11, extra_rows=5)

@@ -134,6 +134,13 @@ def test_far_and_negative_positions(far, lo):
     run_case(33, 4, 2, 64, 64, 1, False, F32, F32, 16, far, lo=lo, seed=3)
 
 
+def test_block_sizes_axes_and_long_prompts():
+    run_case(70, 3, 3, 64, 64, 8, True, F16, F16, 5, 700, seed=21, padded=3)      # any block size
+    run_case(70, 3, 3, 64, 64, 8, False, F32, F32, 1, 700, seed=22)
+    run_case(60001, 2, 1, 64, 64, 2, False, BF16, BF16, 16, 60000, seed=23, padded=77)
+    run_case(300, 129, 2, 128, 32, 1, False, F16, F16, 16, 700, seed=24)         # many query heads
+
+
 def test_in_place_and_strided_rows():
     run_case(50, 8, 2, 128, 128, 3, False, BF16, BF16, 16, 999, stride_pad=8, in_place=True, seed=4)
     run_case(50, 8, 2, 64, 64, 1, True, F16, F16, 16, 999, stride_pad=64, in_place=True, seed=5)
