@@ -76,8 +76,8 @@ struct CrossTcCfg {
   static constexpr int kValueWarp = kSoftmaxWarps + 1;
   static constexpr int kMmaWarp = kSoftmaxWarps + 2;        // one per row tile
   static constexpr int kConvWarp = kMmaWarp + QT;
-  static constexpr int kConvThreads = KV8 ? 128 : 0;
-  static constexpr int kThreads = kConvWarp * 32 + kConvThreads;
+  static constexpr int kConvThreads = KV8 ? 64 : 0;         // for keys, and for values
+  static constexpr int kThreads = kConvWarp * 32 + 2 * kConvThreads;
   static constexpr int kKRingOff = QT * kQBytes;
   static constexpr int kVRingOff = kKRingOff + kKSlots * kTileBytes;
   static constexpr int kRawOff = kVRingOff + kVSlots * kTileBytes;  // K, then V
@@ -522,43 +522,32 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
   } else if (KV8 && warp >= Cfg::kConvWarp) {
     // ---- converters: codes to fp16, one slot of the ring at a time --------------
     if constexpr (KV8) {
-      const int ct = tid - Cfg::kConvWarp * 32;
-      // In the order of use: the first NS K tiles, then V(j) and K(j + NS).
-      RingPos<RAW> kr, vr;
-      RingPos<NK> ka;
-      RingPos<NV> va;
-      for (int kj = 0, vj = 0; vj < n_tiles;) {
-        const bool key = kj < n_tiles && kj < vj + NS;
-        bool ok;
-        if (key) {
-          ok = mbar_wait(raw_full(0, kr.slot), kr.phase);
-          if (ok && kj >= NK) ok = mbar_wait(k_empty(ka.slot), ka.phase ^ 1u);
-        } else {
-          ok = mbar_wait(raw_full(1, vr.slot), vr.phase);
-          if (ok && vj >= NV) ok = mbar_wait(v_empty(va.slot), va.phase ^ 1u);
-        }
+      // Two warps for keys and two for values, so that neither waits for the
+      // other's slots.
+      const int which = (warp - Cfg::kConvWarp) >> 1, ct = tid & 63;
+      const int slots = which ? NV : NK;
+      const uint32_t fulls = which ? v_full(0) : k_full(0), empties = which ? v_empty(0) : k_empty(0);
+      unsigned char* const ring = smem + (which ? Cfg::kVRingOff : Cfg::kKRingOff);
+      RingPos<RAW> from;
+      int slot = 0;
+      uint32_t phase = 0;
+      for (int j = 0; j < n_tiles; ++j) {
+        bool ok = mbar_wait(raw_full(which, from.slot), from.phase);
+        if (ok && j >= slots) ok = mbar_wait(empties + 8u * slot, phase ^ 1u);
         if (__any_sync(kFullMask, !ok)) {
           failed = true;
           break;
         }
-        const unsigned char* raw =
-            smem + Cfg::kRawOff + (key ? kr.slot : RAW + vr.slot) * Cfg::kRawBytes;
-        unsigned char* dst = smem + (key ? Cfg::kKRingOff + ka.slot * Cfg::kTileBytes
-                                         : Cfg::kVRingOff + va.slot * Cfg::kTileBytes);
-        widen_tile<KT, Cfg::kConvThreads>(raw, dst, key ? KT : hi - lo - vj * KT, ct);
+        widen_tile<KT, Cfg::kConvThreads>(
+            smem + Cfg::kRawOff + (which * RAW + from.slot) * Cfg::kRawBytes,
+            ring + slot * Cfg::kTileBytes, which ? hi - lo - j * KT : KT, ct);
         fence_proxy_async_smem();
-        if (key) {
-          mbar_arrive(k_full(ka.slot));
-          mbar_arrive(raw_empty(0, kr.slot));
-          kr.next();
-          ka.next();
-          ++kj;
-        } else {
-          mbar_arrive(v_full(va.slot));
-          mbar_arrive(raw_empty(1, vr.slot));
-          vr.next();
-          va.next();
-          ++vj;
+        mbar_arrive(fulls + 8u * slot);
+        mbar_arrive(raw_empty(which, from.slot));
+        from.next();
+        if (++slot == slots) {
+          slot = 0;
+          phase ^= 1u;
         }
       }
     }
