@@ -178,22 +178,31 @@ __device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const 
 template <int KEYS, int THREADS>
 __device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned char* dst, int valid,
                                            int thread) {
+  constexpr int kUnits = KEYS * 8 / THREADS, kBatch = 4;  // (four loads in flight: 164 -> 154 us)
+  static_assert(kUnits % kBatch == 0, "whole batches");
+#pragma unroll 1
+  for (int u0 = 0; u0 < kUnits; u0 += kBatch) {
+    uint4 x[kBatch];
 #pragma unroll
-  for (int u = 0; u < KEYS * 8 / THREADS; ++u) {
-    const int unit = thread + u * THREADS;
-    const int row = unit >> 3, ch = unit & 7;
-    uint4 a = make_uint4(0u, 0u, 0u, 0u), z = a;
-    if (row < valid) {
-      const uint4 x = *reinterpret_cast<const uint4*>(raw + row * 128 + ((ch ^ (row & 7)) << 4));
-      e4m3x4_to_f16x4(x.x, a.x, a.y);
-      e4m3x4_to_f16x4(x.y, a.z, a.w);
-      e4m3x4_to_f16x4(x.z, z.x, z.y);
-      e4m3x4_to_f16x4(x.w, z.z, z.w);
+    for (int i = 0; i < kBatch; ++i) {
+      const int unit = thread + (u0 + i) * THREADS, row = unit >> 3, ch = unit & 7;
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < valid)
+        x[i] = *reinterpret_cast<const uint4*>(raw + row * 128 + ((ch ^ (row & 7)) << 4));
     }
-    const int c2 = (ch & 3) * 2;
-    unsigned char* drow = dst + (row >> 3) * 2048 + (ch >> 2) * 1024 + (row & 7) * 128;
-    *reinterpret_cast<uint4*>(drow + ((c2 ^ (row & 7)) << 4)) = a;
-    *reinterpret_cast<uint4*>(drow + (((c2 + 1) ^ (row & 7)) << 4)) = z;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int unit = thread + (u0 + i) * THREADS, row = unit >> 3, ch = unit & 7;
+      uint4 a, z;
+      e4m3x4_to_f16x4(x[i].x, a.x, a.y);
+      e4m3x4_to_f16x4(x[i].y, a.z, a.w);
+      e4m3x4_to_f16x4(x[i].z, z.x, z.y);
+      e4m3x4_to_f16x4(x[i].w, z.z, z.w);
+      const int c2 = (ch & 3) * 2;
+      unsigned char* drow = dst + (row >> 3) * 2048 + (ch >> 2) * 1024 + (row & 7) * 128;
+      *reinterpret_cast<uint4*>(drow + ((c2 ^ (row & 7)) << 4)) = a;
+      *reinterpret_cast<uint4*>(drow + (((c2 + 1) ^ (row & 7)) << 4)) = z;
+    }
   }
 }
 
