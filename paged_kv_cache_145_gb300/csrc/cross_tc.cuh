@@ -14,7 +14,8 @@
 //        memory), all of a tile's products from one thread, so that they run
 //        in the order of issue: S(j + 2) is issued right behind P.V(j), whose
 //        P it overwrites;
-//   FP8 pools: four converter warps between rings of codes and the others.
+//   FP8 pools: converter warps, two for K and two for V, between rings of codes
+//        and the others.
 // Two S buffers: S(j + 1) is made while the softmax works on S(j).  The
 // running maximum is raised lazily (by more than 2^kSlack, so that O is
 // rescaled rarely); sums, maxima and O are float32.  P is rounded to the
@@ -35,8 +36,9 @@
 // and lanes that each issue one do it one after the other (a copy costs its
 // thread about 90 cycles; the same four copies from four lanes took 1000).
 // FP8 pools keep 256 rows where a sequence has more than 128: widening each
-// tile costs more than the chain (8 x 300-512 queries over 1000-4000 states:
-// 194 us, 241 with 128 rows).
+// tile costs more than the chain (8 x 300-512 queries over 1000-4000 states,
+// 32/8 heads of 128: 154 us, 205 with blocks of 128 rows).  Two converter warps
+// for keys and two for values: 164 us, all four for one after the other 195.
 //
 // Tensor memory per row tile: two buffers of S (64 columns each, P in the first
 // 32), then O (D columns).  Every wait is bounded.
@@ -178,7 +180,9 @@ __device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const 
 template <int KEYS, int THREADS>
 __device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned char* dst, int valid,
                                            int thread) {
-  constexpr int kUnits = KEYS * 8 / THREADS, kBatch = 4;  // (four loads in flight: 164 -> 154 us)
+  // Eight loads in flight (8 x 300-512 queries over 1000-4000 states: one 164 us,
+  // four 154, eight 150).
+  constexpr int kUnits = KEYS * 8 / THREADS, kBatch = 8;
   static_assert(kUnits % kBatch == 0, "whole batches");
 #pragma unroll 1
   for (int u0 = 0; u0 < kUnits; u0 += kBatch) {
