@@ -335,10 +335,12 @@ int paged_attention_prefill(const pkv_cache* cache, const void* q, int64_t total
  * for paged_attention_decode.  fp16 and bf16 pools, and FP8 pools of
  * head_dim 128, run on tensor cores, where probabilities are rounded to the
  * 16-bit operand type (bf16 pools: bf16; others: fp16) and sums are not
- * (num_blocks * num_kv_heads must be below 2^31 - 1 there).  A NaN or an
- * infinity among a sequence's states reaches every query of the sequence, as
- * in the formula; what lies behind the states, in their last block too, does
- * not count.
+ * (num_blocks * num_kv_heads must be below 2^31 - 1 there).  Infinities and
+ * NaN among a sequence's states act as in the formula: a score of minus infinity
+ * has weight 0, a row with a score of plus infinity or NaN, or with no other
+ * scores than minus infinity, is NaN, and a value that is not finite reaches
+ * every query of the sequence (as NaN where its weight is 0 or rounds to it).
+ * What lies behind the states, in their last block too, does not count.
  *
  *   q, out        device, [total_queries][num_heads][head_dim], cache dtype
  *                 (io_dtype for FP8 pools)

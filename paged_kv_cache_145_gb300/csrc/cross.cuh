@@ -66,7 +66,10 @@ __device__ __forceinline__ CrossSeq cross_seq(const CrossParams& p, int s) {
 }
 
 // One warp per row: joins the parts of a sequence's rows.  With
-// M = max m_i, w_i = l_i 2^(m_i - M): out = sum w_i o_i / sum w_i.
+// M = max m_i, w_i = l_i 2^(m_i - M): out = sum w_i o_i / sum w_i.  A part
+// whose scores are all -inf has l = 0 and weighs nothing (its o is read all the
+// same: 0 times a NaN is one); where all parts are like that, out is 0 / 0.  The
+// parts of a sequence with a bad table have l = 1 and o = 0.
 constexpr int kCrossMergeWarps = 4;
 
 template <typename T, int D>
@@ -90,17 +93,16 @@ __global__ void __launch_bounds__(kCrossMergeWarps * 32) cross_merge_kernel(cons
     float w = 0.f;
     if (base + lane < c.parts) {
       const float2 x = ml[base + lane];
-      w = x.y > 0.f || x.y != x.y ? x.y * ex2(x.x - M) : 0.f;  // an empty part weighs nothing
+      w = x.y == 0.f ? 0.f : x.y * ex2(x.x - M);
     }
     const int n = min(32, c.parts - base);
     for (int i0 = 0; i0 < n; i0 += 8) {  // eight parts' loads in flight
       float f[8][E];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float wi = __shfl_sync(kFullMask, w, i0 + i);
 #pragma unroll
         for (int e = 0; e < E; ++e) f[i][e] = 0.f;
-        if (wi != 0.f) RowLoad<float, E>::load(o + (int64_t)(base + i0 + i) * D + lane * E, f[i]);
+        if (i0 + i < n) RowLoad<float, E>::load(o + (int64_t)(base + i0 + i) * D + lane * E, f[i]);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kCrossMergeWarps * 32) cross_merge_kernel(cons
       }
     }
   }
-  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  const float inv = 1.f / sum;
   T* dst = static_cast<T*>(p.out) + at * D + lane * E;
 #pragma unroll
   for (int e = 0; e < E; ++e) dst[e] = Elem<T>::from_f(acc[e] * inv);
@@ -240,20 +242,23 @@ __global__ void __launch_bounds__(kCrossWarps * 32) cross_kernel(const CrossPara
 #pragma unroll
     for (int w = 0; w < kCrossWarps; ++w) {
       const float2 x = s_ml[w][r];
-      if (x.x == -INFINITY && x.y == 0.f) continue;  // a warp without keys
+      // (a warp without keys, or whose scores are all -inf: 0)
       const float f = ex2(x.x - (M == -INFINITY ? 0.f : M));
       sum += x.y * f;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] += s_o[w][r][lane * E + e] * f;
     }
-    const float inv = sum != 0.f ? vs / sum : 0.f;
+    // No states, or a bad table: zeros.  sum = 0 else: every score was -inf,
+    // as in the tensor-core kernel NaN for a whole row, no weight for a part.
+    const bool none = bad || c.L == 0;
+    const float inv = none ? 0.f : sum == 0.f && c.parts > 1 ? vs : vs / sum;
     if (c.parts == 1) {
       T* dst = out + row_at(r) + lane * E;
 #pragma unroll
       for (int e = 0; e < E; ++e) dst[e] = Elem<T>::from_f(o[e] * inv);
     } else {
       const int64_t at = (row_at(r) / D) * p.parts + part;
-      if (lane == 0) p.ws_ml[at] = make_float2(M, sum);
+      if (lane == 0) p.ws_ml[at] = bad ? make_float2(0.f, 1.f) : make_float2(M, sum);
 #pragma unroll
       for (int e = 0; e < E; ++e) p.ws_o[at * D + lane * E + e] = o[e] * inv;
     }

@@ -605,9 +605,11 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
           m = mx;
         }
       }
-      // 2^(s * scale - m + bias) in pairs, its sum, and P over S's columns
+      // 2^(s * scale - m + bias) in pairs, its sum, and P over S's columns.
+      // While every score so far is -inf the weights are 2^-inf = 0.
+      const float neg_m = Cfg::kBias - (m == -INFINITY ? 0.f : m);
       const float2 qs2 = make_float2(qscale, qscale);
-      const float2 nm2 = make_float2(Cfg::kBias - m, Cfg::kBias - m);
+      const float2 nm2 = make_float2(neg_m, neg_m);
       float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                         make_float2(0.f, 0.f)};
       uint32_t pk[KT / 2];
@@ -671,10 +673,13 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
     const bool whole = c.parts == 1;
     if (ok) {
       tc_fence_after();
-      const float inv = vs / l;
+      // l = 0: every score was -inf.  A row of such scores is 0 / 0 (NaN); a
+      // part of them leaves O as it is, NaN where a value was not finite, and
+      // weighs nothing in the merge.
+      const float inv = l == 0.f && !whole ? vs : vs / l;
       const int64_t at = row_at(min(r, nr - 1));
       const int64_t wrow = at / D * p.parts + part;
-      if (!whole && r < nr) p.ws_ml[wrow] = bad ? make_float2(-INFINITY, 0.f) : make_float2(m, l);
+      if (!whole && r < nr) p.ws_ml[wrow] = bad ? make_float2(0.f, 1.f) : make_float2(m, l);
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
         uint32_t w[32];
