@@ -130,13 +130,18 @@ __device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const 
                                            unsigned char* tile, int rr) {
   const uint4* src = reinterpret_cast<const uint4*>(row);
   bool neg = p.qscale < 0.f;
-  float shrink = 1.f, qscale = fabsf(p.qscale);
+  float shift = 1.f, qscale = fabsf(p.qscale);
   if constexpr (KV8) {
-    qscale *= fabsf(p.k_scale[kvh]);
+    const float ks = fabsf(p.k_scale[kvh]);
     neg = neg != (p.k_scale[kvh] < 0.f);
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-      // bf16 rows enter as fp16; one that reaches 2^15 is first scaled by a
-      // power of two (exact), undone in the row's factor
+    if constexpr (!std::is_same<T, __nv_bfloat16>::value) {
+      qscale *= ks;
+    } else {
+      // bf16 rows enter as fp16, scaled by the power of two that brings the
+      // largest element to 2^14 .. 2^15 (2^126 at most): exact but for elements
+      // 2^29 times smaller.  The row's factor undoes it; its product is formed
+      // from mantissas and exponents, so that no step of it leaves float32's
+      // range unless the whole does.
       float amax = 0.f;
 #pragma unroll 4
       for (int i = 0; i < D / 8; ++i) {
@@ -147,12 +152,14 @@ __device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const 
           amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[k] << 16)),
                                    fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
       }
-      if (amax >= 32768.f && amax <= 3.0e38f) {
-        int e = 0;
-        frexpf(amax, &e);
-        shrink = ldexpf(1.f, 15 - e);
-        qscale = ldexpf(qscale, e - 15);
+      int e = 0, eq = 0, ek = 0;
+      if (amax > 0.f && amax < INFINITY) {
+        frexpf(amax, &e);  // amax < 2^e
+        e = min(15 - e, 126);
+        shift = ldexpf(1.f, e);
       }
+      const float mq = frexpf(qscale, &eq), mk = frexpf(ks, &ek);
+      qscale = ldexpf(mq * mk, eq + ek - e);
     }
   }
   // A zero scale becomes zero queries, so that hidden keys stay at -inf.
@@ -165,8 +172,8 @@ __device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const 
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if constexpr (KV8 && std::is_same<T, __nv_bfloat16>::value)
-        w[k] = pack_pair<__half>(__uint_as_float(w[k] << 16) * shrink,
-                                 __uint_as_float(w[k] & 0xFFFF0000u) * shrink);
+        w[k] = pack_pair<__half>(__uint_as_float(w[k] << 16) * shift,
+                                 __uint_as_float(w[k] & 0xFFFF0000u) * shift);
       if (neg) w[k] ^= 0x80008000u;
     }
     *reinterpret_cast<uint4*>(tile + (i >> 3) * 128 * 128 + rr * 128 +
