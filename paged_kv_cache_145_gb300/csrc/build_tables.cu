@@ -24,6 +24,7 @@
 // graph: 8 rows of one token 3.7 us; 256 rows with arrivals and releases, slot
 // map of 16384, 8.6 us; 1024 prompts of 262144 tokens 13.4 us.
 #include <algorithm>
+#include <atomic>
 
 #include <cooperative_groups.h>
 
@@ -70,6 +71,9 @@ struct BuildParams {
 constexpr int kBuildThreads = 512;
 constexpr int kBuildWarps = kBuildThreads / 32;
 constexpr int kBuildCluster = 8;  // the portable cluster size
+constexpr int kBuildMaxRows = 65535;
+// Row data of a thread block: five numbers for each of its rows.
+constexpr int build_smem(int share) { return share * 5 * (int)sizeof(int); }
 
 // Blocks taken, blocks given back and new tokens: of a row, of a run of
 // rows, or before a row.  Sums stop at kMany, above any count that passes
@@ -426,15 +430,24 @@ int pkv_launch_build_tables(pkv::BuildParams p, cudaStream_t stream) {
   p.fill = p.max_tokens <= 16384;
   p.vectors = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15u) == 0;
   p.share = (p.num_seqs + cluster - 1) / cluster;
-  const size_t smem = (size_t)p.share * 5 * sizeof(int);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess)
-    return PKV_ERR_CUDA;
+  // The most that any number of rows needs is asked for once per device and
+  // never less, so that no call takes it from a launch on another thread.
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load() & bit)) {
+    constexpr int kMost = build_smem((kBuildMaxRows + kBuildCluster - 1) / kBuildCluster);
+    static_assert(kMost <= 224 * 1024, "shared memory of a block");
+    if (cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMost) != cudaSuccess)
+      return PKV_ERR_CUDA;
+    ready.fetch_or(bit);
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)cluster);
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = build_smem(p.share);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -462,7 +475,7 @@ extern "C" int paged_build_tables(int64_t num_blocks, int32_t block_size, int32_
                                   int32_t* query_starts, int64_t* slot_mapping,
                                   int32_t* positions, int64_t max_tokens, cudaStream_t stream) {
   if (num_blocks < 1 || num_blocks > (1 << 30) || block_size < 1 || num_seqs < 0 ||
-      num_seqs > 65535 || max_blocks_per_seq < 1 || max_tokens < 0 || max_tokens > (1 << 30))
+      num_seqs > pkv::kBuildMaxRows || max_blocks_per_seq < 1 || max_tokens < 0 || max_tokens > (1 << 30))
     return PKV_ERR_ARG;
   if (!free_list || !free_state || !free_state_out || !query_starts) return PKV_ERR_NULL;
   if (num_seqs > 0 && (!old_lens || !new_lens || !block_tables || !seq_lens)) return PKV_ERR_NULL;
