@@ -196,8 +196,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
                                          &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
+        q != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
       f = nullptr;
+    }
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
   }();
   return fn;
@@ -230,11 +232,17 @@ bool encode_pool_map(CUtensorMap* map, const pkv_cache* c, void* base) {
 
 unsigned* pkv_error_word() {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    (void)cudaGetLastError();
+    return nullptr;
+  }
   std::lock_guard<std::mutex> lock(g_err_mu);
   if (!g_err_ptr[dev]) {
     void* ptr = nullptr;
-    if (cudaGetSymbolAddress(&ptr, g_pkv_error) != cudaSuccess) return nullptr;
+    if (cudaGetSymbolAddress(&ptr, g_pkv_error) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return nullptr;
+    }
     g_err_ptr[dev] = static_cast<unsigned*>(ptr);
   }
   return g_err_ptr[dev];
@@ -749,11 +757,11 @@ int paged_block_swap(const pkv_cache* cache, void* host_k, void* host_v, int64_t
 
 int paged_get_device_error(cudaStream_t stream, uint32_t* bits) {
   if (!bits) return PKV_ERR_NULL;
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaStreamSynchronize(stream) != cudaSuccess) return pkv_cuda_failed();
   unsigned v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_pkv_error, sizeof(v)) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaMemcpyFromSymbol(&v, g_pkv_error, sizeof(v)) != cudaSuccess) return pkv_cuda_failed();
   const unsigned zero = 0;
-  if (cudaMemcpyToSymbol(g_pkv_error, &zero, sizeof(zero)) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaMemcpyToSymbol(g_pkv_error, &zero, sizeof(zero)) != cudaSuccess) return pkv_cuda_failed();
   *bits = v;
   return PKV_OK;
 }

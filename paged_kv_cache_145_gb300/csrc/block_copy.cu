@@ -74,7 +74,7 @@ static int launch_move(const int64_t* pairs, int64_t num_pairs, const void* sk, 
       pairs, static_cast<const uint4*>(sk), static_cast<const uint4*>(sv), src_blocks,
       static_cast<uint4*>(dk), static_cast<uint4*>(dv), dst_blocks, block_vecs, same_pool,
       pkv_error_word());
-  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return pkv_launch_status();
 }
 
 int pkv_launch_block_copy(const pkv_cache* c, const int64_t* pairs, int64_t num_pairs,

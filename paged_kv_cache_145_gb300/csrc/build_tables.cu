@@ -434,14 +434,14 @@ int pkv_launch_build_tables(pkv::BuildParams p, cudaStream_t stream) {
   // never less, so that no call takes it from a launch on another thread.
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return pkv_cuda_failed();
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load() & bit)) {
     constexpr int kMost = build_smem((kBuildMaxRows + kBuildCluster - 1) / kBuildCluster);
     static_assert(kMost <= 224 * 1024, "shared memory of a block");
     if (cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kMost) != cudaSuccess)
-      return PKV_ERR_CUDA;
+      return pkv_cuda_failed();
     ready.fetch_or(bit);
   }
   cudaLaunchConfig_t cfg{};
@@ -455,7 +455,7 @@ int pkv_launch_build_tables(pkv::BuildParams p, cudaStream_t stream) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, build_tables_kernel, p) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, build_tables_kernel, p) != cudaSuccess) return pkv_cuda_failed();
   if (p.fill) return PKV_OK;
   const int64_t per = kFillThreads * kGroup;
   cfg.gridDim = dim3((unsigned)((p.max_tokens + per - 1) / per));
@@ -464,7 +464,7 @@ int pkv_launch_build_tables(pkv::BuildParams p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, fill_slots_kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, fill_slots_kernel, p) == cudaSuccess ? PKV_OK : pkv_cuda_failed();
 }
 
 extern "C" int paged_build_tables(int64_t num_blocks, int32_t block_size, int32_t* free_list,

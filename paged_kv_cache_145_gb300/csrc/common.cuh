@@ -263,3 +263,16 @@ struct CacheRow<__nv_fp8_e4m3, N> {
 
 // Host-side: address of the per-device error word (defined in api.cu).
 unsigned* pkv_error_word();
+
+// Host-side: the code for a runtime call that failed.  The runtime (linked into
+// the library, which has its error state to itself) keeps the error until it is
+// asked for; asking here keeps it from the launches of later calls.
+inline int pkv_cuda_failed() {
+  (void)cudaGetLastError();
+  return PKV_ERR_CUDA;
+}
+
+// Host-side: the code for the launches just made.
+inline int pkv_launch_status() {
+  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}

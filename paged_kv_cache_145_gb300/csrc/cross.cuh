@@ -278,9 +278,9 @@ int launch_cross_merge(const CrossParams& p, int num_seqs, cudaStream_t stream) 
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, cross_merge_kernel<T, D>, p) != cudaSuccess) return PKV_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, cross_merge_kernel<T, D>, p) != cudaSuccess) return pkv_cuda_failed();
   }
-  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return pkv_launch_status();
 }
 
 }  // namespace pkv

@@ -725,12 +725,12 @@ int launch_cross_tc(const CrossParams& p, int num_seqs, const CrossMaps& maps, c
   auto kern = cross_tc_kernel<T, D, QT, KV8>;
   static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use its shared memory
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return pkv_cuda_failed();
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load() & bit)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes) !=
         cudaSuccess)
-      return PKV_ERR_CUDA;
+      return pkv_cuda_failed();
     ready.fetch_or(bit);
   }
   const int64_t tiles = ((int64_t)p.max_queries * p.group + Cfg::kRows - 1) / Cfg::kRows;

@@ -30,12 +30,12 @@ template <typename Tag, typename K>
 int allow_smem(K kern, int bytes) {
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return pkv_cuda_failed();
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load() & bit)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
         cudaSuccess)
-      return PKV_ERR_CUDA;
+      return pkv_cuda_failed();
     ready.fetch_or(bit);
   }
   return PKV_OK;
@@ -76,7 +76,7 @@ int launch_decode_cfg(const DecodeParams& p, int num_seqs, const DecodeMaps* map
     kern<<<grid, Cfg::kThreads, Cfg::smem_bytes(p.part_size), stream>>>(p);
   }
   launch_reduce<T, D>(p, num_seqs, stream);
-  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return pkv_launch_status();
 }
 
 // Shared-prefix decode (16-bit pools): the groups' shared partitions, then
@@ -93,7 +93,7 @@ int launch_shared_dup(const DecodeParams& p, int max_group_size, const DecodeMap
   if (allow_smem<Cfg>(kern, Cfg::kSmemBytes) != PKV_OK) return PKV_ERR_CUDA;
   dim3 grid((unsigned)p.kv_heads, (unsigned)p.num_groups, (unsigned)(p.num_parts * row_blocks));
   kern<<<grid, Cfg::kThreads, Cfg::kSmemBytes, stream>>>(p, (int)row_blocks, maps->k, maps->v);
-  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return pkv_launch_status();
 }
 
 // Groups of at most 32 stacked rows (max_group_size x G) run with every row
@@ -109,7 +109,7 @@ int launch_shared_cfg(const DecodeParams& p, int num_seqs, int max_group_size,
   if (p.tail_parts == 1) {  // every tail in one partition: tail and merge in one pass
     decode_tail_merge_kernel<T, D, BS, G>
         <<<dim3((unsigned)p.kv_heads, (unsigned)num_seqs), 128, 0, stream>>>(p);
-    return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return pkv_launch_status();
   }
   return launch_decode_cfg<T, D, BS, G>(p, num_seqs, part_maps, stream);
 }
@@ -156,7 +156,7 @@ int launch_decode_fp8_cfg(const DecodeParams& p, int num_seqs, const DecodeMaps*
     kern<<<grid, Cfg::kThreads, Cfg::smem_bytes(p.part_size), stream>>>(p);
   }
   launch_reduce<T, D>(p, num_seqs, stream);
-  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return pkv_launch_status();
 }
 
 template <typename T>

@@ -36,8 +36,8 @@ void* static_ws_address() {
   if (!g_static_ptr[dev]) {
     void* ptr = nullptr;
     if (cudaGetSymbolAddress(&ptr, g_pkv_static_ws) != cudaSuccess || !ptr) {
-      // Clear the runtime's last error: the launchers judge their own
-      // launches with cudaPeekAtLastError and must not see this one.
+      // Clear the runtime's last error: the launchers judge their launches by
+      // it and must not see this one.
       (void)cudaGetLastError();
       return nullptr;
     }

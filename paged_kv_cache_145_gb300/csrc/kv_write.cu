@@ -112,7 +112,7 @@ int pkv_launch_kv_write_fp8(const pkv_cache* c, const void* k, const void* v,
     launch(pkv::kv_write_fp8_kernel<__half>);
   else
     launch(pkv::kv_write_fp8_kernel<__nv_bfloat16>);
-  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return pkv_launch_status();
 }
 
 int pkv_launch_kv_write(const pkv_cache* c, const void* k, const void* v, const int64_t* slots,
@@ -125,5 +125,5 @@ int pkv_launch_kv_write(const pkv_cache* c, const void* k, const void* v, const 
       static_cast<const uint4*>(k), static_cast<const uint4*>(v), slots,
       static_cast<uint4*>(c->k_cache), static_cast<uint4*>(c->v_cache), c->num_blocks,
       c->block_size, c->num_kv_heads, row_vecs, total, pkv_error_word());
-  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return pkv_launch_status();
 }

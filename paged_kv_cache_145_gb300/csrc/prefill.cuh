@@ -374,12 +374,12 @@ int launch_prefill_cfg(const PrefillParams& p, int num_seqs, const CUtensorMap& 
   auto kern = prefill_mma_kernel<T, D, BS, G>;
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return pkv_cuda_failed();
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load() & bit)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
         cudaSuccess)
-      return PKV_ERR_CUDA;
+      return pkv_cuda_failed();
     ready.fetch_or(bit);
   }
   const int smem = Cfg::smem_bytes(p.max_blocks);
@@ -387,7 +387,7 @@ int launch_prefill_cfg(const PrefillParams& p, int num_seqs, const CUtensorMap& 
   dim3 grid((unsigned)((p.max_queries + Cfg::kQueries - 1) / Cfg::kQueries), (unsigned)p.kv_heads,
             (unsigned)num_seqs);
   kern<<<grid, Cfg::kThreads, smem, stream>>>(p, mk, mv);
-  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return pkv_launch_status();
 }
 
 template <typename T, int D, int BS>

@@ -966,12 +966,12 @@ int launch_prefill_tc_cfg(const PrefillParams& p, int num_seqs, const CUtensorMa
   auto kern = prefill_tc_kernel<T, D, BS, G, KV8>;
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return pkv_cuda_failed();
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load() & bit)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Cfg::kSmemBytes) != cudaSuccess)
-      return PKV_ERR_CUDA;
+      return pkv_cuda_failed();
     ready.fetch_or(bit);
   }
   // One CTA per SM.  When the last wave would hold at most half the SMs'
@@ -982,7 +982,7 @@ int launch_prefill_tc_cfg(const PrefillParams& p, int num_seqs, const CUtensorMa
   int sms = sm_count[dev & 63].load();
   if (sms == 0) {
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-      return PKV_ERR_CUDA;
+      return pkv_cuda_failed();
     sm_count[dev & 63].store(sms);
   }
   PrefillParams q = p;
@@ -1000,7 +1000,7 @@ int launch_prefill_tc_cfg(const PrefillParams& p, int num_seqs, const CUtensorMa
   if (items + split > 0x7FFFFFFF) return PKV_ERR_GEOMETRY;
   q.n_full = (int)(items - split);
   kern<<<(unsigned)(items + split), Cfg::kThreads, Cfg::kSmemBytes, stream>>>(q, mk, mv);
-  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return pkv_launch_status();
 }
 
 template <typename T, int D, int BS, bool KV8>

@@ -276,7 +276,7 @@ int launch_rope(RopeParams& p, cudaStream_t stream) {
   // Blocks that run at a time, per device and variant (looked up once).
   static std::atomic<int> running[64][3];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return pkv_cuda_failed();
   std::atomic<int>& known = running[dev & 63][single ? 0 : inter ? 1 : 2];
   int slots = known.load();
   if (slots == 0) {
@@ -284,7 +284,7 @@ int launch_rope(RopeParams& p, cudaStream_t stream) {
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kRopeThreads, 0) != cudaSuccess ||
         sms < 1 || per_sm < 1)
-      return PKV_ERR_CUDA;
+      return pkv_cuda_failed();
     slots = sms * per_sm;
     known.store(slots);
   }
@@ -295,7 +295,7 @@ int launch_rope(RopeParams& p, cudaStream_t stream) {
   const int64_t passes = (p.heads + 2 * (int64_t)p.kv_heads + lanes - 1) / lanes;  // of one token
   const int64_t y = std::max<int64_t>(1, std::min<int64_t>(passes, slots / x));
   kern<<<dim3((unsigned)x, (unsigned)std::min<int64_t>(y, 65535)), kRopeThreads, 0, stream>>>(p);
-  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return pkv_launch_status();
 }
 
 }  // namespace pkv

@@ -57,12 +57,11 @@ extern "C" int paged_selftest_read_stream(const void* buf, size_t bytes, uint32_
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
-    (void)cudaGetLastError();
-    return PKV_ERR_CUDA;
+    return pkv_cuda_failed();
   }
   pkv::read_stream_kernel<<<(unsigned)sms * 4, 512, 0, stream>>>(
       static_cast<const uint4*>(buf), bytes / 16, sink);
-  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return pkv_launch_status();
 }
 
 extern "C" int paged_selftest_wait_timeout(uint64_t limit_ns, cudaStream_t stream) {
@@ -70,5 +69,5 @@ extern "C" int paged_selftest_wait_timeout(uint64_t limit_ns, cudaStream_t strea
   unsigned* err = pkv_error_word();
   if (!err) return PKV_ERR_CUDA;
   pkv::selftest_wait_kernel<<<1, 32, 0, stream>>>(limit_ns, err);
-  return cudaPeekAtLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return pkv_launch_status();
 }
