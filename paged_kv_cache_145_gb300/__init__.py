@@ -148,22 +148,28 @@ class RotaryAxes:
 
     ``rotary_dim``: leading elements of a head that rotate (even);
     ``inv_freq``: radians per position of each of the ``rotary_dim / 2``
-    pairs; ``pair_axis``: the axis whose position turns each pair (None: one
-    axis); ``interleaved``: pairs are neighbours (2i, 2i + 1) instead of
-    halves (i, i + rotary_dim / 2).
+    pairs; ``pair_axis``: the axis whose position turns each pair (None: axis
+    0); ``interleaved``: pairs are neighbours (2i, 2i + 1) instead of halves
+    (i, i + rotary_dim / 2); ``num_axes``: rows of the positions, for plans
+    whose last axes turn no pair (None: up to the last axis that does).
     """
 
-    def __init__(self, rotary_dim, inv_freq, pair_axis=None, interleaved=False):
+    def __init__(self, rotary_dim, inv_freq, pair_axis=None, interleaved=False, num_axes=None):
         freq = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
         if freq.shape != (rotary_dim // 2,):
             raise ValueError("inv_freq must hold rotary_dim / 2 frequencies")
         axes = None
+        if pair_axis is None and num_axes is not None:
+            pair_axis = np.zeros(freq.shape, dtype=np.int32)
         if pair_axis is not None:
             axes = np.ascontiguousarray(np.asarray(pair_axis, dtype=np.int32))
             if axes.shape != freq.shape or axes.min(initial=0) < 0:
                 raise ValueError("pair_axis must name an axis for each pair")
         self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
-        self.num_axes = 1 if axes is None else int(axes.max(initial=0)) + 1
+        used = 1 if axes is None else int(axes.max(initial=0)) + 1
+        self.num_axes = used if num_axes is None else int(num_axes)
+        if self.num_axes < used:
+            raise ValueError("pair_axis names axis %d of %d" % (used - 1, self.num_axes))
         self._c = _lib.pkv_rotary()
         _lib.check(_lib.lib().paged_rotary_init(
             ctypes.byref(self._c), self.rotary_dim, self.num_axes, freq.ctypes.data,
@@ -172,11 +178,12 @@ class RotaryAxes:
     @classmethod
     def sections(cls, sections, base=10000.0, interleaved=False):
         """Contiguous runs of pairs, one per axis (``[16, 24, 24]``: the first
-        16 of 64 pairs turn with axis 0, ...), at frequencies
-        ``base ** (-2 i / rotary_dim)``."""
+        16 of 64 pairs turn with axis 0, ...; an axis may have none), at
+        frequencies ``base ** (-2 i / rotary_dim)``."""
         pairs = int(sum(sections))
         axis = [a for a, n in enumerate(sections) for _ in range(n)]
-        return cls(2 * pairs, [float(base) ** (-i / pairs) for i in range(pairs)], axis, interleaved)
+        return cls(2 * pairs, [float(base) ** (-i / pairs) for i in range(pairs)], axis, interleaved,
+                   num_axes=len(sections))
 
     @property
     def ref(self):
