@@ -82,6 +82,14 @@ def _need(t, name, dtype=None, device=None):
         raise ValueError("%s is on %s, the cache on %s" % (name, t.device, device))
 
 
+def _int32(x, name):
+    """``x`` as an int that the library's 32-bit argument holds."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError("%s must fit 32 bits, got %d" % (name, x))
+    return x
+
+
 class PagedKVCache:
     """The physical pool: two ``[N, Hk, b, D]`` tensors (keys, values).
 
@@ -374,7 +382,8 @@ def paged_attention_cross_workspace_bytes(cache, total_queries, num_seqs, num_he
                                           max_enc_len):
     """Bytes of workspace that :func:`paged_attention_cross` needs."""
     return int(_lib.lib().paged_attention_cross_workspace_bytes(
-        cache.ref, total_queries, num_seqs, num_heads, max_queries, max_enc_len))
+        cache.ref, total_queries, _int32(num_seqs, "num_seqs"), _int32(num_heads, "num_heads"),
+        _int32(max_queries, "max_queries"), _int32(max_enc_len, "max_enc_len")))
 
 
 def paged_attention_cross(cache, q, query_starts, block_tables, enc_lens, scale, max_queries,
@@ -402,7 +411,8 @@ def paged_attention_cross(cache, q, query_starts, block_tables, enc_lens, scale,
     if enc_lens.shape != (num_seqs,) or query_starts.shape != (num_seqs + 1,) or \
             block_tables.dim() != 2 or block_tables.shape[0] != num_seqs:
         raise ValueError("enc_lens must be [S], query_starts [S + 1] and block_tables [S, max_blocks]")
-    max_queries, max_enc_len = int(max_queries), int(max_enc_len)
+    max_queries = _int32(max_queries, "max_queries")
+    max_enc_len = _int32(max_enc_len, "max_enc_len")
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
@@ -509,6 +519,7 @@ def paged_build_tables(free_list, free_state, old_lens, new_lens, block_tables, 
     width = block_tables.shape
     if len(width) != 2 or width[0] != n or old_lens.dim() != 1 or new_lens.shape != (n,):
         raise ValueError("old_lens and new_lens must be [S] and block_tables [S, max_blocks]")
+    block_size, max_tokens = _int32(block_size, "block_size"), int(max_tokens)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
     there = _elsewhere(dev, stream)
