@@ -347,7 +347,8 @@ int paged_attention_prefill(const pkv_cache* cache, const void* q, int64_t total
  *   query_starts  device, int32[num_seqs + 1], non-decreasing, last <=
  *                 total_queries; rows of out from the last on are left as
  *                 they were
- *   max_queries   host bound on any sequence's Q (sizes the launch), >= 1
+ *   max_queries   host bound on any sequence's Q (sizes the launch; no more
+ *                 than total_queries counts), >= 1
  *   block_tables, scale: as for paged_attention_decode
  *   enc_lens      device, int32[num_seqs]
  *   max_enc_len   host bound on enc_lens (0 = max_blocks_per_seq * b), at

@@ -613,6 +613,12 @@ WsLayout cross_workspace(int64_t total_queries, int num_heads, int head_dim, int
   return w;
 }
 
+// No sequence has more queries than q holds: a bound beyond them is cut to that,
+// so that the launch, the plan and the workspace do not grow with it.
+int cross_max_queries(int max_queries, int64_t total_queries) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(max_queries, total_queries));
+}
+
 bool cross_args_ok(const pkv_cache* c, int64_t total_queries, int num_seqs, int num_heads,
                    int max_queries) {
   return num_seqs >= 0 && num_seqs <= 65535 && num_heads >= 1 && max_queries >= 1 &&
@@ -628,6 +634,7 @@ size_t paged_attention_cross_workspace_bytes(const pkv_cache* cache, int64_t tot
   if (!cache || !cross_args_ok(cache, total_queries, num_seqs, num_heads, max_queries) ||
       max_enc_len < 0)
     return 0;
+  max_queries = cross_max_queries(max_queries, total_queries);
   const CrossPlan sp = cross_plan(cache, num_seqs, num_heads, max_queries, max_enc_len);
   return cross_workspace(total_queries, num_heads, cache->head_dim, sp.parts).total;
 }
@@ -647,6 +654,7 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
       max_blocks_per_seq < 0 || !std::isfinite(scale))
     return PKV_ERR_ARG;
   if (num_seqs == 0 || total_queries == 0) return PKV_OK;
+  max_queries = cross_max_queries(max_queries, total_queries);
   const int64_t cap = (int64_t)max_blocks_per_seq * cache->block_size;
   if (max_enc_len < 0 || max_enc_len > cap || (max_enc_len ? max_enc_len : cap) > (1 << 30))
     return PKV_ERR_ARG;
