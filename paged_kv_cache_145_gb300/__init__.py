@@ -380,7 +380,16 @@ def paged_attention_prefill(cache, q, query_starts, block_tables, seq_lens, scal
 
 def paged_attention_cross_workspace_bytes(cache, total_queries, num_seqs, num_heads, max_queries,
                                           max_enc_len):
-    """Bytes of workspace that :func:`paged_attention_cross` needs."""
+    """Bytes of workspace that :func:`paged_attention_cross` needs.
+
+    ``max_enc_len`` is the bound itself: table width x block size where the
+    call is given 0.
+    """
+    there = _elsewhere(cache.device, None)  # the plan goes by the device's size
+    if there is not None:
+        with there:
+            return paged_attention_cross_workspace_bytes(cache, total_queries, num_seqs, num_heads,
+                                                         max_queries, max_enc_len)
     return int(_lib.lib().paged_attention_cross_workspace_bytes(
         cache.ref, total_queries, _int32(num_seqs, "num_seqs"), _int32(num_heads, "num_heads"),
         _int32(max_queries, "max_queries"), _int32(max_enc_len, "max_enc_len")))
