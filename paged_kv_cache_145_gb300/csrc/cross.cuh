@@ -163,9 +163,14 @@ __global__ void __launch_bounds__(kCrossWarps * 32) cross_kernel(const CrossPara
     const int e = trow[i];
     bad |= e < 0 || (int64_t)e >= p.num_blocks;
   }
+  constexpr bool kFp8 = std::is_same<TC, __nv_fp8_e4m3>::value;
+  const float qs = p.qscale * (kFp8 ? p.k_scale[kvh] : 1.f);
+  // A scale of zero goes into the queries, so that no product of theirs is
+  // beyond float32.
+  const float in = qs == 0.f ? 0.f : 1.f;
   for (int e = tid; e < R * D; e += kCrossWarps * 32) {
     const int r = e / D;
-    s_q[r][e % D] = r < nr ? static_cast<float>(static_cast<const T*>(p.q)[row_at(r) + e % D]) : 0.f;
+    s_q[r][e % D] = r < nr ? static_cast<float>(static_cast<const T*>(p.q)[row_at(r) + e % D]) * in : 0.f;
   }
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) set_error(p.err, PKV_DEV_TABLE_RANGE);
@@ -178,8 +183,6 @@ __global__ void __launch_bounds__(kCrossWarps * 32) cross_kernel(const CrossPara
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[r][e] = 0.f;
   }
-  constexpr bool kFp8 = std::is_same<TC, __nv_fp8_e4m3>::value;
-  const float qs = p.qscale * (kFp8 ? p.k_scale[kvh] : 1.f);
   const TC* const kp = static_cast<const TC*>(p.k_cache);
   const TC* const vp = static_cast<const TC*>(p.v_cache);
   const int lo = part * p.part, hi = bad ? lo : min(c.L, lo + p.part);

@@ -121,6 +121,13 @@ __device__ __forceinline__ bool table_row_bad(const CrossParams& p, const int32_
   return bad;
 }
 
+// Two 16-bit elements times zero: zeros, NaN for what is not finite.
+template <typename T>
+__device__ __forceinline__ uint32_t zero_pair(uint32_t w) {
+  constexpr uint32_t kExp = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
+  return ((w & kExp) == kExp ? 0x7FFFu : 0u) | ((w & kExp << 16) == kExp << 16 ? 0x7FFF0000u : 0u);
+}
+
 // A thread's Q row, from global memory into row rr of a 128-row tile in the
 // 128-byte-swizzled operand layout; returns the factor that makes its
 // products scores in base-2 units (never negative: the sign of the scale goes
@@ -162,12 +169,9 @@ __device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const 
       qscale = ldexpf(mq * mk, eq + ek - e);
     }
   }
-  // A zero scale becomes zero queries, so that hidden keys stay at -inf.
-  const bool none = qscale == 0.f;
-  if (none) qscale = 1.f;
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {  // (all loads in flight)
-    const uint4 x = none ? make_uint4(0u, 0u, 0u, 0u) : src[i];
+    const uint4 x = src[i];
     uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -178,6 +182,18 @@ __device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const 
     }
     *reinterpret_cast<uint4*>(tile + (i >> 3) * 128 * 128 + rr * 128 +
                               (((i & 7) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (qscale == 0.f) {
+    // A zero scale goes into the queries, so that hidden keys stay at -inf.
+    using Op = typename std::conditional<KV8, __half, T>::type;
+#pragma unroll 1
+    for (int i = 0; i < D / 8; ++i) {
+      uint4* const at = reinterpret_cast<uint4*>(tile + (i >> 3) * 128 * 128 + rr * 128 +
+                                                 ((i & 7) << 4));  // (in any order)
+      *at = make_uint4(zero_pair<Op>(at->x), zero_pair<Op>(at->y), zero_pair<Op>(at->z),
+                       zero_pair<Op>(at->w));
+    }
+    qscale = 1.f;
   }
   return qscale;
 }
