@@ -171,8 +171,8 @@ int paged_rotary_init(pkv_rotary* rotary, int32_t rotary_dim, int32_t num_axes,
  * token t and pair i of rotary (elements x, y of every query and key head):
  *     a = positions[axis_i][t] * inv_freq_i
  *     x' = x cos a - y sin a,   y' = y cos a + x sin a
- * in float32 from angles reduced exactly, for any 32-bit position (negative
- * ones too).  Elements from rotary_dim on, and values, are copied.  q_out
+ * in float32 from angles reduced in 64-bit fixed point, as good at any 32-bit
+ * position (negative ones too) as near 0: within 1e-7 radians.  Elements from rotary_dim on, and values, are copied.  q_out
  * and the pool rows are rounded once (FP8 pools: e4m3(x / scale[h]) from the
  * float32 values, as in paged_kv_write).  Every token's query is written;
  * keys and values only where slot_mapping[t] >= 0 (a negative slot marks
@@ -334,8 +334,10 @@ int paged_attention_prefill(const pkv_cache* cache, const void* q, int64_t total
  * fp16, bf16, fp32 and FP8 pools; head_dim, block_size and head grouping as
  * for paged_attention_decode.  fp16 and bf16 pools, and FP8 pools of
  * head_dim 128, run on tensor cores, where probabilities are rounded to the
- * 16-bit operand type (bf16 pools: bf16; others: fp16) and sums are not
- * (num_blocks * num_kv_heads must be below 2^31 - 1 there).  Infinities and
+ * 16-bit operand type (bf16 pools: bf16; others: fp16) and sums are not: an
+ * output moves by at most 2^-8 (bf16) or 2^-11 (fp16) of the weighted mean of
+ * |V_t|.  (paged_attention_decode, for one query per sequence, keeps more bits.)
+ * num_blocks * num_kv_heads must be below 2^31 - 1 there.  Infinities and
  * NaN among a sequence's states act as in the formula: a score of minus infinity
  * has weight 0, a row with a score of plus infinity or NaN, or with no other
  * scores than minus infinity, is NaN, and a value that is not finite reaches

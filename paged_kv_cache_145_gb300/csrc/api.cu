@@ -538,8 +538,10 @@ namespace {
 // sequence has more rows than that, of 256; else on CUDA cores in blocks of
 // 8 rows.  Where the blocks would not fill the GPU the states are split in
 // whole runs of 128 positions, into as many parts as there are free places
-// (one token of four sequences over 5200-6400 states: 23.9 us; twice and four
-// times as many parts: 29.2 and 34.5).
+// (one token of four sequences over 5200-6400 states: 22.6 us; twice and four
+// times as many parts: 27.3 and 31.6).  FP8 pools, 8 sequences over 1000-4000
+// states, rows of 32/8 heads: 128 rows 42 us in blocks of 128 and 35 of 256, 132
+// rows 61 and 40, 256 rows 64 and 47.
 struct CrossPlan {
   bool tc, wide;
   int parts, part;

@@ -22,7 +22,10 @@
 // stores, and the instructions on it count (32-bit saturating sums and
 // division by multiplication took 8 rows from 4.8 to 3.7 us).  Measured, in a
 // graph: 8 rows of one token 3.7 us; 256 rows with arrivals and releases, slot
-// map of 16384, 8.6 us; 1024 prompts of 262144 tokens 13.4 us.
+// map of 16384, 8.7 us; 1024 prompts of 262144 tokens 13.4 us.  Moved blocks are
+// walked by the one cluster or block: 1024 rows that give back 250 each take
+// 71 us, 256 rows that give back 2048 each 123 us, and 2.1 ms where few rows and
+// tokens choose the one small block (see pkv_launch_build_tables).
 #include <algorithm>
 #include <atomic>
 
@@ -421,10 +424,12 @@ int pkv_launch_build_tables(pkv::BuildParams p, cudaStream_t stream) {
   using namespace pkv;
   p.err = pkv_error_word();
   if (!p.err) return PKV_ERR_CUDA;
-  // One small block serves a step of few rows and tokens (8 rows: 3.8 us; a
-  // cluster 5.4), a cluster the others.  Up to 16384 tokens are written along
-  // (256 rows, 16384 tokens: 10 us), a wider slot map by a second kernel over
-  // the whole GPU.
+  // One small block serves a step of few rows and tokens (8 rows: 3.7 us, 5.3 in
+  // a cluster; 256 rows of one token: 5.1 and 7.5), a cluster the others.  Up to
+  // 16384 tokens are written along, a wider slot map by a second kernel over
+  // the whole GPU (256 mixed rows, written along and by the second kernel:
+  // 8192 tokens 8.1 and 9.9 us, 16384 8.8 and 9.6, 65536 9.6 and 9.3; 1024
+  // prompts of 262144 tokens 33.5 and 13.4).
   const bool small = p.num_seqs <= 256 && p.max_tokens <= 1024;
   const int cluster = small ? 1 : kBuildCluster, threads = small ? 256 : kBuildThreads;
   p.fill = p.max_tokens <= 16384;

@@ -18,27 +18,31 @@
 //        and the others.
 // Two S buffers: S(j + 1) is made while the softmax works on S(j).  The
 // running maximum is raised lazily (by more than 2^kSlack, so that O is
-// rescaled rarely); sums, maxima and O are float32.  P is rounded to the
-// operand type: bf16 for bf16 pools (2^-8 of each weight at most, the step
-// of the output itself), fp16 else, scaled by 2^kBias to keep small weights
-// out of fp16's subnormals.
+// rescaled rarely); sums, maxima and O are float32.  P is rounded once to the
+// operand type, bf16 for bf16 pools (a weight by 2^-8 of itself at most), fp16
+// else (2^-11, scaled by 2^kBias to keep small weights out of the subnormals):
+// half a step of what the output is rounded to anyway, for one P.V product per
+// tile.  Values of N(0, 1) come out with 1.35 times the error of an output
+// rounded from float32 weights (fp16 and bf16 pools); an output moves by 2^-8 or
+// 2^-11 of sum p |V| at most, which for values far beyond the output is more
+// than its own rounding.
 //
 // What bounds it.  Many rows: each tile's chain softmax -> P.V -> next S, and
 // the special function unit (an exponential takes a warp about 7 cycles); two
 // blocks of 128 rows per SM hide one another's chains better than one block
 // of 256 rows, although that reads each K and V tile half as often.  Measured
 // (8 sequences of 2048 queries over 2000-6400 states, bf16, 32/8 heads of 128):
-// 783 us (1495 TFLOP/s) with two blocks of 128 rows; one block of 256 rows with
-// 128-key tiles and one S buffer 883.  Few rows: HBM, and below some
-// megabytes per SM the fixed costs of a block (4 us from launch to first tile
-// and last tile to end).  Copies and MMAs are issued by one elected thread
+// 792 us (1477 TFLOP/s) with two blocks of 128 rows (784 before scores of minus
+// infinity were provided for); one block of 256 rows with 128-key tiles and one
+// S buffer took 883.  Few rows: HBM, and below some megabytes per SM the fixed
+// costs of a block (4 us from launch to first tile and last tile to end).  Copies and MMAs are issued by one elected thread
 // each: an operand in a uniform register costs several instructions to fill,
 // and lanes that each issue one do it one after the other (a copy costs its
 // thread about 90 cycles; the same four copies from four lanes took 1000).
 // FP8 pools keep 256 rows where a sequence has more than 128: widening each
 // tile costs more than the chain (8 x 300-512 queries over 1000-4000 states,
-// 32/8 heads of 128: 154 us, 205 with blocks of 128 rows).  Two converter warps
-// for keys and two for values: 164 us, all four for one after the other 195.
+// 32/8 heads of 128: 150 us, 215 with blocks of 128 rows).  All four converter
+// warps for keys and values in turn took 195 us where two for each took 164.
 //
 // Tensor memory per row tile: two buffers of S (64 columns each, P in the first
 // 32), then O (D columns).  Every wait is bounded.
@@ -203,8 +207,8 @@ __device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const 
 template <int KEYS, int THREADS>
 __device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned char* dst, int valid,
                                            int thread) {
-  // Eight loads in flight (8 x 300-512 queries over 1000-4000 states: one 164 us,
-  // four 154, eight 150).
+  // Eight loads in flight: 150 us for 8 x 300-512 queries over 1000-4000 states,
+  // where one took 164 and four 154.
   constexpr int kUnits = KEYS * 8 / THREADS, kBatch = 8;
   static_assert(kUnits % kBatch == 0, "whole batches");
 #pragma unroll 1
@@ -654,7 +658,6 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
           ok = false;
           break;
         }
-        // (both row tiles do it: the same zeros)
         clear_tail<D, KT>(smem + Cfg::kVRingOff + (j % NV) * Cfg::kTileBytes, hi - lo - j * KT, b, rr,
                           32 * tile_warps(t));
       }
