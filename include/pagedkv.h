@@ -76,16 +76,22 @@ typedef enum { PKV_F32 = 0, PKV_F16 = 1, PKV_BF16 = 2, PKV_FP8_E4M3 = 3 } pkv_dt
 #define PKV_DEV_SLOT_RANGE   1u  /* paged_kv_write: slot >= num_blocks * b        */
 #define PKV_DEV_TABLE_RANGE  2u  /* decode: a used table entry not in [0, N)      */
 #define PKV_DEV_SEQ_LEN      4u  /* decode: length not in [1, max_seq_len]        */
-#define PKV_DEV_PAIR_RANGE   8u  /* paged_block_copy: src or dst not in [0, N)    */
+#define PKV_DEV_PAIR_RANGE   8u  /* paged_block_copy: src or dst not in [0, N);   */
+                                 /* paged_fork_tables: a parent not in [-1, S)    */
 #define PKV_DEV_TIMEOUT     16u  /* a bounded wait for a bulk copy gave up        */
 #define PKV_DEV_SHARING     32u  /* shared-prefix decode: a member's table or     */
-                                 /* length disagrees with its group's prefix      */
+                                 /* length disagrees with its group's prefix;     */
+                                 /* paged_fork_tables: more entries name a block  */
+                                 /* than it has holders                           */
 #define PKV_DEV_LAUNCH      64u  /* a kernel found its shared memory not 1 KiB    */
                                  /* aligned and computed nothing                  */
-#define PKV_DEV_NOMEM      128u  /* paged_build_tables: too few free blocks       */
-#define PKV_DEV_FREE_LIST  256u  /* paged_build_tables: the ring's state or a     */
-                                 /* taken entry is out of range, or more blocks   */
-                                 /* come back than the ring has room for          */
+#define PKV_DEV_NOMEM      128u  /* paged_build_tables, paged_fork_tables: too    */
+                                 /* few free blocks                               */
+#define PKV_DEV_FREE_LIST  256u  /* paged_build_tables, paged_fork_tables: the    */
+                                 /* ring's state or a taken entry is out of       */
+                                 /* range, or more blocks come back than the ring */
+                                 /* has room for; paged_compact: free and held    */
+                                 /* blocks are not all there are                  */
 #define PKV_DEV_TOKENS     512u  /* paged_build_tables: more than max_tokens      */
 /* After PKV_DEV_TIMEOUT the launch that set it may have ended with bulk
  * copies still in flight into its shared memory (the drain after a timeout
@@ -198,6 +204,41 @@ int paged_rope_kv_write(const pkv_cache* cache, const pkv_rotary* rotary, const 
                         int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping,
                         int64_t num_tokens, int32_t num_heads, void* q_out, int64_t q_out_stride,
                         cudaStream_t stream);
+
+/*
+ * pkv_norm_weight -- a norm's weights: D elements shared by every head, or
+ * [heads][D], one row per head.
+ */
+typedef struct {
+  const void* data;      /* device, 16-byte aligned; NULL: all ones           */
+  int32_t dtype;         /* PKV_F32, or the type of q, k and v                */
+  int32_t per_head;      /* 0: [D], else [heads][D]                           */
+} pkv_norm_weight;
+
+/*
+ * paged_norm_rope_kv_write -- paged_rope_kv_write with a norm of each query
+ * and key head in front of the rotation, in the same pass.
+ *
+ * For every head x of q and of k (D = head_dim elements):
+ *     y_d = x_d * w_d / sqrt(mean_d(x_d^2) + eps)
+ * and y, not x, is rotated and written.  Values are copied.  Everything is
+ * float32 from the stored elements and rounded once, at the end, as there;
+ * heads whose squares leave float32's range are scaled by a power of two
+ * first.  A head with an infinity or NaN has NaN and zeros, as in the formula.
+ *
+ *   q_weight, k_weight  host; NULL for weights of one
+ *   eps                 >= 0, finite
+ *
+ * Everything else, the strides, slots, errors and geometry among it, is as for
+ * paged_rope_kv_write, but that a head has at most 1024 bytes of the io type
+ * (else PKV_ERR_GEOMETRY) and q_out may be q only with the same stride.
+ */
+int paged_norm_rope_kv_write(const pkv_cache* cache, const pkv_rotary* rotary, const void* q,
+                             int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, const int32_t* positions,
+                             const int64_t* slot_mapping, int64_t num_tokens, int32_t num_heads,
+                             const pkv_norm_weight* q_weight, const pkv_norm_weight* k_weight,
+                             float eps, void* q_out, int64_t q_out_stride, cudaStream_t stream);
 
 /*
  * paged_attention_partition_size -- the partition length (in positions) a
@@ -374,6 +415,56 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
                           const int32_t* enc_lens, int32_t max_enc_len, int32_t num_heads,
                           float scale, void* out, void* workspace, size_t workspace_bytes,
                           cudaStream_t stream);
+
+/*
+ * paged_attention_window -- causal attention of each sequence's new queries
+ * to a sliding window of its last positions and to its first positions, which
+ * stay visible.
+ *
+ * Sequence s holds L = seq_lens[s] positions, the last
+ * Q = query_starts[s+1] - query_starts[s] of which are its new queries' (their
+ * keys and values already written), as for paged_attention_prefill.  Query i
+ * sits at position p = L - Q + i and sees
+ *     position t  iff  t <= p  and  (t > p - window  or  t < sinks)
+ *     out[query_starts[s] + i][h] = softmax-weighted mean of V_t, as in
+ *     paged_attention_decode, over the t it sees
+ * accumulated in float32.  One query per sequence is the decode step.
+ *
+ * A table entry is read only if some query of the sequence sees a position of
+ * its block: blocks between the sinks and the window may have been given back
+ * (paged_fork_tables does that), their entries hold anything.  What a query
+ * does not see does not reach it, infinities and NaN included, wherever it
+ * lies: behind a sequence, before the window, or seen by another query.  What
+ * it sees acts as in the formula, as for paged_attention_cross.
+ *
+ * Pools, geometry, precision and the split of long spans with few rows are as
+ * for paged_attention_cross.
+ *
+ *   q, out, query_starts, max_queries, block_tables, scale, workspace
+ *                 as for paged_attention_cross; rows of out from the last
+ *                 sequence's on are left as they were
+ *   seq_lens      device, int32[num_seqs], 0 .. max_seq_len, at least Q
+ *   max_seq_len   host bound on seq_lens (0 = max_blocks_per_seq * b), at most
+ *                 2^30
+ *   window        >= 1: positions up to a query's own that it sees
+ *   sinks         >= 0: first positions that every query sees
+ *
+ * A sequence with Q > max_queries, Q > L or L outside [0, max_seq_len] gets
+ * zero rows and PKV_DEV_SEQ_LEN, one with an entry outside [0, num_blocks)
+ * among those that its queries read zero rows and PKV_DEV_TABLE_RANGE; one
+ * whose query range leaves [0, total_queries) sets PKV_DEV_SEQ_LEN and is not
+ * written.
+ */
+size_t paged_attention_window_workspace_bytes(const pkv_cache* cache, int64_t total_queries,
+                                              int32_t num_seqs, int32_t num_heads,
+                                              int32_t max_queries, int32_t window, int32_t sinks,
+                                              int32_t max_seq_len);
+int paged_attention_window(const pkv_cache* cache, const void* q, int64_t total_queries,
+                           const int32_t* query_starts, int32_t num_seqs, int32_t max_queries,
+                           const int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* seq_lens, int32_t max_seq_len, int32_t window,
+                           int32_t sinks, int32_t num_heads, float scale, void* out,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * paged_attention_decode_shared -- paged_attention_decode for batches in
@@ -573,6 +664,107 @@ int paged_build_tables(int64_t num_blocks, int32_t block_size, int32_t* free_lis
                        int32_t max_blocks_per_seq, int32_t* seq_lens, int64_t* free_state_out,
                        int32_t* query_starts, int64_t* slot_mapping, int32_t* positions,
                        int64_t max_tokens, cudaStream_t stream);
+
+/*
+ * paged_fork_tables -- the rows of the next step chosen among the rows of this
+ * one, on the device: forks, beams that change places, requests that end, and
+ * blocks that a sliding window has left.
+ *
+ * The device counterpart of the host block manager's fork, append (its
+ * copy-on-write) and release, with shared blocks counted on the device: block
+ * x has extra_refs[x] + 1 holders, a holder being an entry of a row (or what
+ * else the caller counts there: a kept prefix, say).  Blocks that one row
+ * holds, those paged_build_tables takes among them, have 0, and so have free
+ * ones.  Next row s continues this step's row r = parents[s]:
+ *   - lens_out[s] = seq_lens[r]; parents[s] = -1 is an empty row, length 0;
+ *   - tables_out[s] holds r's entries, each block with a holder more; -1 past
+ *     the row's last block, and with window > 0 in the place of every block
+ *     that no query from position seq_lens[r] on sees (block e is seen if
+ *     e * b < sinks or (e + 1) * b > seq_lens[r] + 1 - window); entries of -1
+ *     stay;
+ *   - a partly filled last block is to be written to and becomes the row's
+ *     own: the first s that names r keeps it if r alone held it; every other
+ *     s takes a block from the head of the ring, in the order of s, and its
+ *     keys and values are copied there;
+ *   - every entry of this step's rows gives its hold up.  Blocks without a
+ *     holder go back behind the ring's tail, each once, in the order in which
+ *     this step's rows first name them; they can be taken from the next call
+ *     on.
+ * The tables feed paged_build_tables for the rows' next tokens.  Rows that
+ * share blocks, or have given some back, end or go back here (that call takes
+ * every block for one row's own).
+ *
+ * All or nothing: if the free blocks do not cover the copies (PKV_DEV_NOMEM), a
+ * length is outside [0, max_blocks_per_seq * b] (PKV_DEV_SEQ_LEN), a parent
+ * outside [-1, num_seqs) (PKV_DEV_PAIR_RANGE), an entry of a row's length
+ * outside [-1, num_blocks), or -1 for its partly filled last block
+ * (PKV_DEV_TABLE_RANGE), the ring inconsistent (PKV_DEV_FREE_LIST) or a block
+ * named by more entries than it has holders (PKV_DEV_SHARING), then every next
+ * row is empty and pool, ring, state and counts stay as they were (extra_out =
+ * extra_refs): the step can be taken again from the same inputs.
+ *
+ *   free_list, free_state  as for paged_build_tables (the ring is updated in
+ *                   place, behind the tail)
+ *   extra_refs      device, int32[num_blocks], not negative
+ *   parents         device, int32[num_next]
+ *   block_tables    device, int32[num_seqs][max_blocks_per_seq]
+ *   seq_lens        device, int32[num_seqs]
+ *   tables_out      device, int32[num_next][max_blocks_per_seq], apart from
+ *                   block_tables
+ *   lens_out        device, int32[num_next], apart from seq_lens
+ *   extra_out       device, int32[num_blocks]; may be extra_refs
+ *   state_out       device, int64[2]; may be free_state
+ *   window, sinks   window 0: nothing is given back for a window
+ *   workspace       device, >= paged_fork_tables_workspace_bytes(num_seqs,
+ *                   num_next) bytes, 16-byte aligned; calls that may overlap
+ *                   need one each
+ *
+ * num_seqs and num_next at most 65535, rows times width at most 2^30,
+ * num_blocks at most 2^30.
+ */
+size_t paged_fork_tables_workspace_bytes(int32_t num_seqs, int32_t num_next);
+int paged_fork_tables(const pkv_cache* cache, int32_t* free_list, const int64_t* free_state,
+                      const int32_t* extra_refs, const int32_t* parents, int32_t num_next,
+                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                      const int32_t* seq_lens, int32_t num_seqs, int32_t window, int32_t sinks,
+                      int32_t* tables_out, int32_t* lens_out, int32_t* extra_out,
+                      int64_t* state_out, void* workspace, size_t workspace_bytes,
+                      cudaStream_t stream);
+
+/*
+ * paged_compact -- moves the blocks that the rows hold to the front of the
+ * pool, so that its end can be cut off, or handed to another pool.
+ *
+ * With n different blocks named by the rows' entries (entries of -1 name
+ * none), the k-th of them from id n on moves to the k-th id below n that is not
+ * among them, in ascending order; those below n stay.  Keys and values are
+ * moved, the rows' entries rewritten, moved_to[x] is x's new id (-1 for blocks
+ * that the rows do not hold), extra_out[moved_to[x]] = extra_refs[x] and 0
+ * elsewhere, the ring holds n .. num_blocks - 1 (-1 behind them) and its state
+ * is {0, num_blocks - n}.  moved_to serves whatever else names blocks (other
+ * tables over the same pool are best given as further rows).
+ *
+ * All or nothing: if free and held blocks are not num_blocks together, so that
+ * one would be lost, or the ring's state is out of range (PKV_DEV_FREE_LIST), a
+ * length is outside [0, max_blocks_per_seq * b] (PKV_DEV_SEQ_LEN) or an entry
+ * outside [-1, num_blocks) (PKV_DEV_TABLE_RANGE), then nothing moves:
+ * moved_to[x] = x, and the outputs are the inputs.
+ *
+ *   free_list       device, int32[num_blocks], rewritten in place
+ *   tables_out      device, as block_tables; may be block_tables
+ *   extra_out       device, int32[num_blocks]; may be extra_refs
+ *   state_out       device, int64[2]; may be free_state
+ *   moved_to        device, int32[num_blocks]
+ *   workspace       device, >= paged_compact_workspace_bytes(num_blocks) bytes,
+ *                   16-byte aligned; calls that may overlap need one each
+ * and the rest, and the bounds, as for paged_fork_tables.
+ */
+size_t paged_compact_workspace_bytes(int64_t num_blocks);
+int paged_compact(const pkv_cache* cache, int32_t* free_list, const int64_t* free_state,
+                  const int32_t* extra_refs, const int32_t* block_tables,
+                  int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs,
+                  int32_t* tables_out, int32_t* extra_out, int64_t* state_out, int32_t* moved_to,
+                  void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * paged_get_device_error -- synchronise `stream`, then read and clear the

@@ -18,7 +18,7 @@ import torch
 
 from . import _lib
 from ._lib import (PKV_DEV_FREE_LIST, PKV_DEV_NOMEM, PKV_DEV_PAIR_RANGE,  # noqa: F401
-                   PKV_DEV_SEQ_LEN, PKV_DEV_SLOT_RANGE, PKV_DEV_TABLE_RANGE, PKV_DEV_TIMEOUT,
+                   PKV_DEV_SEQ_LEN, PKV_DEV_SHARING, PKV_DEV_SLOT_RANGE, PKV_DEV_TABLE_RANGE, PKV_DEV_TIMEOUT,
                    PKV_DEV_TOKENS, PKV_ERR_NOMEM, PKV_SWAP_IN,
                    PKV_SWAP_OUT)
 
@@ -32,7 +32,9 @@ __all__ = [
     "paged_block_copy", "paged_block_swap", "paged_get_device_error",
     "paged_selftest_wait_timeout", "paged_selftest_read_stream", "paged_attention_decode_shared",
     "paged_build_tables", "RotaryAxes", "paged_rope_kv_write", "paged_attention_cross",
-    "paged_attention_cross_workspace_bytes",
+    "paged_attention_cross_workspace_bytes", "paged_norm_rope_kv_write",
+    "paged_attention_window", "paged_attention_window_workspace_bytes", "paged_fork_tables",
+    "paged_fork_tables_workspace_bytes", "paged_compact", "paged_compact_workspace_bytes",
     "library_path",
 ]
 
@@ -212,15 +214,8 @@ def _need_rows(t, name, heads, dim, dtype, device):
     return row
 
 
-def paged_rope_kv_write(cache, rotary, q, k, v, positions, slot_mapping, q_out=None, stream=None):
-    """Rotate ``q`` ``[T, H, D]`` and ``k`` ``[T, Hk, D]`` by the tokens'
-    positions and store ``k`` and ``v`` at ``slot_mapping`` (int64 ``[T]``).
-
-    ``positions``: int32 ``[num_axes, T]`` (or ``[T]`` with one axis).  q, k
-    and v may be slices of one projection (heads contiguous, tokens strided
-    by a multiple of 16 bytes).  ``q_out`` may be ``q``; it is allocated when
-    not given.  Returns ``q_out``.
-    """
+def _rope_rows(cache, rotary, q, k, v, positions, slot_mapping):
+    """The checks of a rotary write: tokens, query heads, strides of q, k, v."""
     dev, io, dim = cache.device, cache.io_dtype, cache.head_dim
     if q.dim() != 3:
         raise ValueError("q must be [num_tokens, num_heads, head_dim]")
@@ -235,23 +230,81 @@ def paged_rope_kv_write(cache, rotary, q, k, v, positions, slot_mapping, q_out=N
     if positions.shape != (rotary.num_axes, n) and not (rotary.num_axes == 1 and
                                                         positions.shape == (n,)):
         raise ValueError("positions must be [num_axes, num_tokens]")
+    return n, heads, qs, ks, vs
+
+
+def _rope_out(q_out, n, heads, dim, io, dev):
+    """``q_out``, checked or new, and its token stride."""
+    if q_out is None:
+        return torch.empty((n, heads, dim), dtype=io, device=dev), heads * dim
+    os = _need_rows(q_out, "q_out", heads, dim, io, dev)
+    if q_out.shape[0] != n:
+        raise ValueError("q_out must have q's shape")
+    return q_out, os
+
+
+def paged_rope_kv_write(cache, rotary, q, k, v, positions, slot_mapping, q_out=None, stream=None):
+    """Rotate ``q`` ``[T, H, D]`` and ``k`` ``[T, Hk, D]`` by the tokens'
+    positions and store ``k`` and ``v`` at ``slot_mapping`` (int64 ``[T]``).
+
+    ``positions``: int32 ``[num_axes, T]`` (or ``[T]`` with one axis).  q, k
+    and v may be slices of one projection (heads contiguous, tokens strided
+    by a multiple of 16 bytes).  ``q_out`` may be ``q``; it is allocated when
+    not given.  Returns ``q_out``.
+    """
+    dev, io, dim = cache.device, cache.io_dtype, cache.head_dim
+    n, heads, qs, ks, vs = _rope_rows(cache, rotary, q, k, v, positions, slot_mapping)
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
             return paged_rope_kv_write(cache, rotary, q, k, v, positions, slot_mapping, q_out)
-    if q_out is None:
-        q_out = torch.empty((n, heads, dim), dtype=io, device=dev)
-        os = heads * dim
-    else:
-        os = _need_rows(q_out, "q_out", heads, dim, io, dev)
-        if q_out.shape[0] != n:
-            raise ValueError("q_out must have q's shape")
+    q_out, os = _rope_out(q_out, n, heads, dim, io, dev)
     rc = _lib.lib().paged_rope_kv_write(
         cache.ref, rotary.ref, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
         positions.data_ptr(), slot_mapping.data_ptr(), n, heads, q_out.data_ptr(), os,
         _raw_stream(dev.index))
     if rc:
         _lib.check(rc, "paged_rope_kv_write")
+    return q_out
+
+
+def _norm_weight(w, name, heads, cache):
+    """``w`` (None, ``[D]`` or ``[heads, D]``) as the library takes it."""
+    if w is None:
+        return None
+    _need(w, name, None, cache.device)
+    if w.dtype != torch.float32 and w.dtype != cache.io_dtype:
+        raise ValueError("%s must have dtype float32 or %s, got %s" % (name, cache.io_dtype, w.dtype))
+    if w.shape != (cache.head_dim,) and w.shape != (heads, cache.head_dim):
+        raise ValueError("%s must be [head_dim] or [%d, head_dim]" % (name, heads))
+    return ctypes.byref(_lib.pkv_norm_weight(w.data_ptr(), _DTYPE_CODE[w.dtype], int(w.dim() == 2)))
+
+
+def paged_norm_rope_kv_write(cache, rotary, q, k, v, positions, slot_mapping, q_weight=None,
+                             k_weight=None, eps=1e-6, q_out=None, stream=None):
+    """:func:`paged_rope_kv_write` with each query and key head normed before
+    it turns: ``x * weight / sqrt(mean(x ** 2) + eps)`` over the head's
+    elements, in one pass.
+
+    ``q_weight``/``k_weight``: ``[D]`` (shared by the heads) or ``[H, D]`` /
+    ``[Hk, D]``, float32 or the type of q; None for ones.  Returns ``q_out``.
+    """
+    dev, io, dim = cache.device, cache.io_dtype, cache.head_dim
+    n, heads, qs, ks, vs = _rope_rows(cache, rotary, q, k, v, positions, slot_mapping)
+    qw = _norm_weight(q_weight, "q_weight", heads, cache)
+    kw = _norm_weight(k_weight, "k_weight", cache.num_kv_heads, cache)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return paged_norm_rope_kv_write(cache, rotary, q, k, v, positions, slot_mapping,
+                                            q_weight, k_weight, eps, q_out)
+    q_out, os = _rope_out(q_out, n, heads, dim, io, dev)
+    rc = _lib.lib().paged_norm_rope_kv_write(
+        cache.ref, rotary.ref, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        positions.data_ptr(), slot_mapping.data_ptr(), n, heads, qw, kw, float(eps),
+        q_out.data_ptr(), os, _raw_stream(dev.index))
+    if rc:
+        _lib.check(rc, "paged_norm_rope_kv_write")
     return q_out
 
 
@@ -453,6 +506,84 @@ def paged_attention_cross(cache, q, query_starts, block_tables, enc_lens, scale,
     return out
 
 
+def paged_attention_window_workspace_bytes(cache, total_queries, num_seqs, num_heads, max_queries,
+                                           window, sinks, max_seq_len):
+    """Bytes of workspace that :func:`paged_attention_window` needs.
+
+    ``max_seq_len`` is the bound itself: table width x block size where the
+    call is given 0.
+    """
+    there = _elsewhere(cache.device, None)  # the plan goes by the device's size
+    if there is not None:
+        with there:
+            return paged_attention_window_workspace_bytes(cache, total_queries, num_seqs, num_heads,
+                                                          max_queries, window, sinks, max_seq_len)
+    return int(_lib.lib().paged_attention_window_workspace_bytes(
+        cache.ref, total_queries, _int32(num_seqs, "num_seqs"), _int32(num_heads, "num_heads"),
+        _int32(max_queries, "max_queries"), _int32(window, "window"), _int32(sinks, "sinks"),
+        _int32(max_seq_len, "max_seq_len")))
+
+
+def paged_attention_window(cache, q, query_starts, block_tables, seq_lens, scale, max_queries,
+                           window, sinks=0, max_seq_len=0, out=None, workspace=None, stream=None):
+    """Causal attention of each sequence's new queries to a sliding window of
+    positions and to the first ones: the query at position p sees t <= p with
+    ``t > p - window`` or ``t < sinks``.
+
+    ``q``: ``[total_queries, H, D]``, sequence s's queries at
+    ``query_starts[s] .. query_starts[s + 1] - 1``, its last positions;
+    ``query_starts``: int32 ``[S + 1]``; ``block_tables``: int32 ``[S,
+    max_blocks]`` (entries of blocks that no query sees may be anything);
+    ``seq_lens``: int32 ``[S]`` (with the queries); ``max_queries``: host bound
+    on a sequence's queries; ``max_seq_len``: host bound on ``seq_lens`` (0 =
+    table width x block size).  Rows of ``out`` behind the last sequence's are
+    left as they were.  Returns ``out``.
+    """
+    dev = cache.device
+    _need(q, "q", cache.io_dtype, dev)
+    _need(query_starts, "query_starts", torch.int32, dev)
+    _need(block_tables, "block_tables", torch.int32, dev)
+    _need(seq_lens, "seq_lens", torch.int32, dev)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError("q must be [total_queries, num_heads, head_dim]")
+    num_seqs = seq_lens.numel()
+    if seq_lens.shape != (num_seqs,) or query_starts.shape != (num_seqs + 1,) or \
+            block_tables.dim() != 2 or block_tables.shape[0] != num_seqs:
+        raise ValueError("seq_lens must be [S], query_starts [S + 1] and block_tables [S, max_blocks]")
+    max_queries, max_seq_len = _int32(max_queries, "max_queries"), _int32(max_seq_len, "max_seq_len")
+    window, sinks = _int32(window, "window"), _int32(sinks, "sinks")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return paged_attention_window(cache, q, query_starts, block_tables, seq_lens, scale,
+                                          max_queries, window, sinks, max_seq_len, out, workspace)
+    lib, total, heads, width = _lib.lib(), q.shape[0], q.shape[1], block_tables.shape[1]
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", cache.io_dtype, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if workspace is None:
+        need = lib.paged_attention_window_workspace_bytes(
+            cache.ref, total, num_seqs, heads, max_queries, window, sinks,
+            max_seq_len or min(width * cache.block_size, 1 << 30))
+        ws, ws_len = None, need
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws = workspace.data_ptr()
+    else:
+        _need(workspace, "workspace", None, dev)
+        ws, ws_len = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    rc = lib.paged_attention_window(
+        cache.ref, q.data_ptr(), total, query_starts.data_ptr(), num_seqs, max_queries,
+        block_tables.data_ptr(), width, seq_lens.data_ptr(), max_seq_len, window, sinks, heads,
+        scale, out.data_ptr(), ws, ws_len, _raw_stream(dev.index))
+    if rc:
+        _lib.check(rc, "paged_attention_window")
+    return out
+
+
 def paged_block_copy(cache, pairs, stream=None):
     """Copy blocks ``pairs[i, 0] -> pairs[i, 1]`` (int64 ``[n, 2]``)."""
     _need(pairs, "pairs", torch.int64, cache.device)
@@ -552,6 +683,139 @@ def paged_build_tables(free_list, free_state, old_lens, new_lens, block_tables, 
     if rc:
         _lib.check(rc, "paged_build_tables")
     return seq_lens, free_state_out, query_starts, slot_mapping, positions
+
+
+def _need_pages(cache, free_list, free_state, extra_refs, block_tables, seq_lens):
+    """The checks that the calls on a pool's rows share; rows and width."""
+    dev = cache.device
+    _need(free_list, "free_list", torch.int32, dev)
+    _need(free_state, "free_state", torch.int64, dev)
+    _need(extra_refs, "extra_refs", torch.int32, dev)
+    _need(block_tables, "block_tables", torch.int32, dev)
+    _need(seq_lens, "seq_lens", torch.int32, dev)
+    if free_list.shape != (cache.num_blocks,) or extra_refs.shape != (cache.num_blocks,) or \
+            free_state.shape != (2,):
+        raise ValueError("free_list and extra_refs must be [num_blocks] and free_state [2]")
+    n = seq_lens.numel()
+    if seq_lens.shape != (n,) or block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("seq_lens must be [S] and block_tables [S, max_blocks]")
+    return n, block_tables.shape[1]
+
+
+def _out_table(t, name, shape, like):
+    """``t`` checked against the int32 table that the call writes, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=torch.int32, device=like.device)
+    _need(t, name, torch.int32, like.device)
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    return t
+
+
+def _scratch(workspace, need, dev):
+    """The workspace, given or new, its address and its size."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", None, dev)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def paged_fork_tables_workspace_bytes(num_seqs, num_next):
+    """Bytes of workspace that :func:`paged_fork_tables` needs."""
+    return int(_lib.lib().paged_fork_tables_workspace_bytes(_int32(num_seqs, "num_seqs"),
+                                                            _int32(num_next, "num_next")))
+
+
+def paged_fork_tables(cache, free_list, free_state, extra_refs, parents, block_tables, seq_lens,
+                      window=0, sinks=0, tables_out=None, lens_out=None, extra_out=None,
+                      free_state_out=None, workspace=None, stream=None):
+    """The rows of the next step, each continuing one of this step's rows
+    (``parents``, -1: an empty row), on the device: shared blocks are counted,
+    partly filled last blocks copied for all but their first child, and blocks
+    without a holder given back to the ring.
+
+    ``free_list``: int32 ``[num_blocks]`` ring, updated in place;
+    ``free_state``: int64 ``[2]`` (head, count); ``extra_refs``: int32
+    ``[num_blocks]``, each block's holders beyond the first; ``parents``: int32
+    ``[S_next]``; ``block_tables``: int32 ``[S, max_blocks]``; ``seq_lens``:
+    int32 ``[S]``; ``window``/``sinks``: blocks that no later query of
+    :func:`paged_attention_window` sees are given back (window 0: none).
+    Outputs are allocated when not given; ``extra_out`` may be ``extra_refs``
+    and ``free_state_out`` may be ``free_state``, the tables and lengths must
+    be new ones.  Returns ``(tables_out, lens_out, extra_out,
+    free_state_out)``.  A step that cannot be taken whole gives empty rows,
+    changes nothing else and sets a device error bit.
+    """
+    dev = cache.device
+    n, width = _need_pages(cache, free_list, free_state, extra_refs, block_tables, seq_lens)
+    _need(parents, "parents", torch.int32, dev)
+    nxt = parents.numel()
+    if parents.dim() != 1:
+        raise ValueError("parents must be [S_next]")
+    window, sinks = _int32(window, "window"), _int32(sinks, "sinks")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return paged_fork_tables(cache, free_list, free_state, extra_refs, parents,
+                                     block_tables, seq_lens, window, sinks, tables_out, lens_out,
+                                     extra_out, free_state_out, workspace)
+    tables_out = _out_table(tables_out, "tables_out", (nxt, width), free_list)
+    lens_out = _out_table(lens_out, "lens_out", (nxt,), free_list)
+    extra_out = _out_table(extra_out, "extra_out", (cache.num_blocks,), free_list)
+    free_state_out = _output(free_state_out, "free_state_out", 2, torch.int64, dev)
+    lib = _lib.lib()
+    workspace, ws, ws_len = _scratch(workspace, lib.paged_fork_tables_workspace_bytes(n, nxt), dev)
+    rc = lib.paged_fork_tables(
+        cache.ref, free_list.data_ptr(), free_state.data_ptr(), extra_refs.data_ptr(),
+        parents.data_ptr(), nxt, block_tables.data_ptr(), width, seq_lens.data_ptr(), n, window,
+        sinks, tables_out.data_ptr(), lens_out.data_ptr(), extra_out.data_ptr(),
+        free_state_out.data_ptr(), ws, ws_len, _raw_stream(dev.index))
+    if rc:
+        _lib.check(rc, "paged_fork_tables")
+    return tables_out, lens_out, extra_out, free_state_out
+
+
+def paged_compact_workspace_bytes(num_blocks):
+    """Bytes of workspace that :func:`paged_compact` needs."""
+    return int(_lib.lib().paged_compact_workspace_bytes(num_blocks))
+
+
+def paged_compact(cache, free_list, free_state, extra_refs, block_tables, seq_lens,
+                  tables_out=None, extra_out=None, free_state_out=None, moved_to=None,
+                  workspace=None, stream=None):
+    """Move the blocks that the rows hold to the front of the pool.
+
+    Arguments as for :func:`paged_fork_tables`; ``free_list`` is rewritten in
+    place.  Outputs are allocated when not given; ``tables_out``,
+    ``extra_out`` and ``free_state_out`` may be the inputs.  Returns
+    ``(tables_out, extra_out, free_state_out, moved_to)``: ``moved_to`` (int32
+    ``[num_blocks]``) is each held block's new id, -1 for the others; the free
+    blocks are the last ``free_state_out[1]``.  Where free and held blocks are
+    not all there are, nothing moves and a device error bit is set.
+    """
+    dev = cache.device
+    n, width = _need_pages(cache, free_list, free_state, extra_refs, block_tables, seq_lens)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return paged_compact(cache, free_list, free_state, extra_refs, block_tables, seq_lens,
+                                 tables_out, extra_out, free_state_out, moved_to, workspace)
+    tables_out = _out_table(tables_out, "tables_out", (n, width), free_list)
+    extra_out = _out_table(extra_out, "extra_out", (cache.num_blocks,), free_list)
+    moved_to = _out_table(moved_to, "moved_to", (cache.num_blocks,), free_list)
+    free_state_out = _output(free_state_out, "free_state_out", 2, torch.int64, dev)
+    lib = _lib.lib()
+    workspace, ws, ws_len = _scratch(workspace, lib.paged_compact_workspace_bytes(cache.num_blocks),
+                                     dev)
+    rc = lib.paged_compact(
+        cache.ref, free_list.data_ptr(), free_state.data_ptr(), extra_refs.data_ptr(),
+        block_tables.data_ptr(), width, seq_lens.data_ptr(), n, tables_out.data_ptr(),
+        extra_out.data_ptr(), free_state_out.data_ptr(), moved_to.data_ptr(), ws, ws_len,
+        _raw_stream(dev.index))
+    if rc:
+        _lib.check(rc, "paged_compact")
+    return tables_out, extra_out, free_state_out, moved_to
 
 
 def paged_get_device_error(stream=None):

@@ -55,11 +55,20 @@ class pkv_rotary(ctypes.Structure):
     ]
 
 
+class pkv_norm_weight(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("per_head", ctypes.c_int32),
+    ]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _CACHE = ctypes.POINTER(pkv_cache)
 _ROTARY = ctypes.POINTER(pkv_rotary)
+_WEIGHT = ctypes.POINTER(pkv_norm_weight)
 
 # name -> (restype, argtypes); every symbol the header declares.
 SIGNATURES = {
@@ -84,6 +93,20 @@ SIGNATURES = {
     "paged_rotary_init": (ctypes.c_int, [_ROTARY, _I32, _I32, _P, _P, _I32]),
     "paged_rope_kv_write": (ctypes.c_int, [_CACHE, _ROTARY, _P, _I64, _P, _I64, _P, _I64, _P, _P,
                                            _I64, _I32, _P, _I64, _P]),
+    "paged_norm_rope_kv_write": (ctypes.c_int, [_CACHE, _ROTARY, _P, _I64, _P, _I64, _P, _I64, _P,
+                                                _P, _I64, _I32, _WEIGHT, _WEIGHT, ctypes.c_float,
+                                                _P, _I64, _P]),
+    "paged_attention_window_workspace_bytes": (ctypes.c_size_t, [_CACHE, _I64, _I32, _I32, _I32,
+                                                                 _I32, _I32, _I32]),
+    "paged_attention_window": (ctypes.c_int, [_CACHE, _P, _I64, _P, _I32, _I32, _P, _I32, _P, _I32,
+                                              _I32, _I32, _I32, ctypes.c_float, _P, _P,
+                                              ctypes.c_size_t, _P]),
+    "paged_fork_tables_workspace_bytes": (ctypes.c_size_t, [_I32, _I32]),
+    "paged_fork_tables": (ctypes.c_int, [_CACHE, _P, _P, _P, _P, _I32, _P, _I32, _P, _I32, _I32,
+                                         _I32, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "paged_compact_workspace_bytes": (ctypes.c_size_t, [_I64]),
+    "paged_compact": (ctypes.c_int, [_CACHE, _P, _P, _P, _P, _I32, _P, _I32, _P, _P, _P, _P, _P,
+                                     ctypes.c_size_t, _P]),
     "paged_build_tables": (ctypes.c_int, [_I64, _I32, _P, _P, _P, _P, _I32, _P, _I32, _P, _P, _P,
                                           _P, _P, _I64, _P]),
     "paged_get_device_error": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_uint32)]),

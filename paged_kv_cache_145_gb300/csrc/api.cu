@@ -20,6 +20,27 @@ int pkv_launch_cross_tc_fp8(const pkv::CrossParams&, int, int, bool, const pkv::
                             cudaStream_t);
 int pkv_launch_cross(const pkv::CrossParams& p, int dtype, int io_dtype, int num_seqs, int dim,
                      cudaStream_t stream);
+int pkv_launch_window(const pkv::WindowParams& p, int dtype, int io_dtype, int num_seqs, int dim,
+                      cudaStream_t stream);
+size_t pkv_fork_workspace(int rows, int next);
+int pkv_launch_fork_tables(const pkv_cache* c, size_t elem_bytes, int32_t* ring,
+                           const int64_t* state, const int32_t* extra, const int32_t* parents,
+                           int next, const int32_t* tables, const int32_t* lens, int rows,
+                           int width, int window, int sinks, int32_t* tables_out,
+                           int32_t* lens_out, int32_t* extra_out, int64_t* state_out,
+                           void* workspace, cudaStream_t stream);
+size_t pkv_compact_workspace(int64_t num_blocks);
+int pkv_launch_compact(const pkv_cache* c, size_t elem_bytes, int32_t* ring, const int64_t* state,
+                       const int32_t* extra, const int32_t* tables, const int32_t* lens, int rows,
+                       int width, int32_t* tables_out, int32_t* extra_out, int64_t* state_out,
+                       int32_t* moved_to, void* workspace, cudaStream_t stream);
+int pkv_launch_norm_rope_write(const pkv_cache* c, const pkv_rotary* rot, const void* q,
+                               int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, const int32_t* positions, const int64_t* slots,
+                               int64_t num_tokens, int num_heads, const void* q_weight,
+                               int q_weight_stride, bool q_weight_f32, const void* k_weight,
+                               int k_weight_stride, bool k_weight_f32, float eps, void* q_out,
+                               int64_t q_out_stride, cudaStream_t stream);
 int pkv_launch_rope_write(const pkv_cache* c, const pkv_rotary* rot, const void* q,
                           int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                           int64_t v_stride, const int32_t* positions, const int64_t* slots,
@@ -268,11 +289,12 @@ int paged_kv_write(const pkv_cache* cache, const void* k, const void* v,
                              stream);
 }
 
-int paged_rope_kv_write(const pkv_cache* cache, const pkv_rotary* rotary, const void* q,
-                        int64_t q_stride, const void* k, int64_t k_stride, const void* v,
-                        int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping,
-                        int64_t num_tokens, int32_t num_heads, void* q_out, int64_t q_out_stride,
-                        cudaStream_t stream) {
+// The checks of a rotary write; PKV_OK with num_tokens 0 means nothing to do.
+static int check_rope_write(const pkv_cache* cache, const pkv_rotary* rotary, const void* q,
+                            int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, const int32_t* positions,
+                            const int64_t* slot_mapping, int64_t num_tokens, int32_t num_heads,
+                            void* q_out, int64_t q_out_stride) {
   int rc = check_cache(cache);
   if (rc) return rc;
   rc = check_scales(cache);
@@ -301,9 +323,49 @@ int paged_rope_kv_write(const pkv_cache* cache, const pkv_rotary* rotary, const 
       (reinterpret_cast<uintptr_t>(positions) & 3u) ||
       (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
     return PKV_ERR_ALIGN;
+  return PKV_OK;
+}
+
+int paged_rope_kv_write(const pkv_cache* cache, const pkv_rotary* rotary, const void* q,
+                        int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping,
+                        int64_t num_tokens, int32_t num_heads, void* q_out, int64_t q_out_stride,
+                        cudaStream_t stream) {
+  const int rc = check_rope_write(cache, rotary, q, q_stride, k, k_stride, v, v_stride, positions,
+                                  slot_mapping, num_tokens, num_heads, q_out, q_out_stride);
+  if (rc || num_tokens == 0) return rc;
   if (!pkv_error_word()) return PKV_ERR_CUDA;
   return pkv_launch_rope_write(cache, rotary, q, q_stride, k, k_stride, v, v_stride, positions,
                                slot_mapping, num_tokens, num_heads, q_out, q_out_stride, stream);
+}
+
+int paged_norm_rope_kv_write(const pkv_cache* cache, const pkv_rotary* rotary, const void* q,
+                             int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, const int32_t* positions,
+                             const int64_t* slot_mapping, int64_t num_tokens, int32_t num_heads,
+                             const pkv_norm_weight* q_weight, const pkv_norm_weight* k_weight,
+                             float eps, void* q_out, int64_t q_out_stride, cudaStream_t stream) {
+  const int rc = check_rope_write(cache, rotary, q, q_stride, k, k_stride, v, v_stride, positions,
+                                  slot_mapping, num_tokens, num_heads, q_out, q_out_stride);
+  if (rc) return rc;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return PKV_ERR_ARG;
+  // A head's vectors lie in one warp, two a lane.
+  const int io = cache->dtype == PKV_FP8_E4M3 ? cache->io_dtype : cache->dtype;
+  if ((int64_t)cache->head_dim * (int64_t)elem_bytes(io) > 1024) return PKV_ERR_GEOMETRY;
+  const pkv_norm_weight none{};
+  const pkv_norm_weight* w[2] = {q_weight ? q_weight : &none, k_weight ? k_weight : &none};
+  for (const pkv_norm_weight* x : w) {
+    if (!x->data) continue;
+    if (x->dtype != PKV_F32 && x->dtype != io) return PKV_ERR_ARG;
+    if (!aligned16(x->data)) return PKV_ERR_ALIGN;
+  }
+  if (num_tokens == 0) return PKV_OK;
+  if (!pkv_error_word()) return PKV_ERR_CUDA;
+  const int D = cache->head_dim;
+  return pkv_launch_norm_rope_write(
+      cache, rotary, q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping, num_tokens,
+      num_heads, w[0]->data, w[0]->per_head ? D : 0, w[0]->dtype == PKV_F32, w[1]->data,
+      w[1]->per_head ? D : 0, w[1]->dtype == PKV_F32, eps, q_out, q_out_stride, stream);
 }
 
 int32_t paged_attention_partition_size(const pkv_cache* cache, int32_t num_seqs,
@@ -641,12 +703,15 @@ size_t paged_attention_cross_workspace_bytes(const pkv_cache* cache, int64_t tot
   return cross_workspace(total_queries, num_heads, cache->head_dim, sp.parts).total;
 }
 
-int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_queries,
-                          const int32_t* query_starts, int32_t num_seqs, int32_t max_queries,
-                          const int32_t* block_tables, int32_t max_blocks_per_seq,
-                          const int32_t* enc_lens, int32_t max_enc_len, int32_t num_heads,
-                          float scale, void* out, void* workspace, size_t workspace_bytes,
-                          cudaStream_t stream) {
+// Checks the arguments that cross and windowed attention share and fills the
+// parameters that do not depend on the plan; *any is false where there is
+// nothing to do.
+static int cross_params(pkv::CrossParams* out_p, bool* any, const pkv_cache* cache, const void* q,
+                        int64_t total_queries, const int32_t* query_starts, int32_t num_seqs,
+                        int32_t max_queries, const int32_t* block_tables,
+                        int32_t max_blocks_per_seq, const int32_t* lens, int32_t max_len_arg,
+                        int32_t num_heads, float scale, void* out) {
+  *any = false;
   int rc = check_cache(cache);
   if (rc) return rc;
   rc = check_scales(cache);
@@ -658,23 +723,15 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
   if (num_seqs == 0 || total_queries == 0) return PKV_OK;
   max_queries = cross_max_queries(max_queries, total_queries);
   const int64_t cap = (int64_t)max_blocks_per_seq * cache->block_size;
-  if (max_enc_len < 0 || max_enc_len > cap || (max_enc_len ? max_enc_len : cap) > (1 << 30))
+  if (max_len_arg < 0 || max_len_arg > cap || (max_len_arg ? max_len_arg : cap) > (1 << 30))
     return PKV_ERR_ARG;
-  const int max_len = max_enc_len ? max_enc_len : (int)cap;
-  if (!q || !out || !query_starts || !enc_lens || (!block_tables && max_len > 0)) return PKV_ERR_NULL;
+  const int max_len = max_len_arg ? max_len_arg : (int)cap;
+  if (!q || !out || !query_starts || !lens || (!block_tables && max_len > 0)) return PKV_ERR_NULL;
   if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
-      (reinterpret_cast<uintptr_t>(enc_lens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(lens) & 3u) ||
       (reinterpret_cast<uintptr_t>(query_starts) & 3u))
     return PKV_ERR_ALIGN;
-  const CrossPlan sp = cross_plan(cache, num_seqs, num_heads, max_queries, max_len);
-  const WsLayout ws = cross_workspace(total_queries, num_heads, cache->head_dim, sp.parts);
-  if (ws.total > 0) {
-    if (!workspace || workspace_bytes < ws.total) return PKV_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return PKV_ERR_ALIGN;
-  }
-  unsigned* err = pkv_error_word();
-  if (!err) return PKV_ERR_CUDA;
-  pkv::CrossParams p{};
+  pkv::CrossParams& p = *out_p;
   p.k_cache = cache->k_cache;
   p.v_cache = cache->v_cache;
   p.num_blocks = cache->num_blocks;
@@ -689,16 +746,46 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
   p.max_queries = max_queries;
   p.tables = block_tables;
   p.max_blocks = max_blocks_per_seq;
-  p.lens = enc_lens;
+  p.lens = lens;
   p.max_len = max_len;
   p.qscale = scale * 1.4426950408889634f;  // log2(e): scores in base-2 units
-  p.parts = sp.parts;
-  p.part = sp.part;
-  p.ws_ml = ws.total ? static_cast<float2*>(workspace) : nullptr;
-  p.ws_o = ws.total ? reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.o_offset) : nullptr;
   p.k_scale = cache->k_scale;
   p.v_scale = cache->v_scale;
-  p.err = err;
+  *any = true;
+  return PKV_OK;
+}
+
+// The rest of them: the plan's parts and the caller's workspace for them.
+static int cross_workspace_params(pkv::CrossParams* p, const pkv_cache* cache, int parts, int part,
+                                  void* workspace, size_t workspace_bytes) {
+  const WsLayout ws = cross_workspace(p->total_queries, p->num_heads, cache->head_dim, parts);
+  if (ws.total > 0) {
+    if (!workspace || workspace_bytes < ws.total) return PKV_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return PKV_ERR_ALIGN;
+  }
+  p->parts = parts;
+  p->part = part;
+  p->ws_ml = ws.total ? static_cast<float2*>(workspace) : nullptr;
+  p->ws_o = ws.total ? reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.o_offset) : nullptr;
+  p->err = pkv_error_word();
+  return p->err ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_queries,
+                          const int32_t* query_starts, int32_t num_seqs, int32_t max_queries,
+                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                          const int32_t* enc_lens, int32_t max_enc_len, int32_t num_heads,
+                          float scale, void* out, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream) {
+  pkv::CrossParams p{};
+  bool any = false;
+  int rc = cross_params(&p, &any, cache, q, total_queries, query_starts, num_seqs, max_queries,
+                        block_tables, max_blocks_per_seq, enc_lens, max_enc_len, num_heads, scale,
+                        out);
+  if (rc || !any) return rc;
+  const CrossPlan sp = cross_plan(cache, num_seqs, num_heads, p.max_queries, p.max_len);
+  rc = cross_workspace_params(&p, cache, sp.parts, sp.part, workspace, workspace_bytes);
+  if (rc) return rc;
   if (!sp.tc)
     return pkv_launch_cross(p, cache->dtype, cache->io_dtype, num_seqs, cache->head_dim, stream);
   // Pages are a 32-bit coordinate, and one past the last is used.
@@ -711,6 +798,67 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
     return pkv_launch_cross_tc_fp8(p, cache->io_dtype, num_seqs, sp.wide, maps, stream);
   return (cache->dtype == PKV_F16 ? pkv_launch_cross_tc_f16 : pkv_launch_cross_tc_bf16)(
       p, num_seqs, cache->head_dim, maps, stream);
+}
+
+namespace {
+
+// How windowed attention runs.
+struct WindowPlan {
+  int parts, part, tile_queries;
+};
+
+WindowPlan window_plan(const pkv_cache* c, int num_seqs, int num_heads, int max_queries, int window,
+                       int sinks, int max_len) {
+  WindowPlan w{};
+  const int G = num_heads / c->num_kv_heads;
+  w.tile_queries = std::max(1, pkv::kCrossRows / G);
+  // The most positions that a row tile walks, in tiles of 64.
+  const int64_t whole = ((int64_t)max_len + 63) / 64;
+  const int64_t most = (std::min<int64_t>(sinks, max_len) + 63) / 64 +
+                       ((int64_t)window + std::min(w.tile_queries, max_queries) + 61) / 64 + 1;
+  const int span = (int)std::min(whole, most) * 64;
+  const CrossPlan sp = cross_plan(c, num_seqs, num_heads, max_queries, span);
+  w.parts = sp.parts;
+  w.part = sp.part;
+  return w;
+}
+
+}  // namespace
+
+size_t paged_attention_window_workspace_bytes(const pkv_cache* cache, int64_t total_queries,
+                                              int32_t num_seqs, int32_t num_heads,
+                                              int32_t max_queries, int32_t window, int32_t sinks,
+                                              int32_t max_seq_len) {
+  if (!cache || !cross_args_ok(cache, total_queries, num_seqs, num_heads, max_queries) ||
+      window < 1 || sinks < 0 || max_seq_len < 0 || max_seq_len > (1 << 30))
+    return 0;
+  max_queries = cross_max_queries(max_queries, total_queries);
+  const WindowPlan w =
+      window_plan(cache, num_seqs, num_heads, max_queries, window, sinks, max_seq_len);
+  return cross_workspace(total_queries, num_heads, cache->head_dim, w.parts).total;
+}
+
+int paged_attention_window(const pkv_cache* cache, const void* q, int64_t total_queries,
+                           const int32_t* query_starts, int32_t num_seqs, int32_t max_queries,
+                           const int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* seq_lens, int32_t max_seq_len, int32_t window,
+                           int32_t sinks, int32_t num_heads, float scale, void* out,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (window < 1 || sinks < 0) return PKV_ERR_ARG;
+  pkv::WindowParams p{};
+  bool any = false;
+  const int rc = cross_params(&p, &any, cache, q, total_queries, query_starts, num_seqs,
+                              max_queries, block_tables, max_blocks_per_seq, seq_lens, max_seq_len,
+                              num_heads, scale, out);
+  if (rc || !any) return rc;
+  const WindowPlan w =
+      window_plan(cache, num_seqs, num_heads, p.max_queries, window, sinks, p.max_len);
+  p.window = window;
+  p.sinks = sinks;
+  p.tile_queries = w.tile_queries;
+  const int wrc = cross_workspace_params(&p, cache, w.parts, w.part, workspace, workspace_bytes);
+  if (wrc) return wrc;
+  return pkv_launch_window(p, cache->dtype, cache->io_dtype, num_seqs, cache->head_dim, stream);
 }
 
 int paged_block_copy(const pkv_cache* cache, const int64_t* src_dst_pairs, int64_t num_pairs,
@@ -726,6 +874,83 @@ int paged_block_copy(const pkv_cache* cache, const int64_t* src_dst_pairs, int64
     return PKV_ERR_GEOMETRY;
   if (!pkv_error_word()) return PKV_ERR_CUDA;
   return pkv_launch_block_copy(cache, src_dst_pairs, num_pairs, elem_bytes(cache->dtype), stream);
+}
+
+size_t paged_fork_tables_workspace_bytes(int32_t num_seqs, int32_t num_next) {
+  if (num_seqs < 0 || num_seqs > 65535 || num_next < 0 || num_next > 65535) return 0;
+  return pkv_fork_workspace(num_seqs, num_next);
+}
+
+// Checks that paged_fork_tables and paged_compact share.
+static int check_pages(const pkv_cache* cache, const void* free_list, const void* free_state,
+                       const void* extra_refs, const void* tables, const void* lens,
+                       int32_t num_seqs, int32_t width, const void* tables_out,
+                       const void* extra_out, const void* state_out, const void* workspace) {
+  const int rc = check_cache(cache);
+  if (rc) return rc;
+  if (cache->num_blocks > (1 << 30) || num_seqs < 0 || num_seqs > 65535 || width < 1 ||
+      (int64_t)num_seqs * width > (1 << 30) || (int64_t)width * cache->block_size > INT32_MAX)
+    return PKV_ERR_ARG;
+  if ((int64_t)cache->num_kv_heads * cache->block_size * cache->head_dim *
+          (int64_t)elem_bytes(cache->dtype) % 16)
+    return PKV_ERR_GEOMETRY;
+  if (!free_list || !free_state || !extra_refs || !extra_out || !state_out) return PKV_ERR_NULL;
+  if (num_seqs > 0 && (!tables || !lens)) return PKV_ERR_NULL;
+  if (!workspace) return PKV_ERR_WORKSPACE;
+  for (const void* x : {free_list, extra_refs, tables, lens, tables_out, extra_out})
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return PKV_ERR_ALIGN;
+  for (const void* x : {free_state, state_out})
+    if (reinterpret_cast<uintptr_t>(x) & 7u) return PKV_ERR_ALIGN;
+  return aligned16(workspace) ? PKV_OK : PKV_ERR_ALIGN;
+}
+
+int paged_fork_tables(const pkv_cache* cache, int32_t* free_list, const int64_t* free_state,
+                      const int32_t* extra_refs, const int32_t* parents, int32_t num_next,
+                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                      const int32_t* seq_lens, int32_t num_seqs, int32_t window, int32_t sinks,
+                      int32_t* tables_out, int32_t* lens_out, int32_t* extra_out,
+                      int64_t* state_out, void* workspace, size_t workspace_bytes,
+                      cudaStream_t stream) {
+  const int rc = check_pages(cache, free_list, free_state, extra_refs, block_tables, seq_lens,
+                             num_seqs, max_blocks_per_seq, tables_out, extra_out, state_out,
+                             workspace);
+  if (rc) return rc;
+  if (num_next < 0 || num_next > 65535 || (int64_t)num_next * max_blocks_per_seq > (1 << 30) ||
+      window < 0 || sinks < 0)
+    return PKV_ERR_ARG;
+  if (num_next > 0 && (!parents || !tables_out || !lens_out)) return PKV_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(parents) & 3u) || (reinterpret_cast<uintptr_t>(lens_out) & 3u))
+    return PKV_ERR_ALIGN;
+  if (num_next > 0 && (tables_out == block_tables || lens_out == seq_lens)) return PKV_ERR_ARG;
+  if (workspace_bytes < pkv_fork_workspace(num_seqs, num_next)) return PKV_ERR_WORKSPACE;
+  if (!pkv_error_word()) return PKV_ERR_CUDA;
+  return pkv_launch_fork_tables(cache, elem_bytes(cache->dtype), free_list, free_state, extra_refs,
+                                parents, num_next, block_tables, seq_lens, num_seqs,
+                                max_blocks_per_seq, window, sinks, tables_out, lens_out, extra_out,
+                                state_out, workspace, stream);
+}
+
+size_t paged_compact_workspace_bytes(int64_t num_blocks) {
+  if (num_blocks < 1 || num_blocks > (1 << 30)) return 0;
+  return pkv_compact_workspace(num_blocks);
+}
+
+int paged_compact(const pkv_cache* cache, int32_t* free_list, const int64_t* free_state,
+                  const int32_t* extra_refs, const int32_t* block_tables,
+                  int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs,
+                  int32_t* tables_out, int32_t* extra_out, int64_t* state_out, int32_t* moved_to,
+                  void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  const int rc = check_pages(cache, free_list, free_state, extra_refs, block_tables, seq_lens,
+                             num_seqs, max_blocks_per_seq, tables_out, extra_out, state_out,
+                             workspace);
+  if (rc) return rc;
+  if (!moved_to || (num_seqs > 0 && !tables_out)) return PKV_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(moved_to) & 3u) return PKV_ERR_ALIGN;
+  if (workspace_bytes < pkv_compact_workspace(cache->num_blocks)) return PKV_ERR_WORKSPACE;
+  if (!pkv_error_word()) return PKV_ERR_CUDA;
+  return pkv_launch_compact(cache, elem_bytes(cache->dtype), free_list, free_state, extra_refs,
+                            block_tables, seq_lens, num_seqs, max_blocks_per_seq, tables_out,
+                            extra_out, state_out, moved_to, workspace, stream);
 }
 
 // Device-side address of a host pool, or nullptr if the memory is neither

@@ -1,5 +1,6 @@
-// Cross attention over paged encoder states: parameters, the CUDA-core
-// kernel and the merge of split states.  (Tensor cores: cross_tc.cuh.)
+// Cross attention over paged encoder states, and causal attention with a
+// sliding window: parameters, the CUDA-core kernel and the merge of split keys.
+// (Tensor cores: cross_tc.cuh, window_token.cuh.)
 //
 // Sequence s has Q queries and L states, no mask between them: each row (a
 // query of one head) is softmax(scale * q.K^T) V over positions 0 .. L - 1.
@@ -9,6 +10,14 @@
 // part leaves its rows' maximum and sum of 2^(z - m) and the normalised
 // output, and cross_merge_kernel joins them.  A sequence that fits one part
 // writes its rows directly.
+//
+// With a window the L positions are the sequence's own, the last Q of them the
+// queries', and the query at position p sees t <= p with t < sinks or
+// t > p - window.  A thread block's rows see two runs of positions together,
+// [0, s0) and [w0, last]; the block walks the tiles that hold them as if they
+// were one run (WindowSpan), and everything that counts tiles or parts counts
+// these.  Pages that no query sees are not read, whatever their table entries
+// hold.
 #pragma once
 
 #include <type_traits>
@@ -41,6 +50,41 @@ struct CrossParams {
   unsigned* err;
 };
 
+struct WindowParams : CrossParams {
+  int window, sinks;
+  int tile_queries;         // queries in a row tile
+};
+
+// Whether the query at position p sees position t.
+__device__ __forceinline__ bool window_sees(const WindowParams& p, int pos, int t) {
+  return t <= pos && (t < p.sinks || t > pos - p.window);
+}
+
+// The tiles of KT positions with what queries at positions first .. last see.
+template <int KT>
+struct WindowSpan {
+  int s0, w0;       // seen by one of them: t < s0, and w0 <= t <= last
+  int last;
+  int head, skip;   // tiles before the gap, tiles in it
+  int tiles;
+
+  __device__ __forceinline__ WindowSpan(const WindowParams& p, int first, int last_)
+      : last(last_) {
+    w0 = max(0, first - p.window + 1);
+    s0 = min(p.sinks, w0);
+    head = (s0 + KT - 1) / KT;
+    skip = max(0, w0 / KT - head);
+    tiles = last / KT + 1 - skip;
+  }
+  // First position of the j-th tile.
+  __device__ __forceinline__ int pos(int j) const { return (j < head ? j : j + skip) * KT; }
+  __device__ __forceinline__ bool sees(int t) const { return t <= last && (t < s0 || t >= w0); }
+  // Whether any position of a page of `size` positions from t on is seen.
+  __device__ __forceinline__ bool sees_page(int t, int size) const {
+    return t <= last && (t < s0 || t + size > w0);
+  }
+};
+
 // Where a sequence's rows are and whether its numbers hold.
 struct CrossSeq {
   int q0, Q, L;     // first query, queries, states (0 after a bad length)
@@ -65,6 +109,43 @@ __device__ __forceinline__ CrossSeq cross_seq(const CrossParams& p, int s) {
   return c;
 }
 
+// L is the sequence's length with its queries; parts are of the tiles of 64
+// that a row tile walks (where it walks fewer than the sequence's other row
+// tiles its last parts are empty).
+__device__ __forceinline__ CrossSeq cross_seq(const WindowParams& p, int s) {
+  CrossSeq c = cross_seq(static_cast<const CrossParams&>(p), s);
+  if (c.Q > c.L) c.bits = PKV_DEV_SEQ_LEN;
+  c.parts = 1;
+  if (c.bits || c.Q == 0) {
+    c.L = 0;
+    return c;
+  }
+  int tiles = WindowSpan<64>(p, c.L - c.Q, c.L - 1).tiles;
+  if (c.Q > p.tile_queries) {
+    const int64_t most = (min(p.sinks, c.L) + 63) / 64 +
+                         ((int64_t)p.window + p.tile_queries + 61) / 64 + 1;
+    tiles = (int)min((int64_t)tiles, most);
+  }
+  c.parts = (tiles + p.part / 64 - 1) / (p.part / 64);
+  return c;
+}
+
+// Whether an entry of a table row that the sequence's queries read is out of
+// range, in one of `threads` threads' share of them.
+__device__ __forceinline__ bool window_row_bad(const WindowParams& p, const CrossSeq& c,
+                                               const int32_t* trow, int thread, int threads) {
+  const WindowSpan<64> span(p, c.L - c.Q, c.L - 1);
+  const int b = p.block_size;
+  const int head = (span.s0 + b - 1) / b, gap = max(0, span.w0 / b - head);
+  const int n = span.last / b + 1 - gap;
+  bool bad = false;
+  for (int i = thread; i < n; i += threads) {
+    const int e = trow[i < head ? i : i + gap];
+    bad |= e < 0 || (int64_t)e >= p.num_blocks;
+  }
+  return bad;
+}
+
 // One warp per row: joins the parts of a sequence's rows.  With
 // M = max m_i, w_i = l_i 2^(m_i - M): out = sum w_i o_i / sum w_i.  A part
 // whose scores are all -inf has l = 0 and weighs nothing (its o is read all the
@@ -72,8 +153,8 @@ __device__ __forceinline__ CrossSeq cross_seq(const CrossParams& p, int s) {
 // parts of a sequence with a bad table have l = 1 and o = 0.
 constexpr int kCrossMergeWarps = 4;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kCrossMergeWarps * 32) cross_merge_kernel(const CrossParams p) {
+template <typename T, int D, typename P>
+__global__ void __launch_bounds__(kCrossMergeWarps * 32) cross_merge_kernel(const P p) {
   const CrossSeq c = cross_seq(p, blockIdx.y);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the parts are computed
   if (c.parts <= 1) return;  // written directly
@@ -129,9 +210,12 @@ constexpr int kCrossWarps = 4;
 // takes every fourth run of 32 keys with its own running maximum and sum.
 // Scores: a lane per key, queries broadcast from shared memory.  Values: a
 // lane per D / 32 dimensions, the probabilities passed by shuffles.  The
-// four warps' results are joined in shared memory.
-template <typename T, typename TC, int D>
-__global__ void __launch_bounds__(kCrossWarps * 32) cross_kernel(const CrossParams p) {
+// four warps' results are joined in shared memory.  With a window (P is
+// WindowParams) a key that a row does not see is left out of its sums, so that
+// nothing in a hidden place reaches it.
+template <typename T, typename TC, int D, typename P>
+__global__ void __launch_bounds__(kCrossWarps * 32) cross_kernel(const P p) {
+  constexpr bool WIN = std::is_same<P, WindowParams>::value;
   constexpr int R = kCrossRows, E = D / 32;
   __shared__ __align__(16) float s_q[R][D];
   __shared__ __align__(16) float s_o[kCrossWarps][R][D];
@@ -158,10 +242,14 @@ __global__ void __launch_bounds__(kCrossWarps * 32) cross_kernel(const CrossPara
   const int nr = min(R, rows - r0);
   const int32_t* trow = p.tables + (int64_t)s * p.max_blocks;
   int bad = 0;
-  const int nblk = c.L > 0 ? (c.L - 1) / b + 1 : 0;
-  for (int i = tid; i < nblk; i += kCrossWarps * 32) {
-    const int e = trow[i];
-    bad |= e < 0 || (int64_t)e >= p.num_blocks;
+  if constexpr (WIN) {
+    bad = window_row_bad(p, c, trow, tid, kCrossWarps * 32);
+  } else {
+    const int nblk = c.L > 0 ? (c.L - 1) / b + 1 : 0;
+    for (int i = tid; i < nblk; i += kCrossWarps * 32) {
+      const int e = trow[i];
+      bad |= e < 0 || (int64_t)e >= p.num_blocks;
+    }
   }
   constexpr bool kFp8 = std::is_same<TC, __nv_fp8_e4m3>::value;
   const float qs = p.qscale * (kFp8 ? p.k_scale[kvh] : 1.f);
@@ -185,14 +273,31 @@ __global__ void __launch_bounds__(kCrossWarps * 32) cross_kernel(const CrossPara
   }
   const TC* const kp = static_cast<const TC*>(p.k_cache);
   const TC* const vp = static_cast<const TC*>(p.v_cache);
-  const int lo = part * p.part, hi = bad ? lo : min(c.L, lo + p.part);
-  for (int k0 = lo + warp * 32; k0 < hi; k0 += kCrossWarps * 32) {
-    const int n = min(32, hi - k0), key = k0 + min(lane, n - 1);
-    const int64_t at = (((int64_t)trow[key / b] * p.kv_heads + kvh) * b + key % b) * D;
+  // The block's keys: runs of 32 positions (with a window, tiles of its span).
+  int lo = part * p.part, hi = bad ? lo : min(c.L, lo + p.part);
+  [[maybe_unused]] const int base = c.L - c.Q;  // the first query's position
+  auto span = [&] {
+    if constexpr (WIN) return WindowSpan<32>(p, base + r0 / G, base + (r0 + nr - 1) / G);
+    else return 0;
+  }();
+  if constexpr (WIN) hi = bad ? lo : min(span.tiles * 32, lo + p.part);
+  for (int v0 = lo + warp * 32; v0 < hi; v0 += kCrossWarps * 32) {
+    int n = min(32, hi - v0), key = v0 + min(lane, n - 1);
+    bool seen = true;
+    if constexpr (WIN) {
+      const int k0 = span.pos(v0 / 32);
+      n = min(32, span.last + 1 - k0);
+      key = k0 + min(lane, n - 1);
+      seen = span.sees(key);
+    }
+    // (the entries of pages that no row sees may be anything)
+    const int64_t at =
+        seen ? (((int64_t)trow[key / b] * p.kv_heads + kvh) * b + key % b) * D : -1;
     float z[R] = {};
 #pragma unroll 4
     for (int d = 0; d < D; d += 4) {
       float f[4];
+      if (WIN && !seen) break;
       CacheRow<TC, 4>::load(kp + at + d, f);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -200,9 +305,15 @@ __global__ void __launch_bounds__(kCrossWarps * 32) cross_kernel(const CrossPara
         z[r] += x.x * f[0] + x.y * f[1] + x.z * f[2] + x.w * f[3];
       }
     }
+    [[maybe_unused]] uint32_t sees[R];  // keys that row r sees
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      z[r] = lane < n ? z[r] * qs : -INFINITY;
+      bool ok = lane < n;
+      if constexpr (WIN) {
+        ok = ok && window_sees(p, base + (r0 + min(r, nr - 1)) / G, key);
+        sees[r] = __ballot_sync(kFullMask, ok);
+      }
+      z[r] = ok ? z[r] * qs : -INFINITY;
       float top = z[r];
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, d));
@@ -220,11 +331,13 @@ __global__ void __launch_bounds__(kCrossWarps * 32) cross_kernel(const CrossPara
 #pragma unroll 4
     for (int j = 0; j < n; ++j) {
       const int64_t vat = __shfl_sync(kFullMask, at, j);
+      if (WIN && vat < 0) continue;
       float f[E];
       CacheRow<TC, E>::load(vp + vat + lane * E, f);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const float w = __shfl_sync(kFullMask, z[r], j);
+        if (WIN && !(sees[r] >> j & 1u)) continue;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[r][e] += w * f[e];
       }
@@ -268,8 +381,8 @@ __global__ void __launch_bounds__(kCrossWarps * 32) cross_kernel(const CrossPara
   }
 }
 
-template <typename T, int D>
-int launch_cross_merge(const CrossParams& p, int num_seqs, cudaStream_t stream) {
+template <typename T, int D, typename P>
+int launch_cross_merge(const P& p, int num_seqs, cudaStream_t stream) {
   if (p.parts > 1) {
     const int64_t rows = (int64_t)p.max_queries * p.num_heads;
     cudaLaunchConfig_t cfg{};
@@ -281,7 +394,7 @@ int launch_cross_merge(const CrossParams& p, int num_seqs, cudaStream_t stream) 
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, cross_merge_kernel<T, D>, p) != cudaSuccess) return pkv_cuda_failed();
+    if (cudaLaunchKernelEx(&cfg, cross_merge_kernel<T, D, P>, p) != cudaSuccess) return pkv_cuda_failed();
   }
   return pkv_launch_status();
 }
