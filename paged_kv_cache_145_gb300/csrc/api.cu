@@ -20,6 +20,10 @@ int pkv_launch_cross_tc_fp8(const pkv::CrossParams&, int, int, bool, const pkv::
                             cudaStream_t);
 int pkv_launch_cross(const pkv::CrossParams& p, int dtype, int io_dtype, int num_seqs, int dim,
                      cudaStream_t stream);
+int pkv_launch_window_tc_f16(const pkv::WindowParams&, int, int, const pkv::CrossMaps&, cudaStream_t);
+int pkv_launch_window_tc_bf16(const pkv::WindowParams&, int, int, const pkv::CrossMaps&, cudaStream_t);
+int pkv_launch_window_tc_fp8(const pkv::WindowParams&, int, int, bool, const pkv::CrossMaps&,
+                             cudaStream_t);
 int pkv_launch_window(const pkv::WindowParams& p, int dtype, int io_dtype, int num_seqs, int dim,
                       cudaStream_t stream);
 size_t pkv_fork_workspace(int rows, int next);
@@ -609,13 +613,19 @@ struct CrossPlan {
   int parts, part;
 };
 
+bool tensor_cores(const pkv_cache* c) {
+  return c->dtype == PKV_F16 || c->dtype == PKV_BF16 ||
+         (c->dtype == PKV_FP8_E4M3 && c->head_dim == 128);
+}
+
+bool wide_rows(const pkv_cache* c, int64_t rows) { return c->dtype == PKV_FP8_E4M3 && rows > 128; }
+
 CrossPlan cross_plan(const pkv_cache* c, int num_seqs, int num_heads, int max_queries,
                      int max_len) {
   CrossPlan pl{};
-  pl.tc = c->dtype == PKV_F16 || c->dtype == PKV_BF16 ||
-          (c->dtype == PKV_FP8_E4M3 && c->head_dim == 128);
+  pl.tc = tensor_cores(c);
   const int64_t rows = (int64_t)max_queries * (num_heads / c->num_kv_heads);
-  pl.wide = c->dtype == PKV_FP8_E4M3 && rows > 128;
+  pl.wide = wide_rows(c, rows);
   static std::atomic<int> sm_count[kMaxDevices];  // looked up once per device
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) {
@@ -771,6 +781,15 @@ static int cross_workspace_params(pkv::CrossParams* p, const pkv_cache* cache, i
   return p->err ? PKV_OK : PKV_ERR_CUDA;
 }
 
+static int page_maps(pkv::CrossMaps* maps, const pkv_cache* cache) {
+  // Pages are a 32-bit coordinate, and one past the last is used.
+  if (cache->num_blocks * cache->num_kv_heads >= INT32_MAX) return PKV_ERR_ARG;
+  return encode_page_map(&maps->k, cache, cache->k_cache) &&
+                 encode_page_map(&maps->v, cache, cache->v_cache)
+             ? PKV_OK
+             : PKV_ERR_CUDA;
+}
+
 int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_queries,
                           const int32_t* query_starts, int32_t num_seqs, int32_t max_queries,
                           const int32_t* block_tables, int32_t max_blocks_per_seq,
@@ -788,12 +807,9 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
   if (rc) return rc;
   if (!sp.tc)
     return pkv_launch_cross(p, cache->dtype, cache->io_dtype, num_seqs, cache->head_dim, stream);
-  // Pages are a 32-bit coordinate, and one past the last is used.
-  if (cache->num_blocks * cache->num_kv_heads >= INT32_MAX) return PKV_ERR_ARG;
   pkv::CrossMaps maps;
-  if (!encode_page_map(&maps.k, cache, cache->k_cache) ||
-      !encode_page_map(&maps.v, cache, cache->v_cache))
-    return PKV_ERR_CUDA;
+  rc = page_maps(&maps, cache);
+  if (rc) return rc;
   if (cache->dtype == PKV_FP8_E4M3)
     return pkv_launch_cross_tc_fp8(p, cache->io_dtype, num_seqs, sp.wide, maps, stream);
   return (cache->dtype == PKV_F16 ? pkv_launch_cross_tc_f16 : pkv_launch_cross_tc_bf16)(
@@ -804,6 +820,7 @@ namespace {
 
 // How windowed attention runs.
 struct WindowPlan {
+  bool tc, wide;
   int parts, part, tile_queries;
 };
 
@@ -811,7 +828,9 @@ WindowPlan window_plan(const pkv_cache* c, int num_seqs, int num_heads, int max_
                        int sinks, int max_len) {
   WindowPlan w{};
   const int G = num_heads / c->num_kv_heads;
-  w.tile_queries = std::max(1, pkv::kCrossRows / G);
+  w.tc = tensor_cores(c);
+  w.wide = w.tc && wide_rows(c, (int64_t)max_queries * G);
+  w.tile_queries = (!w.tc ? pkv::kCrossRows : w.wide ? 256 : 128) / G;
   // The most positions that a row tile walks, in tiles of 64.
   const int64_t whole = ((int64_t)max_len + 63) / 64;
   const int64_t most = (std::min<int64_t>(sinks, max_len) + 63) / 64 +
@@ -858,7 +877,15 @@ int paged_attention_window(const pkv_cache* cache, const void* q, int64_t total_
   p.tile_queries = w.tile_queries;
   const int wrc = cross_workspace_params(&p, cache, w.parts, w.part, workspace, workspace_bytes);
   if (wrc) return wrc;
-  return pkv_launch_window(p, cache->dtype, cache->io_dtype, num_seqs, cache->head_dim, stream);
+  if (!w.tc)
+    return pkv_launch_window(p, cache->dtype, cache->io_dtype, num_seqs, cache->head_dim, stream);
+  pkv::CrossMaps maps;
+  const int mrc = page_maps(&maps, cache);
+  if (mrc) return mrc;
+  if (cache->dtype == PKV_FP8_E4M3)
+    return pkv_launch_window_tc_fp8(p, cache->io_dtype, num_seqs, w.wide, maps, stream);
+  return (cache->dtype == PKV_F16 ? pkv_launch_window_tc_f16 : pkv_launch_window_tc_bf16)(
+      p, num_seqs, cache->head_dim, maps, stream);
 }
 
 int paged_block_copy(const pkv_cache* cache, const int64_t* src_dst_pairs, int64_t num_pairs,

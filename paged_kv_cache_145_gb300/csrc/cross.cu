@@ -15,11 +15,8 @@ int launch(const P& p, int num_seqs, cudaStream_t stream) {
   return pkv::launch_cross_merge<T, D>(p, num_seqs, stream);
 }
 
-}  // namespace
-
-// fp32 pools (head_dim 64 or 128) and FP8 pools of head_dim 64.
-int pkv_launch_cross(const pkv::CrossParams& p, int dtype, int io_dtype, int num_seqs, int dim,
-                     cudaStream_t stream) {
+template <typename P>
+int launch_pool(const P& p, int dtype, int io_dtype, int num_seqs, int dim, cudaStream_t stream) {
   switch (dtype) {
     case PKV_F32:
       return dim == 64 ? launch<float, float, 64>(p, num_seqs, stream)
@@ -31,26 +28,16 @@ int pkv_launch_cross(const pkv::CrossParams& p, int dtype, int io_dtype, int num
   return PKV_ERR_ARG;
 }
 
-// With a window, any pool.
+}  // namespace
+
+// fp32 pools (head_dim 64 or 128) and FP8 pools of head_dim 64.
+int pkv_launch_cross(const pkv::CrossParams& p, int dtype, int io_dtype, int num_seqs, int dim,
+                     cudaStream_t stream) {
+  return launch_pool(p, dtype, io_dtype, num_seqs, dim, stream);
+}
+
+// With a window: the same pools.
 int pkv_launch_window(const pkv::WindowParams& p, int dtype, int io_dtype, int num_seqs, int dim,
                       cudaStream_t stream) {
-  const bool d64 = dim == 64;
-  switch (dtype) {
-    case PKV_F32:
-      return d64 ? launch<float, float, 64>(p, num_seqs, stream)
-                 : launch<float, float, 128>(p, num_seqs, stream);
-    case PKV_F16:
-      return d64 ? launch<__half, __half, 64>(p, num_seqs, stream)
-                 : launch<__half, __half, 128>(p, num_seqs, stream);
-    case PKV_BF16:
-      return d64 ? launch<__nv_bfloat16, __nv_bfloat16, 64>(p, num_seqs, stream)
-                 : launch<__nv_bfloat16, __nv_bfloat16, 128>(p, num_seqs, stream);
-    case PKV_FP8_E4M3:
-      if (io_dtype == PKV_F16)
-        return d64 ? launch<__half, __nv_fp8_e4m3, 64>(p, num_seqs, stream)
-                   : launch<__half, __nv_fp8_e4m3, 128>(p, num_seqs, stream);
-      return d64 ? launch<__nv_bfloat16, __nv_fp8_e4m3, 64>(p, num_seqs, stream)
-                 : launch<__nv_bfloat16, __nv_fp8_e4m3, 128>(p, num_seqs, stream);
-  }
-  return PKV_ERR_ARG;
+  return launch_pool(p, dtype, io_dtype, num_seqs, dim, stream);
 }

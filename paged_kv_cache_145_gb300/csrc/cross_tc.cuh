@@ -1,10 +1,18 @@
-// Cross attention on the fifth-generation tensor cores: fp16 and bf16 pools,
-// and FP8 pools of head_dim 128 (widened to fp16 in shared memory, exactly).
+// Cross attention, and causal attention with a sliding window, on the
+// fifth-generation tensor cores: fp16 and bf16 pools, and FP8 pools of head_dim
+// 128 (widened to fp16 in shared memory, exactly).
 //
 // One thread block holds QT tiles of 128 rows (queries of the grouped heads
 // of one KV head, stacked) and walks one part of the sequence's states in
-// tiles of 64 keys.  No mask falls between queries and states, so only the
-// last tile has keys to hide, and they are the same ones for every row.
+// tiles of 64 keys.  Without a window no mask falls between queries and states,
+// so only the last tile has keys to hide, and they are the same ones for every
+// row.  With one (P is WindowParams) the block walks the tiles of its rows'
+// WindowSpan; the tiles at its edges, where some row does not see some
+// position, are masked row by row (about 3 of 19 with a window of 1024).  There
+// a value that is not finite must reach the rows that see it and no other,
+// which a product with weights of zero does not do: edge tiles are multiplied
+// with such values cleared, and where there were any, every row that sees them
+// adds them to its O afterwards, read again from the pool.
 // Roles:
 //   softmax warps, four per row tile  a thread per row (= tensor-memory lane):
 //        the S row to registers, running maximum and sum, P over S's columns;
@@ -88,10 +96,11 @@ struct CrossTcCfg {
   static constexpr int kVRingOff = kKRingOff + kKSlots * kTileBytes;
   static constexpr int kRawOff = kVRingOff + kVSlots * kTileBytes;  // K, then V
   static constexpr int kBarOff = kRawOff + 2 * kRawSlots * kRawBytes;
-  static constexpr int kNumBars = 2 * kSlots + 4 * kRawSlots + QT * (2 * kBufs + 3) + 2;
+  static constexpr int kNumBars = 2 * kSlots + 4 * kRawSlots + QT * (2 * kBufs + 3) + 3;
   static constexpr int kTmemOff = kBarOff + kNumBars * 8;
   static constexpr int kFlagOff = kTmemOff + 4;
-  static constexpr int kSmemBytes = kTmemOff + 16;
+  static constexpr int kDirtyOff = kTmemOff + 8;            // with a window; FP8: 2 a V slot
+  static constexpr int kSmemBytes = kDirtyOff + (KV8 ? 8 * kVSlots : 8);
   static constexpr uint32_t kTileCols = 256;
   static constexpr uint32_t kTmemCols = QT * kTileCols;
   static constexpr uint32_t kOCol = kBufs * kKeys;
@@ -103,7 +112,7 @@ struct CrossTcCfg {
   // P stays at or below 2^(kSlack + kBias): 2^15 in fp16.
   static constexpr float kSlack = 8.f, kBias = kBf16 ? 0.f : 7.f;
   static_assert(kOCol + D <= kTileCols, "tensor memory");
-  static_assert(kKSlots >= 1 && kVSlots >= 1, "rings");
+  static_assert(kKSlots >= 1 && kVSlots >= 2, "rings");
   static_assert(kSmemBytes <= (QT == 2 ? 227 : 113) * 1024, "shared memory");
   // never more blocks on an SM than its 512 tensor-memory columns serve
   static_assert(QT == 1 || 2 * kSmemBytes > 228 * 1024, "blocks per SM");
@@ -123,6 +132,19 @@ __device__ __forceinline__ bool table_row_bad(const CrossParams& p, const int32_
     for (int k = 0; k < 8; ++k) bad |= e[k] < 0 || (int64_t)e[k] >= p.num_blocks;
   }
   return bad;
+}
+
+// Keys k of a tile from position t0 on that the query at position pos sees.
+__device__ __forceinline__ uint64_t window_mask(const WindowParams& p, int pos, int t0) {
+  auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; };
+  return below(pos + 1 - t0) & (~below(max(pos - p.window, -1) + 1 - t0) | below(p.sinks - t0));
+}
+
+// One of the pair's 16-bit elements is not finite.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  constexpr uint32_t kExp = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
+  return ((w & kExp) == kExp ? 0xFFFFu : 0u) | ((w & kExp << 16) == kExp << 16 ? 0xFFFF0000u : 0u);
 }
 
 // Two 16-bit elements times zero: zeros, NaN for what is not finite.
@@ -202,11 +224,20 @@ __device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const 
   return qscale;
 }
 
+// The word with the codes that are NaN (0x7F, 0xFF) cleared.
+__device__ __forceinline__ uint32_t clear_nan_codes(uint32_t w) {
+  const uint32_t nan = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  return w & ~nan;
+}
+
 // A tile of KEYS rows of 128 codes to fp16, both in the 128-byte-swizzled
-// layout, by THREADS threads; rows from `valid` on become zeros.
-template <int KEYS, int THREADS>
-__device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned char* dst, int valid,
-                                           int thread) {
+// layout, by THREADS threads; rows from `valid` on become zeros.  EDGE: rows
+// outside the mask too, and NaN codes; returns whether this thread met one in
+// the mask.
+template <int KEYS, int THREADS, bool EDGE = false>
+__device__ __forceinline__ bool widen_tile(const unsigned char* raw, unsigned char* dst, int valid,
+                                           int thread, uint64_t mask = 0) {
+  bool met = false;
   // Eight loads in flight: 150 us for 8 x 300-512 queries over 1000-4000 states,
   // where one took 164 and four 154.
   constexpr int kUnits = KEYS * 8 / THREADS, kBatch = 8;
@@ -218,8 +249,14 @@ __device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned ch
     for (int i = 0; i < kBatch; ++i) {
       const int unit = thread + (u0 + i) * THREADS, row = unit >> 3, ch = unit & 7;
       x[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (row < valid)
+      if (EDGE ? (mask >> row & 1ull) != 0 : row < valid)
         x[i] = *reinterpret_cast<const uint4*>(raw + row * 128 + ((ch ^ (row & 7)) << 4));
+      if constexpr (EDGE) {
+        const uint4 y = make_uint4(clear_nan_codes(x[i].x), clear_nan_codes(x[i].y),
+                                   clear_nan_codes(x[i].z), clear_nan_codes(x[i].w));
+        met |= y.x != x[i].x || y.y != x[i].y || y.z != x[i].z || y.w != x[i].w;
+        x[i] = y;
+      }
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -235,6 +272,7 @@ __device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned ch
       *reinterpret_cast<uint4*>(drow + (((c2 + 1) ^ (row & 7)) << 4)) = z;
     }
   }
+  return met;
 }
 
 struct CrossMaps {
@@ -279,6 +317,32 @@ __device__ __forceinline__ void clear_tail(unsigned char* v, int valid, int bloc
   fence_proxy_async_smem();
 }
 
+// A value tile at an edge of the window: rows outside `mask` (nobody's) become
+// zeros, elements that are not finite too; returns whether this thread met one
+// in the mask.
+template <typename T, int D, int KEYS>
+__device__ __forceinline__ bool clear_edge(unsigned char* v, uint64_t mask, int thread, int threads) {
+  bool met = false;
+  for (int e = thread; e < KEYS * (D / 8); e += threads) {
+    const int row = e / (D / 8), ch = e % (D / 8);
+    uint4* const at = reinterpret_cast<uint4*>(v + (row >> 3) * (D / 64 * 1024) + (ch >> 3) * 1024 +
+                                               (row & 7) * 128 + ((ch & 7) ^ (row & 7)) * 16);
+    if (!(mask >> row & 1ull)) {
+      *at = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
+    const uint4 x = *at;
+    const uint4 n = make_uint4(not_finite<T>(x.x), not_finite<T>(x.y), not_finite<T>(x.z),
+                               not_finite<T>(x.w));
+    if (n.x | n.y | n.z | n.w) {
+      met = true;
+      *at = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
+    }
+  }
+  fence_proxy_async_smem();
+  return met;
+}
+
 // One page (or the part of it in a tile) of a pool, see kGroupBytes: coordinates
 // are the first group of 8 rows and the page, block * kv_heads + kv_head.
 __device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, int group,
@@ -310,6 +374,18 @@ struct PageTile {
       if (at < end) entry[x] = trow[at >> shift];
     }
   }
+  // The same for a tile of a window's span: pages that no row sees have none.
+  __device__ __forceinline__ void look(const int32_t* trow, int pos, const WindowSpan<KEYS>& span,
+                                       bool any, int shift) {
+    const int step = min(1 << shift, KEYS);
+#pragma unroll
+    for (int x = 0; x < kMax; ++x) {
+      if (x * step >= KEYS) break;
+      const int at = pos + x * step;
+      entry[x] = -1;
+      if (any && span.sees_page(at, step)) entry[x] = trow[at >> shift];
+    }
+  }
   // An entry out of range becomes a page past the pool, which reads as zeros.
   __device__ __forceinline__ void copy(const CrossParams& p, uint32_t dst, const CUtensorMap* map,
                                        int pos, int kvh, int shift, int group_bytes, uint32_t bar,
@@ -326,10 +402,11 @@ struct PageTile {
   }
 };
 
-template <typename T, int D, int QT, bool KV8>
+template <typename T, int D, int QT, bool KV8, typename P>
 __global__ void __launch_bounds__(CrossTcCfg<T, D, QT, KV8>::kThreads, QT == 2 ? 1 : 2)
-cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ CUtensorMap tmk,
+cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tmk,
                 const __grid_constant__ CUtensorMap tmv) {
+  constexpr bool WIN = std::is_same<P, WindowParams>::value;
   using Cfg = CrossTcCfg<T, D, QT, KV8>;
   using Op = typename Cfg::Op;
   constexpr int KT = Cfg::kKeys, NS = Cfg::kBufs;
@@ -372,8 +449,46 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
     return;
   }
   const int32_t* trow = p.tables + (int64_t)s * p.max_blocks;
+  // Keys lo .. hi - 1; with a window, the span's tiles from tile0 on.
   const int lo = part * p.part, hi = min(c.L, lo + p.part);
-  const int n_tiles = (hi - lo + KT - 1) / KT;
+  [[maybe_unused]] const int tile0 = lo / KT;
+  [[maybe_unused]] const int base_pos = c.L - c.Q;  // the first query's position
+  const auto span = [&] {
+    if constexpr (WIN) return WindowSpan<KT>(p, base_pos + r0 / G, base_pos + (r0 + nr - 1) / G);
+    else return 0;
+  }();
+  const int n_tiles = [&] {
+    if constexpr (WIN) return min(span.tiles - tile0, p.part / KT);
+    else return (hi - lo + KT - 1) / KT;
+  }();
+  if (WIN && n_tiles <= 0) {  // a row tile with fewer parts than the sequence
+    for (int e = tid; e < nr; e += Cfg::kThreads)
+      p.ws_ml[row_at(e) / D * p.parts + part] = make_float2(-INFINITY, 0.f);
+    for (int e = tid; e < nr * D; e += Cfg::kThreads)
+      p.ws_o[(row_at(e / D) / D * p.parts + part) * D + e % D] = 0.f;
+    return;
+  }
+  // First position of the j-th tile.
+  auto tile_pos = [&](int j) {
+    if constexpr (WIN) return span.pos(tile0 + j);
+    else return lo + j * KT;
+  };
+  // Whether some row does not see some position of the tile at t0.
+  [[maybe_unused]] auto at_edge = [&](int t0) {
+    if constexpr (WIN)
+      return t0 + KT - 1 > base_pos + r0 / G ||
+             (t0 + KT - 1 >= p.sinks && t0 <= span.last - p.window);
+    else return false;
+  };
+  // Positions of the tile at t0 that some row sees.
+  [[maybe_unused]] auto seen_mask = [&](int t0) {
+    uint64_t m = 0;
+    if constexpr (WIN) {
+      auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; };
+      m = below(span.last + 1 - t0) & (~below(span.w0 - t0) | below(span.s0 - t0));
+    }
+    return m;
+  };
   const int row_n = nr > 128 ? 2 : 1;  // row tiles with rows
 
   // ---- barriers, tensor memory, Q ---------------------------------------------
@@ -397,9 +512,14 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
   const uint32_t q_full = bar0 + 8u * (B1 + 2 * QT * NS + 2 * QT);
   auto drain = [&](int t) { return q_full + 8u * (1 + t); };
   const uint32_t checked = q_full + 8u * (1 + QT);  // the table row
+  const uint32_t cleared = checked + 8u;  // an edge tile's values
   auto tile_warps = [&](int t) {  // softmax warps with rows of row tile t
     return min(4, max(0, (nr - t * 128 + 31) / 32));
   };
+  // Values of an edge tile were cleared.  FP8: a word of each converter warp for
+  // each slot, true or false; else two words for edge tiles in turn, the number
+  // of the last tile that had some.
+  [[maybe_unused]] volatile int* dirty = reinterpret_cast<volatile int*>(smem + Cfg::kDirtyOff);
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) {
       mbar_init(k_full(i), KV8 ? Cfg::kConvThreads : 1);
@@ -426,8 +546,10 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
     }
     mbar_init(q_full, (tile_warps(0) + (QT > 1 ? tile_warps(QT - 1) : 0)) * 32);
     mbar_init(checked, 32);
+    mbar_init(cleared, max(1, tile_warps(0)) * 32);
     fence_mbar_init();
     *reinterpret_cast<int*>(smem + Cfg::kFlagOff) = 0;
+    if constexpr (!KV8) dirty[0] = dirty[1] = -1;
   }
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + Cfg::kTmemOff);
   volatile int* bad_flag = reinterpret_cast<volatile int*>(smem + Cfg::kFlagOff);
@@ -470,8 +592,12 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       const uint32_t bars = KV8 ? raw_full(key ? 0 : 1, 0) : key ? k_full(0) : v_full(0);
       const uint32_t frees = KV8 ? raw_empty(key ? 0 : 1, 0) : key ? k_empty(0) : v_empty(0);
       PageTile<KT> now, next;
-      now.look(trow, lo, hi, shift);
-      next.look(trow, lo + KT, hi, shift);
+      auto look = [&](PageTile<KT>& pages, int j) {
+        if constexpr (WIN) pages.look(trow, span.pos(tile0 + j), span, j < n_tiles, shift);
+        else pages.look(trow, lo + j * KT, hi, shift);
+      };
+      look(now, 0);
+      look(next, 1);
       int slot = 0, issued = 0;
       uint32_t phase = 0;
       for (; issued < n_tiles; ++issued) {
@@ -481,9 +607,9 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
         }
         const uint32_t fb = bars + 8u * slot;
         mbar_arrive_expect_tx(fb, BYTES);
-        now.copy(p, ring + slot * BYTES, map, lo + issued * KT, kvh, shift, GROUP, fb, policy);
+        now.copy(p, ring + slot * BYTES, map, tile_pos(issued), kvh, shift, GROUP, fb, policy);
         now = next;
-        next.look(trow, lo + (issued + 2) * KT, hi, shift);
+        look(next, issued + 2);
         if (++slot == slots) {
           slot = 0;
           phase ^= 1u;
@@ -500,7 +626,10 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       // All copies are under way: the whole table row is checked by every
       // block, so that all parts agree.  (A bad entry's page was read as
       // zeros, and the rows are zeroed at the end.)
-      if (table_row_bad(p, trow, (c.L - 1) / b + 1, lane)) *bad_flag = 1;
+      bool bad;
+      if constexpr (WIN) bad = window_row_bad(p, c, trow, lane, 32);
+      else bad = table_row_bad(p, trow, (c.L - 1) / b + 1, lane);
+      if (bad) *bad_flag = 1;
       mbar_arrive(checked);
     }
   } else if (warp >= Cfg::kMmaWarp && warp < Cfg::kConvWarp) {
@@ -578,9 +707,21 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
           failed = true;
           break;
         }
-        widen_tile<KT, Cfg::kConvThreads>(
-            smem + Cfg::kRawOff + (which * RAW + from.slot) * Cfg::kRawBytes,
-            ring + slot * Cfg::kTileBytes, which ? hi - lo - j * KT : KT, ct);
+        const unsigned char* raw = smem + Cfg::kRawOff + (which * RAW + from.slot) * Cfg::kRawBytes;
+        unsigned char* const wide = ring + slot * Cfg::kTileBytes;
+        if constexpr (WIN) {
+          const int t0 = tile_pos(j);
+          if (which && at_edge(t0)) {
+            const bool met = widen_tile<KT, Cfg::kConvThreads, true>(raw, wide, KT, ct, seen_mask(t0));
+            const bool any = __any_sync(kFullMask, met);
+            if (lane == 0) dirty[2 * slot + (ct >> 5)] = any;
+            __syncwarp();
+          } else {
+            widen_tile<KT, Cfg::kConvThreads>(raw, wide, KT, ct);
+          }
+        } else {
+          widen_tile<KT, Cfg::kConvThreads>(raw, wide, which ? hi - lo - j * KT : KT, ct);
+        }
         fence_proxy_async_smem();
         mbar_arrive(fulls + 8u * slot);
         mbar_arrive(raw_empty(which, from.slot));
@@ -596,6 +737,49 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
     const uint32_t base = tmem + t * Cfg::kTileCols + ((uint32_t)((warp & 3) * 32) << 16);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
+    // With a window: the row's position, the last edge tile with values that are
+    // not finite (-1: none waits) and the keys whose weight is 0 in it, and the
+    // number of edge tiles.
+    [[maybe_unused]] const int pos = base_pos + (r0 + min(r, nr - 1)) / G;
+    [[maybe_unused]] int odd = -1, edges = 0;
+    [[maybe_unused]] uint64_t odd_zero = 0;
+    // Adds that tile's cleared values to O, once its product is in.
+    [[maybe_unused]] auto add_odd = [&] {
+      const int t0 = tile_pos(odd), bs = b;
+      uint64_t seen = 0, sees_keys = 0;
+      if constexpr (WIN) {
+        seen = seen_mask(t0);
+        sees_keys = window_mask(p, pos, t0);
+      }
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        tmem_ld32(base + Cfg::kOCol + q * 32, o);
+#pragma unroll 1
+        for (int k = 0; k < KT; ++k) {
+          if (!(seen >> k & 1ull)) continue;
+          const int e = trow[(t0 + k) / bs];
+          if ((unsigned)e >= (unsigned)p.num_blocks) continue;
+          const int64_t at =
+              ((((int64_t)e * p.kv_heads + kvh) * bs + (t0 + k) % bs) * D + q * 32);
+          const bool sees = sees_keys >> k & 1ull, zero = odd_zero >> k & 1ull;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float x;
+            if constexpr (KV8) {
+              const unsigned char code = static_cast<const unsigned char*>(p.v_cache)[at + i];
+              x = (code & 0x7F) == 0x7F ? NAN : 0.f;
+            } else {
+              x = static_cast<float>(static_cast<const T*>(p.v_cache)[at + i]);
+            }
+            if (sees && !isfinite(x))
+              o[i] = __float_as_uint(__uint_as_float(o[i]) + (zero ? NAN : x));
+          }
+        }
+        tmem_st32(base + Cfg::kOCol + q * 32, o);
+      }
+      odd = -1;
+    };
     for (int j = 0; j < n_tiles; ++j) {
       ok = mbar_wait(s_full(t, j % NS), (uint32_t)((j / NS) & 1));
       if (__any_sync(kFullMask, !ok)) {
@@ -606,11 +790,24 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       const uint32_t sp = base + (j % NS) * KT;
       uint32_t w[KT];
       tmem_ld64(sp, w);
-      const int valid = hi - lo - j * KT;
-      if (valid < KT) {
+      [[maybe_unused]] bool edge = false;
+      if constexpr (WIN) {
+        const int t0 = tile_pos(j);
+        edge = at_edge(t0);
+        if (edge) {
+          const uint64_t sees = window_mask(p, pos, t0);
+          const uint32_t s0 = (uint32_t)sees, s1 = (uint32_t)(sees >> 32);
 #pragma unroll
-        for (int k = 0; k < KT; ++k)
-          if (k >= valid) w[k] = __float_as_uint(-INFINITY);
+          for (int k = 0; k < KT; ++k)
+            if (!((k < 32 ? s0 : s1) >> (k & 31) & 1u)) w[k] = __float_as_uint(-INFINITY);
+        }
+      } else {
+        const int valid = hi - lo - j * KT;
+        if (valid < KT) {
+#pragma unroll
+          for (int k = 0; k < KT; ++k)
+            if (k >= valid) w[k] = __float_as_uint(-INFINITY);
+        }
       }
       float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -652,7 +849,39 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
       const float2 sx = __fadd2_rn(s01, s23);
       l += sx.x + sx.y;
       tmem_st32(sp, pk);
-      if (!KV8 && hi - lo - j * KT < KT) {  // (the last tile)
+      [[maybe_unused]] bool met = false;
+      [[maybe_unused]] uint64_t weightless = 0;
+      if constexpr (WIN) {
+        if (edge) {
+          ok = mbar_wait(v_full(j % NV), (uint32_t)((j / NV) & 1));
+          if (__any_sync(kFullMask, !ok)) {
+            ok = false;
+            break;
+          }
+          if constexpr (KV8) {
+            met = dirty[2 * (j % NV)] != 0 || dirty[2 * (j % NV) + 1] != 0;
+          } else {
+            met = clear_edge<T, D, KT>(smem + Cfg::kVRingOff + (j % NV) * Cfg::kTileBytes,
+                                       seen_mask(tile_pos(j)), rr, 32 * tile_warps(t));
+            if (met) dirty[edges & 1] = j;
+            mbar_arrive(cleared);
+            ok = mbar_wait(cleared, (uint32_t)(edges & 1));
+            if (__any_sync(kFullMask, !ok)) {
+              ok = false;
+              break;
+            }
+            met = dirty[edges & 1] == j;
+            ++edges;
+          }
+          if (met) {
+#pragma unroll
+            for (int k = 0; k < KT; k += 2) {
+              if (!(pk[k / 2] & 0x7FFFu)) weightless |= 1ull << k;
+              if (!(pk[k / 2] & 0x7FFF0000u)) weightless |= 2ull << k;
+            }
+          }
+        }
+      } else if (!KV8 && hi - lo - j * KT < KT) {  // (the last tile)
         ok = mbar_wait(v_full(j % NV), (uint32_t)((j / NV) & 1));
         if (__any_sync(kFullMask, !ok)) {
           ok = false;
@@ -681,6 +910,13 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
           tmem_st32(base + Cfg::kOCol + q * 32, o);
         }
       }
+      if constexpr (WIN) {
+        if (odd >= 0) add_odd();
+        if (met) {
+          odd = j;
+          odd_zero = weightless;
+        }
+      }
       tc_fence_before();
       mbar_arrive(p_full(t, j % NS));
     }
@@ -699,6 +935,9 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
     const bool whole = c.parts == 1;
     if (ok) {
       tc_fence_after();
+      if constexpr (WIN) {
+        if (odd >= 0) add_odd();
+      }
       // l = 0: every score was -inf.  A row of such scores is 0 / 0 (NaN); a
       // part of them leaves O as it is, NaN where a value was not finite, and
       // weighs nothing in the merge.
@@ -738,10 +977,10 @@ cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ C
   if (warp == Cfg::kMmaWarp) tmem_dealloc(tmem, Cfg::kTmemCols);
 }
 
-template <typename T, int D, int QT, bool KV8>
-int launch_cross_tc(const CrossParams& p, int num_seqs, const CrossMaps& maps, cudaStream_t stream) {
+template <typename T, int D, int QT, bool KV8, typename P>
+int launch_cross_tc(const P& p, int num_seqs, const CrossMaps& maps, cudaStream_t stream) {
   using Cfg = CrossTcCfg<T, D, QT, KV8>;
-  auto kern = cross_tc_kernel<T, D, QT, KV8>;
+  auto kern = cross_tc_kernel<T, D, QT, KV8, P>;
   static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use its shared memory
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return pkv_cuda_failed();
