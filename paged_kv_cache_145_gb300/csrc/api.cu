@@ -24,6 +24,8 @@ int pkv_launch_window_tc_f16(const pkv::WindowParams&, int, int, const pkv::Cros
 int pkv_launch_window_tc_bf16(const pkv::WindowParams&, int, int, const pkv::CrossMaps&, cudaStream_t);
 int pkv_launch_window_tc_fp8(const pkv::WindowParams&, int, int, bool, const pkv::CrossMaps&,
                              cudaStream_t);
+int pkv_launch_window_token(const pkv::WindowParams& p, int dtype, int io_dtype, int num_seqs, int dim,
+                            const pkv::CrossMaps& maps, cudaStream_t stream);
 int pkv_launch_window(const pkv::WindowParams& p, int dtype, int io_dtype, int num_seqs, int dim,
                       cudaStream_t stream);
 size_t pkv_fork_workspace(int rows, int next);
@@ -232,7 +234,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 // Describes a [N][Hk][b][D] pool as a 4-D tensor (D fastest) read in boxes of
 // min(b, 16) rows x 128 bytes (64 16-bit elements, or 128 FP8 codes) with the
-// 128-byte shared-memory swizzle.
+// 128-byte shared-memory swizzle; rows of 64 FP8 codes whole, with the 64-byte
+// swizzle.
 bool encode_pool_map(CUtensorMap* map, const pkv_cache* c, void* base) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
@@ -241,7 +244,8 @@ bool encode_pool_map(CUtensorMap* map, const pkv_cache* c, void* base) {
                               (cuuint64_t)c->num_kv_heads, (cuuint64_t)c->num_blocks};
   const cuuint64_t strides[3] = {c->head_dim * elt, c->block_size * c->head_dim * elt,
                                  (cuuint64_t)c->num_kv_heads * c->block_size * c->head_dim * elt};
-  const cuuint32_t box[4] = {(cuuint32_t)(128 / elt),
+  const bool narrow = c->head_dim * elt < 128;
+  const cuuint32_t box[4] = {(cuuint32_t)(narrow ? c->head_dim : 128 / elt),
                              (cuuint32_t)(c->block_size < 16 ? c->block_size : 16), 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUtensorMapDataType ty =
@@ -249,7 +253,7 @@ bool encode_pool_map(CUtensorMap* map, const pkv_cache* c, void* base) {
       : c->dtype == PKV_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   return enc(map, ty, 4, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -613,6 +617,23 @@ struct CrossPlan {
   int parts, part;
 };
 
+// Streaming multiprocessors of the current device; 1 without one.
+int sm_count() {
+  static std::atomic<int> known[kMaxDevices];  // looked up once per device
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) {
+    sms = known[dev].load();
+    if (sms == 0 &&
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && sms > 0)
+      known[dev].store(sms);
+  }
+  if (sms < 1) {
+    cudaGetLastError();
+    sms = 1;
+  }
+  return sms;
+}
+
 bool tensor_cores(const pkv_cache* c) {
   return c->dtype == PKV_F16 || c->dtype == PKV_BF16 ||
          (c->dtype == PKV_FP8_E4M3 && c->head_dim == 128);
@@ -626,18 +647,7 @@ CrossPlan cross_plan(const pkv_cache* c, int num_seqs, int num_heads, int max_qu
   pl.tc = tensor_cores(c);
   const int64_t rows = (int64_t)max_queries * (num_heads / c->num_kv_heads);
   pl.wide = wide_rows(c, rows);
-  static std::atomic<int> sm_count[kMaxDevices];  // looked up once per device
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) {
-    sms = sm_count[dev].load();
-    if (sms == 0 &&
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && sms > 0)
-      sm_count[dev].store(sms);
-  }
-  if (sms < 1) {  // without a device nothing is split
-    cudaGetLastError();
-    sms = 1;
-  }
+  const int sms = sm_count();
   const int64_t per = !pl.tc ? pkv::kCrossRows : pl.wide ? 256 : 128;
   const int64_t places = (int64_t)sms * (!pl.tc ? 8 : pl.wide ? 1 : 2);
   const int64_t blocks =
@@ -818,16 +828,43 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
 
 namespace {
 
-// How windowed attention runs.
+// How windowed attention runs: single tokens over 16-bit and FP8 pools in blocks
+// of one KV head each, the window split where they would not fill the GPU;
+// chunks as cross attention.
 struct WindowPlan {
-  bool tc, wide;
+  bool token, tc, wide;
   int parts, part, tile_queries;
 };
+
+constexpr int64_t kTokenPart = 8192;  // most positions of a part
+
+// Parts of a token's window of `chunks` runs of 16 positions.
+int64_t token_parts(const pkv_cache* c, int num_seqs, int64_t chunks) {
+  constexpr int64_t kMost = kTokenPart / 16;
+  const int64_t blocks = std::max<int64_t>(1, (int64_t)num_seqs * c->num_kv_heads);
+  const int64_t places = (int64_t)sm_count() * 6;
+  const int64_t fill = std::min((places + blocks - 1) / blocks, (chunks + 15) / 16);
+  return std::max<int64_t>(std::max<int64_t>(1, fill), (chunks + kMost - 1) / kMost);
+}
 
 WindowPlan window_plan(const pkv_cache* c, int num_seqs, int num_heads, int max_queries, int window,
                        int sinks, int max_len) {
   WindowPlan w{};
   const int G = num_heads / c->num_kv_heads;
+  // The most positions that a token's span holds, in chunks of 16 (parts index a
+  // grid's z dimension).
+  const int64_t chunks = std::max<int64_t>(
+      1, std::min(((int64_t)max_len + 15) / 16, (std::min<int64_t>(sinks, max_len) + 15) / 16 +
+                                                    ((int64_t)window + 14) / 16 + 1));
+  if (max_queries == 1 && c->dtype != PKV_F32 && chunks <= 65535 * (kTokenPart / 16)) {
+    w.token = true;
+    w.tile_queries = 1;
+    const int64_t want = token_parts(c, num_seqs, chunks);
+    const int64_t per = (chunks + want - 1) / want;
+    w.part = (int)per * 16;
+    w.parts = (int)((chunks + per - 1) / per);
+    return w;
+  }
   w.tc = tensor_cores(c);
   w.wide = w.tc && wide_rows(c, (int64_t)max_queries * G);
   w.tile_queries = (!w.tc ? pkv::kCrossRows : w.wide ? 256 : 128) / G;
@@ -875,8 +912,17 @@ int paged_attention_window(const pkv_cache* cache, const void* q, int64_t total_
   p.window = window;
   p.sinks = sinks;
   p.tile_queries = w.tile_queries;
+  p.token = w.token;
   const int wrc = cross_workspace_params(&p, cache, w.parts, w.part, workspace, workspace_bytes);
   if (wrc) return wrc;
+  if (w.token) {
+    pkv::CrossMaps maps;
+    if (!encode_pool_map(&maps.k, cache, cache->k_cache) ||
+        !encode_pool_map(&maps.v, cache, cache->v_cache))
+      return PKV_ERR_CUDA;
+    return pkv_launch_window_token(p, cache->dtype, cache->io_dtype, num_seqs, cache->head_dim, maps,
+                                   stream);
+  }
   if (!w.tc)
     return pkv_launch_window(p, cache->dtype, cache->io_dtype, num_seqs, cache->head_dim, stream);
   pkv::CrossMaps maps;

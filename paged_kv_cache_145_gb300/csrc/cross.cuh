@@ -53,6 +53,7 @@ struct CrossParams {
 struct WindowParams : CrossParams {
   int window, sinks;
   int tile_queries;         // queries in a row tile
+  bool token;               // single tokens: parts are of chunks of 16 positions
 };
 
 // Whether the query at position p sees position t.
@@ -109,8 +110,8 @@ __device__ __forceinline__ CrossSeq cross_seq(const CrossParams& p, int s) {
   return c;
 }
 
-// L is the sequence's length with its queries; parts are of the tiles of 64
-// that a row tile walks (where it walks fewer than the sequence's other row
+// L is the sequence's length with its queries; parts are of the tiles of 64 (or
+// 16) that a row tile walks (where it walks fewer than the sequence's other row
 // tiles its last parts are empty).
 __device__ __forceinline__ CrossSeq cross_seq(const WindowParams& p, int s) {
   CrossSeq c = cross_seq(static_cast<const CrossParams&>(p), s);
@@ -118,6 +119,10 @@ __device__ __forceinline__ CrossSeq cross_seq(const WindowParams& p, int s) {
   c.parts = 1;
   if (c.bits || c.Q == 0) {
     c.L = 0;
+    return c;
+  }
+  if (p.token) {
+    c.parts = (WindowSpan<16>(p, c.L - 1, c.L - 1).tiles + p.part / 16 - 1) / (p.part / 16);
     return c;
   }
   int tiles = WindowSpan<64>(p, c.L - c.Q, c.L - 1).tiles;
