@@ -836,27 +836,25 @@ struct WindowPlan {
   int parts, part, tile_queries;
 };
 
-constexpr int64_t kTokenPart = 8192;  // most positions of a part
-
-// Parts of a token's window of `chunks` runs of 16 positions.
+// Parts of a token's window of `chunks` runs of 16 positions: two blocks to an SM
+// where there would be fewer, of 6 chunks at least (four sequences of 8 KV heads
+// over 8192 positions: 8 to 10 parts 27.3 us, 19 parts 28.4, 24 parts 34; 64
+// sequences over 1024: one part 43.8 us, two 49, four 53.8; one sequence: four
+// parts 9.8, eight 8.2, sixteen 8.3).
 int64_t token_parts(const pkv_cache* c, int num_seqs, int64_t chunks) {
-  constexpr int64_t kMost = kTokenPart / 16;
   const int64_t blocks = std::max<int64_t>(1, (int64_t)num_seqs * c->num_kv_heads);
-  const int64_t places = (int64_t)sm_count() * 6;
-  const int64_t fill = std::min((places + blocks - 1) / blocks, (chunks + 15) / 16);
-  return std::max<int64_t>(std::max<int64_t>(1, fill), (chunks + kMost - 1) / kMost);
+  return std::max<int64_t>(1, std::min((int64_t)sm_count() * 2 / blocks, chunks / 6));
 }
 
 WindowPlan window_plan(const pkv_cache* c, int num_seqs, int num_heads, int max_queries, int window,
                        int sinks, int max_len) {
   WindowPlan w{};
   const int G = num_heads / c->num_kv_heads;
-  // The most positions that a token's span holds, in chunks of 16 (parts index a
-  // grid's z dimension).
+  // The most positions that a token's span holds, in chunks of 16.
   const int64_t chunks = std::max<int64_t>(
       1, std::min(((int64_t)max_len + 15) / 16, (std::min<int64_t>(sinks, max_len) + 15) / 16 +
                                                     ((int64_t)window + 14) / 16 + 1));
-  if (max_queries == 1 && c->dtype != PKV_F32 && chunks <= 65535 * (kTokenPart / 16)) {
+  if (max_queries == 1 && c->dtype != PKV_F32) {
     w.token = true;
     w.tile_queries = 1;
     const int64_t want = token_parts(c, num_seqs, chunks);

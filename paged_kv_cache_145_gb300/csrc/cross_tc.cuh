@@ -100,7 +100,8 @@ struct CrossTcCfg {
   static constexpr int kTmemOff = kBarOff + kNumBars * 8;
   static constexpr int kFlagOff = kTmemOff + 4;
   static constexpr int kDirtyOff = kTmemOff + 8;            // with a window; FP8: 2 a V slot
-  static constexpr int kSmemBytes = kDirtyOff + (KV8 ? 8 * kVSlots : 8);
+  static constexpr int kSpanOff = kDirtyOff + (KV8 ? 8 * kVSlots : 8);  // with a window: WindowEdges
+  static constexpr int kSmemBytes = kSpanOff + 24;
   static constexpr uint32_t kTileCols = 256;
   static constexpr uint32_t kTmemCols = QT * kTileCols;
   static constexpr uint32_t kOCol = kBufs * kKeys;
@@ -133,6 +134,29 @@ __device__ __forceinline__ bool table_row_bad(const CrossParams& p, const int32_
   }
   return bad;
 }
+
+// A block's span as the softmax threads look it up in shared memory, tile by
+// tile: held in registers it does not fit next to a row of scores (36 bytes of
+// spills a thread).
+struct WindowEdges {
+  int first, last;  // positions of the first and the last row
+  int w0, s0, head, skip;
+
+  template <int KT>
+  __device__ __forceinline__ int pos(int j) const volatile {
+    return (j < head ? j : j + skip) * KT;
+  }
+  // Whether some row does not see some position of the tile at t0.
+  template <int KT>
+  __device__ __forceinline__ bool edge(const WindowParams& p, int t0) const volatile {
+    return t0 + KT - 1 > first || (t0 + KT - 1 >= p.sinks && t0 <= last - p.window);
+  }
+  // Positions of the tile of 64 at t0 that some row sees.
+  __device__ __forceinline__ uint64_t seen(int t0) const volatile {
+    auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; };
+    return below(last + 1 - t0) & (~below(w0 - t0) | below(s0 - t0));
+  }
+};
 
 // Keys k of a tile from position t0 on that the query at position pos sees.
 __device__ __forceinline__ uint64_t window_mask(const WindowParams& p, int pos, int t0) {
@@ -468,27 +492,6 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
       p.ws_o[(row_at(e / D) / D * p.parts + part) * D + e % D] = 0.f;
     return;
   }
-  // First position of the j-th tile.
-  auto tile_pos = [&](int j) {
-    if constexpr (WIN) return span.pos(tile0 + j);
-    else return lo + j * KT;
-  };
-  // Whether some row does not see some position of the tile at t0.
-  [[maybe_unused]] auto at_edge = [&](int t0) {
-    if constexpr (WIN)
-      return t0 + KT - 1 > base_pos + r0 / G ||
-             (t0 + KT - 1 >= p.sinks && t0 <= span.last - p.window);
-    else return false;
-  };
-  // Positions of the tile at t0 that some row sees.
-  [[maybe_unused]] auto seen_mask = [&](int t0) {
-    uint64_t m = 0;
-    if constexpr (WIN) {
-      auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; };
-      m = below(span.last + 1 - t0) & (~below(span.w0 - t0) | below(span.s0 - t0));
-    }
-    return m;
-  };
   const int row_n = nr > 128 ? 2 : 1;  // row tiles with rows
 
   // ---- barriers, tensor memory, Q ---------------------------------------------
@@ -520,6 +523,8 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
   // each slot, true or false; else two words for edge tiles in turn, the number
   // of the last tile that had some.
   [[maybe_unused]] volatile int* dirty = reinterpret_cast<volatile int*>(smem + Cfg::kDirtyOff);
+  [[maybe_unused]] volatile WindowEdges* edges =
+      reinterpret_cast<volatile WindowEdges*>(smem + Cfg::kSpanOff);
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) {
       mbar_init(k_full(i), KV8 ? Cfg::kConvThreads : 1);
@@ -550,6 +555,14 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
     fence_mbar_init();
     *reinterpret_cast<int*>(smem + Cfg::kFlagOff) = 0;
     if constexpr (!KV8) dirty[0] = dirty[1] = -1;
+    if constexpr (WIN) {
+      edges->first = base_pos + r0 / G;
+      edges->last = span.last;
+      edges->w0 = span.w0;
+      edges->s0 = span.s0;
+      edges->head = span.head;
+      edges->skip = span.skip;
+    }
   }
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + Cfg::kTmemOff);
   volatile int* bad_flag = reinterpret_cast<volatile int*>(smem + Cfg::kFlagOff);
@@ -607,7 +620,9 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
         }
         const uint32_t fb = bars + 8u * slot;
         mbar_arrive_expect_tx(fb, BYTES);
-        now.copy(p, ring + slot * BYTES, map, tile_pos(issued), kvh, shift, GROUP, fb, policy);
+        int at = lo + issued * KT;
+        if constexpr (WIN) at = span.pos(tile0 + issued);
+        now.copy(p, ring + slot * BYTES, map, at, kvh, shift, GROUP, fb, policy);
         now = next;
         look(next, issued + 2);
         if (++slot == slots) {
@@ -710,9 +725,9 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
         const unsigned char* raw = smem + Cfg::kRawOff + (which * RAW + from.slot) * Cfg::kRawBytes;
         unsigned char* const wide = ring + slot * Cfg::kTileBytes;
         if constexpr (WIN) {
-          const int t0 = tile_pos(j);
-          if (which && at_edge(t0)) {
-            const bool met = widen_tile<KT, Cfg::kConvThreads, true>(raw, wide, KT, ct, seen_mask(t0));
+          const int t0 = edges->pos<KT>(tile0 + j);
+          if (which && edges->edge<KT>(p, t0)) {
+            const bool met = widen_tile<KT, Cfg::kConvThreads, true>(raw, wide, KT, ct, edges->seen(t0));
             const bool any = __any_sync(kFullMask, met);
             if (lane == 0) dirty[2 * slot + (ct >> 5)] = any;
             __syncwarp();
@@ -741,14 +756,16 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
     // not finite (-1: none waits) and the keys whose weight is 0 in it, and the
     // number of edge tiles.
     [[maybe_unused]] const int pos = base_pos + (r0 + min(r, nr - 1)) / G;
-    [[maybe_unused]] int odd = -1, edges = 0;
+    [[maybe_unused]] int odd = -1, met_edges = 0;
     [[maybe_unused]] uint64_t odd_zero = 0;
     // Adds that tile's cleared values to O, once its product is in.
     [[maybe_unused]] auto add_odd = [&] {
-      const int t0 = tile_pos(odd), bs = b;
+      const int bs = b;
+      int t0 = 0;
       uint64_t seen = 0, sees_keys = 0;
       if constexpr (WIN) {
-        seen = seen_mask(t0);
+        t0 = edges->pos<KT>(tile0 + odd);
+        seen = edges->seen(t0);
         sees_keys = window_mask(p, pos, t0);
       }
 #pragma unroll 1
@@ -792,8 +809,8 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
       tmem_ld64(sp, w);
       [[maybe_unused]] bool edge = false;
       if constexpr (WIN) {
-        const int t0 = tile_pos(j);
-        edge = at_edge(t0);
+        const int t0 = edges->pos<KT>(tile0 + j);
+        edge = edges->edge<KT>(p, t0);
         if (edge) {
           const uint64_t sees = window_mask(p, pos, t0);
           const uint32_t s0 = (uint32_t)sees, s1 = (uint32_t)(sees >> 32);
@@ -862,22 +879,25 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
             met = dirty[2 * (j % NV)] != 0 || dirty[2 * (j % NV) + 1] != 0;
           } else {
             met = clear_edge<T, D, KT>(smem + Cfg::kVRingOff + (j % NV) * Cfg::kTileBytes,
-                                       seen_mask(tile_pos(j)), rr, 32 * tile_warps(t));
-            if (met) dirty[edges & 1] = j;
+                                       edges->seen(edges->pos<KT>(tile0 + j)), rr,
+                                       32 * tile_warps(t));
+            if (met) dirty[met_edges & 1] = j;
             mbar_arrive(cleared);
-            ok = mbar_wait(cleared, (uint32_t)(edges & 1));
+            ok = mbar_wait(cleared, (uint32_t)(met_edges & 1));
             if (__any_sync(kFullMask, !ok)) {
               ok = false;
               break;
             }
-            met = dirty[edges & 1] == j;
-            ++edges;
+            met = dirty[met_edges & 1] == j;
+            ++met_edges;
           }
-          if (met) {
+          if (met) {  // (P as it was stored: its registers are not kept for this)
+            uint32_t pw[KT / 2];
+            tmem_ld32(sp, pw);
 #pragma unroll
             for (int k = 0; k < KT; k += 2) {
-              if (!(pk[k / 2] & 0x7FFFu)) weightless |= 1ull << k;
-              if (!(pk[k / 2] & 0x7FFF0000u)) weightless |= 2ull << k;
+              if (!(pw[k / 2] & 0x7FFFu)) weightless |= 1ull << k;
+              if (!(pw[k / 2] & 0x7FFF0000u)) weightless |= 2ull << k;
             }
           }
         }

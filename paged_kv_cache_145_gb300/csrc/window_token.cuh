@@ -3,8 +3,8 @@
 //
 // What bounds it is HBM: the window's pages are read once for all of the G
 // query heads of a KV head, 2 G operations a byte (16-bit pools).  One block of
-// four warps per (KV head, sequence, part of the window).  A warp takes every
-// fourth chunk of 16 positions of the span, keys and values by TMA into a ring
+// three warps per (KV head, sequence, part of the window).  A warp takes every
+// third chunk of 16 positions of the span, keys and values by TMA into a ring
 // of its own, and both contractions of a chunk are small dense tiles
 //     S^T[16 x 8] = K . Q^T      O^T[D x 8] += V^T . P^T
 // on mma.sync (m16n8k16; columns G .. 7 are padding): with 8 columns at most
@@ -34,7 +34,11 @@ namespace pkv {
 template <typename T, typename TC, int D>
 struct WindowTokenCfg {
   static constexpr bool kFp8 = sizeof(TC) == 1;
-  static constexpr int kWarps = 4, kThreads = kWarps * 32;
+  // Three warps, so that four blocks (five with narrow rows) share an SM: 64
+  // sequences of 8 KV heads then run at once (43.8 us; four warps and three
+  // blocks 52.5, two and six 43.3, which cost 28 us where three take 27 and FP8
+  // pools 95.7 for 91.0).
+  static constexpr int kWarps = 3, kThreads = kWarps * 32;
   static constexpr int kChunk = 16;
   static constexpr int kRow = D * (int)sizeof(TC);          // bytes
   static constexpr int kPitch = kRow < 128 ? kRow : 128;    // bytes of a row in a box
@@ -48,12 +52,10 @@ struct WindowTokenCfg {
   static constexpr int kBarOff = kRing > kMerge ? kRing : kMerge;
   static constexpr int kPtOff = kBarOff + kWarps * kStages * 8;
   static constexpr int kPtBytes = 2 * 8 * kChunk * 2;       // P^T, and its low part
-  static constexpr int kTableOff = kPtOff + kWarps * kPtBytes;
   static constexpr int kAlign = 1024;
   static constexpr float kBias = !kFp8 && std::is_same<T, __nv_bfloat16>::value ? 0.f : 7.f;
-  static constexpr int kMaxPart = 8192;                     // positions
-  static constexpr int kBlocks = kFp8 || D == 64 ? 4 : 3;   // on an SM, by registers
-  static constexpr int smem_bytes(int part) { return kAlign + kTableOff + part / 8 * 4; }
+  static constexpr int kBlocks = kFp8 || D == 64 ? 5 : 4;   // on an SM, by registers
+  static constexpr int kSmem = kAlign + kPtOff + kWarps * kPtBytes;
 };
 
 // Byte offset of 16-byte column ch of a row in a swizzled box.
@@ -97,58 +99,66 @@ window_token_kernel(const __grid_constant__ WindowParams p, const __grid_constan
   const int chunks = min(span.tiles - chunk0, p.part / C);  // of this part, at least 1
   const int32_t* trow = p.tables + (int64_t)s * p.max_blocks;
 
-  // ---- the part's pages, and whether all of the query's are in the pool ---------
+  // ---- the first copies ----------------------------------------------------------
+  // Each warp reads the table entries of its own chunks, 32 chunks at a time
+  // with the next 32 on their way: nothing but the sequence's length stands before
+  // them, and nothing but them before the copies.  An entry out of range is not
+  // copied (what its rows hold does not matter: the row check below zeroes them),
+  // nor is a page that the query does not see (half of a chunk of two: its rows
+  // are masked and zeroed).
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOff);
-  int* const pages = reinterpret_cast<int*>(smem + Cfg::kTableOff);
-  if (lane == 0) {
-#pragma unroll
-    for (int st = 0; st < NST; ++st) mbar_init(smem_addr(&bars[warp * NST + st]), 1);
-    fence_mbar_init();
-  }
-  const int box_rows = min(p.block_size, C), per_chunk = C / box_rows;
-  for (int i = tid; i < chunks * per_chunk; i += Cfg::kThreads) {
-    const int at = span.pos(chunk0 + i / per_chunk) + i % per_chunk * box_rows;
-    pages[i] = span.sees_page(at, box_rows) ? trow[at >> shift] : -1;
-  }
-  const int bad = __syncthreads_or(window_row_bad(p, c, trow, tid, Cfg::kThreads));
-  if (bad) {
-    if (tid == 0) set_error(p.err, PKV_DEV_TABLE_RANGE);
-    for (int e = tid; e < G * D; e += Cfg::kThreads) {
-      if (whole) out[row0 * D + e] = Elem<T>::from_f(0.f);
-      else p.ws_o[((row0 + e / D) * p.parts + part) * D + e % D] = 0.f;
-    }
-    if (!whole && tid < G) p.ws_ml[(row0 + tid) * p.parts + part] = make_float2(0.f, 1.f);
-    return;
-  }
-
   const int count = warp < chunks ? (chunks - warp + NW - 1) / NW : 0;
+  const bool halves = p.block_size < C;  // two pages a chunk
+  struct Pages {
+    int a, b;
+  };
+  auto look = [&](int j0) {
+    Pages g{-1, -1};
+    const int i = warp + (j0 + lane) * NW;
+    if (i < chunks) {
+      const int t0 = span.pos(chunk0 + i);
+      if (!halves || span.sees_page(t0, C / 2)) g.a = trow[t0 >> shift];
+      if (halves && span.sees_page(t0 + C / 2, C / 2)) g.b = trow[(t0 >> shift) + 1];
+    }
+    return g;
+  };
+  Pages now = look(0), next = look(32);
   const uint32_t ring0 = smem_addr(smem) + warp * NST * Cfg::kStage;
   const uint32_t bar0 = smem_addr(&bars[warp * NST]);
+  if (lane == 0) {
+#pragma unroll
+    for (int st = 0; st < NST; ++st) mbar_init(bar0 + 8 * st, 1);
+    fence_mbar_init();
+  }
   const uint64_t policy = policy_evict_first();
-  // A page that the query does not see (half a chunk of two pages) is not
-  // copied: its rows are masked and zeroed.
-  auto issue = [&](int j) {
-    const int i = warp + j * NW, st = j % NST;
+  auto issue = [&](int j) {  // (the whole warp)
+    if (j > 0 && (j & 31) == 0) {
+      now = next;
+      next = look(j + 32);
+    }
+    const int a = __shfl_sync(kFullMask, now.a, j & 31);
+    const int b = halves ? __shfl_sync(kFullMask, now.b, j & 31) : -1;
+    if (lane != 0) return;
+    const int st = j % NST, blocks = (int)p.num_blocks;
     const uint32_t bar = bar0 + st * 8, dst = ring0 + st * Cfg::kStage;
-    const int row = span.pos(chunk0 + i) & (p.block_size - 1) & ~(box_rows - 1);
-    int boxes = 0;
-    for (int h = 0; h < per_chunk; ++h) boxes += pages[i * per_chunk + h] >= 0;
-    mbar_arrive_expect_tx(bar, boxes * box_rows * Cfg::kRow * 2);
-    for (int h = 0; h < per_chunk; ++h) {
-      const int page = pages[i * per_chunk + h];
-      if (page < 0) continue;
+    const bool go_a = (unsigned)a < (unsigned)blocks, go_b = (unsigned)b < (unsigned)blocks;
+    const int rows = halves ? C / 2 : C;
+    mbar_arrive_expect_tx(bar, (go_a + go_b) * rows * Cfg::kRow * 2);
+    auto copy = [&](int page, int at, int row) {
 #pragma unroll
       for (int cb = 0; cb < Cfg::kBoxes; ++cb) {
-        const uint32_t o = cb * Cfg::kBoxBytes + h * box_rows * Cfg::kPitch;
+        const uint32_t o = cb * Cfg::kBoxBytes + at * Cfg::kPitch;
         const int x = cb * Cfg::kPitch / (int)sizeof(TC);
         tma_load_4d(dst + o, &tmk, x, row, kvh, page, bar, policy);
         tma_load_4d(dst + Cfg::kTile + o, &tmv, x, row, kvh, page, bar, policy);
       }
-    }
+    };
+    if (go_a) copy(a, 0, halves ? 0 : span.pos(chunk0 + warp + j * NW) & (p.block_size - 1));
+    if (go_b) copy(b, C / 2, 0);
   };
-  if (lane == 0) {
-    for (int j = 0; j < min(count, NST); ++j) issue(j);
-  }
+  for (int j = 0; j < min(count, NST); ++j) issue(j);
+  // Every block checks the whole row, so that all parts agree.
+  const bool bad_mine = window_row_bad(p, c, trow, tid, Cfg::kThreads);
 
   // ---- Q^T as B fragments: head gi, zero from G on --------------------------------
   // 16-bit pools: k-step kk's rows 2ti, 2ti + 1 and 2ti + 8, 2ti + 9.  FP8: the
@@ -232,8 +242,11 @@ window_token_kernel(const __grid_constant__ WindowParams p, const __grid_constan
       unsigned char* const vt = smem + (vtile - smem_addr(smem));
       const int t0 = span.pos(chunk0 + warp + j * NW);
       // Rows of the chunk that the query sees.
-      auto below = [](int n) { return n <= 0 ? 0u : n >= C ? 0xFFFFu : (1u << n) - 1u; };
-      const uint32_t sees = below(span.last + 1 - t0) & (~below(span.w0 - t0) | below(span.s0 - t0));
+      uint32_t sees = 0xFFFFu;
+      if (t0 < span.w0 || t0 + C - 1 > span.last) {
+        auto below = [](int n) { return n <= 0 ? 0u : n >= C ? 0xFFFFu : (1u << n) - 1u; };
+        sees = below(span.last + 1 - t0) & (~below(span.w0 - t0) | below(span.s0 - t0));
+      }
 
       // ---- S^T = K . Q^T ------------------------------------------------------------
       float sc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -348,11 +361,9 @@ window_token_kernel(const __grid_constant__ WindowParams p, const __grid_constan
           }
         }
       }
+      if (lane == 0) fence_proxy_async();
       __syncwarp();  // the stage and P^T are rewritten next
-      if (lane == 0 && j + NST < count) {
-        fence_proxy_async();
-        issue(j + NST);
-      }
+      if (j + NST < count) issue(j + NST);
     }
     return j;
   };
@@ -367,14 +378,22 @@ window_token_kernel(const __grid_constant__ WindowParams p, const __grid_constan
     if (lane == 0) set_error(p.err, PKV_DEV_TIMEOUT);
   }
 
-  // ---- the four warps' results joined --------------------------------------------------
+  // ---- the warps' results joined --------------------------------------------------
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     l[h] += __shfl_xor_sync(kFullMask, l[h], 4);
     l[h] += __shfl_xor_sync(kFullMask, l[h], 8);
     l[h] += __shfl_xor_sync(kFullMask, l[h], 16);
   }
-  __syncthreads();
+  if (__syncthreads_or(bad_mine)) {
+    if (tid == 0) set_error(p.err, PKV_DEV_TABLE_RANGE);
+    for (int e = tid; e < G * D; e += Cfg::kThreads) {
+      if (whole) out[row0 * D + e] = Elem<T>::from_f(0.f);
+      else p.ws_o[((row0 + e / D) * p.parts + part) * D + e % D] = 0.f;
+    }
+    if (!whole && tid < G) p.ws_ml[(row0 + tid) * p.parts + part] = make_float2(0.f, 1.f);
+    return;
+  }
   float* const red_acc = reinterpret_cast<float*>(smem);  // [warps][G][D]
   float* const red_m = red_acc + NW * G * D;              // [warps][G]
   float* const red_l = red_m + NW * G;
@@ -445,12 +464,12 @@ int launch_window_token(const WindowParams& p, int num_seqs, const CrossMaps& ma
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load() & bit)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Cfg::smem_bytes(Cfg::kMaxPart)) != cudaSuccess)
+                             Cfg::kSmem) != cudaSuccess)
       return pkv_cuda_failed();
     ready.fetch_or(bit);
   }
   const dim3 grid((unsigned)p.kv_heads, (unsigned)num_seqs, (unsigned)p.parts);
-  kern<<<grid, Cfg::kThreads, Cfg::smem_bytes(p.part), stream>>>(p, maps.k, maps.v);
+  kern<<<grid, Cfg::kThreads, Cfg::kSmem, stream>>>(p, maps.k, maps.v);
   return launch_cross_merge<T, D>(p, num_seqs, stream);
 }
 
