@@ -715,14 +715,14 @@ int paged_build_tables(int64_t num_blocks, int32_t block_size, int32_t* free_lis
  *   extra_out       device, int32[num_blocks]; may be extra_refs
  *   state_out       device, int64[2]; may be free_state
  *   window, sinks   window 0: nothing is given back for a window
- *   workspace       device, >= paged_fork_tables_workspace_bytes(num_seqs,
- *                   num_next) bytes, 16-byte aligned; calls that may overlap
- *                   need one each
+ *   workspace       device, >= paged_fork_tables_workspace_bytes(...) bytes,
+ *                   16-byte aligned; calls that may overlap need one each
  *
  * num_seqs and num_next at most 65535, rows times width at most 2^30,
  * num_blocks at most 2^30.
  */
-size_t paged_fork_tables_workspace_bytes(int32_t num_seqs, int32_t num_next);
+size_t paged_fork_tables_workspace_bytes(int64_t num_blocks, int32_t num_seqs, int32_t num_next,
+                                         int32_t max_blocks_per_seq);
 int paged_fork_tables(const pkv_cache* cache, int32_t* free_list, const int64_t* free_state,
                       const int32_t* extra_refs, const int32_t* parents, int32_t num_next,
                       const int32_t* block_tables, int32_t max_blocks_per_seq,

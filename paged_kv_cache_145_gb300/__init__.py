@@ -721,10 +721,11 @@ def _scratch(workspace, need, dev):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def paged_fork_tables_workspace_bytes(num_seqs, num_next):
+def paged_fork_tables_workspace_bytes(num_blocks, num_seqs, num_next, max_blocks_per_seq):
     """Bytes of workspace that :func:`paged_fork_tables` needs."""
-    return int(_lib.lib().paged_fork_tables_workspace_bytes(_int32(num_seqs, "num_seqs"),
-                                                            _int32(num_next, "num_next")))
+    return int(_lib.lib().paged_fork_tables_workspace_bytes(
+        num_blocks, _int32(num_seqs, "num_seqs"), _int32(num_next, "num_next"),
+        _int32(max_blocks_per_seq, "max_blocks_per_seq")))
 
 
 def paged_fork_tables(cache, free_list, free_state, extra_refs, parents, block_tables, seq_lens,
@@ -765,7 +766,8 @@ def paged_fork_tables(cache, free_list, free_state, extra_refs, parents, block_t
     extra_out = _out_table(extra_out, "extra_out", (cache.num_blocks,), free_list)
     free_state_out = _output(free_state_out, "free_state_out", 2, torch.int64, dev)
     lib = _lib.lib()
-    workspace, ws, ws_len = _scratch(workspace, lib.paged_fork_tables_workspace_bytes(n, nxt), dev)
+    workspace, ws, ws_len = _scratch(
+        workspace, lib.paged_fork_tables_workspace_bytes(cache.num_blocks, n, nxt, width), dev)
     rc = lib.paged_fork_tables(
         cache.ref, free_list.data_ptr(), free_state.data_ptr(), extra_refs.data_ptr(),
         parents.data_ptr(), nxt, block_tables.data_ptr(), width, seq_lens.data_ptr(), n, window,

@@ -101,7 +101,7 @@ SIGNATURES = {
     "paged_attention_window": (ctypes.c_int, [_CACHE, _P, _I64, _P, _I32, _I32, _P, _I32, _P, _I32,
                                               _I32, _I32, _I32, ctypes.c_float, _P, _P,
                                               ctypes.c_size_t, _P]),
-    "paged_fork_tables_workspace_bytes": (ctypes.c_size_t, [_I32, _I32]),
+    "paged_fork_tables_workspace_bytes": (ctypes.c_size_t, [_I64, _I32, _I32, _I32]),
     "paged_fork_tables": (ctypes.c_int, [_CACHE, _P, _P, _P, _P, _I32, _P, _I32, _P, _I32, _I32,
                                          _I32, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "paged_compact_workspace_bytes": (ctypes.c_size_t, [_I64]),

@@ -28,7 +28,7 @@ int pkv_launch_window_token(const pkv::WindowParams& p, int dtype, int io_dtype,
                             const pkv::CrossMaps& maps, cudaStream_t stream);
 int pkv_launch_window(const pkv::WindowParams& p, int dtype, int io_dtype, int num_seqs, int dim,
                       cudaStream_t stream);
-size_t pkv_fork_workspace(int rows, int next);
+size_t pkv_fork_workspace(int64_t num_blocks, int rows, int next, int width);
 int pkv_launch_fork_tables(const pkv_cache* c, size_t elem_bytes, int32_t* ring,
                            const int64_t* state, const int32_t* extra, const int32_t* parents,
                            int next, const int32_t* tables, const int32_t* lens, int rows,
@@ -947,9 +947,12 @@ int paged_block_copy(const pkv_cache* cache, const int64_t* src_dst_pairs, int64
   return pkv_launch_block_copy(cache, src_dst_pairs, num_pairs, elem_bytes(cache->dtype), stream);
 }
 
-size_t paged_fork_tables_workspace_bytes(int32_t num_seqs, int32_t num_next) {
-  if (num_seqs < 0 || num_seqs > 65535 || num_next < 0 || num_next > 65535) return 0;
-  return pkv_fork_workspace(num_seqs, num_next);
+size_t paged_fork_tables_workspace_bytes(int64_t num_blocks, int32_t num_seqs, int32_t num_next,
+                                         int32_t max_blocks_per_seq) {
+  if (num_blocks < 1 || num_blocks > (1 << 30) || num_seqs < 0 || num_seqs > 65535 ||
+      num_next < 0 || num_next > 65535 || max_blocks_per_seq < 1)
+    return 0;
+  return pkv_fork_workspace(num_blocks, num_seqs, num_next, max_blocks_per_seq);
 }
 
 // Checks that paged_fork_tables and paged_compact share.
@@ -993,7 +996,9 @@ int paged_fork_tables(const pkv_cache* cache, int32_t* free_list, const int64_t*
   if ((reinterpret_cast<uintptr_t>(parents) & 3u) || (reinterpret_cast<uintptr_t>(lens_out) & 3u))
     return PKV_ERR_ALIGN;
   if (num_next > 0 && (tables_out == block_tables || lens_out == seq_lens)) return PKV_ERR_ARG;
-  if (workspace_bytes < pkv_fork_workspace(num_seqs, num_next)) return PKV_ERR_WORKSPACE;
+  if (workspace_bytes <
+      pkv_fork_workspace(cache->num_blocks, num_seqs, num_next, max_blocks_per_seq))
+    return PKV_ERR_WORKSPACE;
   if (!pkv_error_word()) return PKV_ERR_CUDA;
   return pkv_launch_fork_tables(cache, elem_bytes(cache->dtype), free_list, free_state, extra_refs,
                                 parents, num_next, block_tables, seq_lens, num_seqs,

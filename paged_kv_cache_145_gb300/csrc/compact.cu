@@ -9,9 +9,6 @@
 // the words of the map, and writes where each block goes, the ring and the
 // counts; a second kernel over the whole GPU moves the data and rewrites the
 // tables.  Bound by HBM: 2 x the moved blocks' bytes.
-#include <algorithm>
-#include <atomic>
-
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -32,9 +29,7 @@ struct CompactParams {
   int32_t* tables_out;      // may be tables
   int32_t* moved_to;        // [num_blocks]
   int num_blocks, block_size, rows, width;
-  uint4* k;
-  uint4* v;
-  int64_t block_vecs;
+  PageMover mover;
   unsigned* err;
   // workspace
   unsigned* map;            // [words]: held blocks
@@ -47,8 +42,10 @@ struct CompactParams {
 constexpr int kCompactThreads = 1024;
 constexpr int kCompactCluster = 8;
 
-__global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kCompactThreads, 1)
+compact_plan_kernel(const __grid_constant__ CompactParams p) {
   cg::cluster_group cluster = cg::this_cluster();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the moves' kernel
   const int rank = (int)cluster.block_rank(), blocks = (int)cluster.num_blocks();
   const int tid = threadIdx.x, lane = tid & 31;
   const int threads = blocks * kCompactThreads, all = rank * kCompactThreads + tid;
@@ -132,29 +129,11 @@ __global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(const Com
   }
 }
 
-constexpr int kMoveThreads = 512;
-constexpr int kMoveUnroll = 4;
-
-// Blocks of threads walk the (move, keys or values, slice) items and then the
-// tables' entries.
-__global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const CompactParams p) {
-  constexpr int kSlice = kMoveThreads * kMoveUnroll;
-  const int moves = p.totals[1], slices = (int)((p.block_vecs + kSlice - 1) / kSlice);
-  const int64_t items = (int64_t)moves * 2 * slices;
-  for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-    const int slice = (int)(i % slices), m = (int)(i / slices >> 1);
-    uint4* const pool = (i / slices & 1) ? p.v : p.k;
-    const uint4* src = pool + (int64_t)p.from[m] * p.block_vecs;
-    uint4* dst = pool + (int64_t)p.to[m] * p.block_vecs;
-    const int64_t u0 = (int64_t)slice * kSlice + threadIdx.x;
-    uint4 buf[kMoveUnroll];
-#pragma unroll
-    for (int j = 0; j < kMoveUnroll; ++j)
-      if (u0 + j * kMoveThreads < p.block_vecs) buf[j] = src[u0 + j * kMoveThreads];
-#pragma unroll
-    for (int j = 0; j < kMoveUnroll; ++j)
-      if (u0 + j * kMoveThreads < p.block_vecs) dst[u0 + j * kMoveThreads] = buf[j];
-  }
+// The moves, and the tables' entries.
+__global__ void __launch_bounds__(kMoveThreads)
+compact_move_kernel(const __grid_constant__ CompactParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  move_pages(p.mover, p.from, p.to, p.totals[1]);
   const bool ok = p.totals[2] == 0;
   for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
     const int have = ok && p.lens[r] > 0 ? (p.lens[r] - 1) / p.block_size + 1 : 0;
@@ -192,10 +171,7 @@ int pkv_launch_compact(const pkv_cache* c, size_t elem_bytes, int32_t* ring, con
   p.block_size = c->block_size;
   p.rows = rows;
   p.width = width;
-  p.k = static_cast<uint4*>(c->k_cache);
-  p.v = static_cast<uint4*>(c->v_cache);
-  p.block_vecs =
-      (int64_t)c->num_kv_heads * c->block_size * c->head_dim * (int64_t)elem_bytes / 16;
+  p.mover = page_mover(c, elem_bytes);
   p.err = pkv_error_word();
   const int64_t words = (c->num_blocks + 31) / 32;
   p.map = static_cast<unsigned*>(workspace);
@@ -214,20 +190,12 @@ int pkv_launch_compact(const pkv_cache* c, size_t elem_bytes, int32_t* ring, con
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, compact_plan_kernel, p) != cudaSuccess) return pkv_cuda_failed();
-  static std::atomic<int> places[64];  // thread blocks that run at a time, per device
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return pkv_cuda_failed();
-  int grid = places[dev & 63].load();
-  if (grid == 0) {
-    int sms = 0, per_sm = 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, compact_move_kernel, kMoveThreads, 0) !=
-            cudaSuccess ||
-        sms < 1 || per_sm < 1)
-      return pkv_cuda_failed();
-    grid = sms * per_sm;
-    places[dev & 63].store(grid);
-  }
-  compact_move_kernel<<<grid, kMoveThreads, 0, stream>>>(p);
-  return pkv_launch_status();
+  static PagePlaces places;
+  const int grid = places.of(compact_move_kernel);
+  if (grid < 1) return pkv_cuda_failed();
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kMoveThreads);
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, compact_move_kernel, p) == cudaSuccess ? PKV_OK : pkv_cuda_failed();
 }

@@ -9,14 +9,17 @@
 // first child keeps it, every other child takes a fresh block and a copy.  A
 // block whose holders come to none goes back; a block that several rows drop
 // goes back once, at the place of its first entry (rows in order, logical
-// blocks in order).  That first entry is found by an atomic minimum of the
-// entries' numbers on the block's own count, below every count there is, so
-// that the ring's order does not depend on the order of the threads.
+// blocks in order), found by an atomic minimum of the entries' numbers: the
+// ring's order does not depend on the order of the threads.
 //
 // All or nothing: the counts are added up before anything else is written, and
-// taken back (integer sums are exact in any order) if they show that a block
-// had fewer holders than entries.  One cluster does it, with a cluster barrier
-// between the stages; block_move_kernel then copies over the whole GPU.
+// taken back (integer sums are exact in any order) if a block had fewer holders
+// than entries or the step fails otherwise.
+//
+// What bounds it: latency.  One cluster (one block for few entries) does it, a
+// warp per row with four entries a lane in flight, in five stages with a barrier
+// between them; each is a table entry (from L1 after the first) and one gather.
+// A second kernel, launched early, copies the blocks over the whole GPU.
 #include <algorithm>
 #include <climits>
 
@@ -42,23 +45,32 @@ struct ForkParams {
   int32_t* lens_out;        // [S]
   int num_blocks, block_size, rows, next, width;
   int window, sinks;        // window 0: none
+  int share;                // rows of a thread block
+  PageMover mover;
   unsigned* err;
   // workspace
-  int64_t* pairs;           // [S][2]: copies, (0, 0) for none
+  int* claim;               // [num_blocks]: the first entry that drops a block (written where used)
   int* children;            // [R]
   int* first;               // [R]: a row's first child
   int* solo;                // [R]: its last block has no other holder
-  int* back;                // [R]: blocks given back, then those of the rows before
-  int* fresh;               // [S]: fresh blocks taken before, -1 for a row that takes none
-  int* totals;              // fresh blocks, blocks given back, error bits
+  int* back;                // [R]: blocks given back, by this row
+  int* fresh;               // [S]: fresh blocks taken before
+  int* from;                // [S]: copies
+  int* to;
+  unsigned* gone;           // [R][(W + 31) / 32]: entries whose blocks go back
+  int* totals;              // copies, error bits
 };
 
 constexpr int kForkThreads = 1024;
 constexpr int kForkCluster = 8;
+constexpr int64_t kForkSmall = 8192;  // entries that one block takes
+constexpr int kForkBatch = 4;  // entries a lane holds at a time
 
 // A row of this step, as the lanes of a warp see it.
 struct ForkRow {
   int len, have, partial;   // partial: index of the partly filled last block, or -1
+  int near;                 // entries from here on are in the window
+  int far;                  // entries below are the sinks'
   const int32_t* entries;
 };
 
@@ -67,59 +79,73 @@ __device__ __forceinline__ ForkRow fork_row(const ForkParams& p, int r) {
   w.len = p.lens[r];
   w.have = w.len > 0 ? (w.len - 1) / p.block_size + 1 : 0;
   w.partial = w.len % p.block_size ? w.have - 1 : -1;
+  // (e + 1) b > len + 1 - window, e b < sinks
+  w.near = p.window == 0 || w.len < p.window ? 0 : (w.len + 1 - p.window) / p.block_size;
+  w.far = (p.sinks - 1) / p.block_size + (p.sinks > 0);
   w.entries = p.tables + (int64_t)r * p.width;
   return w;
 }
 
-// Whether entry e of a row of `len` positions is seen by a query from position
-// len on.
-__device__ __forceinline__ bool fork_keeps(const ForkParams& p, int len, int e) {
-  if (p.window == 0) return true;
-  const int64_t from = (int64_t)e * p.block_size;
-  return from < p.sinks || from + p.block_size > (int64_t)len + 1 - p.window;
+// Whether entry e is seen by a query behind the row.
+__device__ __forceinline__ bool fork_keeps(const ForkRow& w, int e) {
+  return e >= w.near || e < w.far;
 }
 
 // Change of the holders of a row's entry e (of a block, not -1).
-__device__ __forceinline__ int fork_delta(const ForkParams& p, const ForkRow& w, int e, int children,
-                                          bool solo) {
+__device__ __forceinline__ int fork_delta(const ForkRow& w, int e, int children, bool solo) {
   if (e == w.partial) return solo && children > 0 ? 0 : -1;
-  return fork_keeps(p, w.len, e) ? children - 1 : -1;
+  return fork_keeps(w, e) ? children - 1 : -1;
 }
 
-__global__ void __launch_bounds__(kForkThreads) fork_tables_kernel(const ForkParams p) {
+// A lane's next kForkBatch entries of a row from e0 on (-1 past the row).
+__device__ __forceinline__ void fork_entries(const ForkRow& w, int e0, int (&x)[kForkBatch]) {
+#pragma unroll
+  for (int k = 0; k < kForkBatch; ++k) x[k] = e0 + 32 * k < w.have ? w.entries[e0 + 32 * k] : -1;
+}
+
+__global__ void __launch_bounds__(kForkThreads, 1)
+fork_tables_kernel(const __grid_constant__ ForkParams p) {
   cg::cluster_group cluster = cg::this_cluster();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the copies' kernel
   const int rank = (int)cluster.block_rank(), blocks = (int)cluster.num_blocks();
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int threads = blocks * kForkThreads, all = rank * kForkThreads + tid;
-  const int warps = threads >> 5, w0 = all >> 5;
-  const int R = p.rows, S = p.next, N = p.num_blocks, b = p.block_size;
+  const int R = p.rows, S = p.next, N = p.num_blocks, b = p.block_size, W = p.width;
+  const int words = (W + 31) / 32, B = kForkBatch * 32;
+  const int r0 = min(rank * p.share, R), r1 = min(r0 + p.share, R);  // this block's rows
   __shared__ int s_scan[33];
   const int64_t head = p.state[0], count = p.state[1];
-  auto fail = [&](unsigned bits) { atomicOr(p.totals + 2, (int)bits); };
-  auto ring_at = [&](int64_t i) { return (head + i) % N; };
-  // Runs f(row, entry index, block) for the held entries of every row, a warp
-  // per row.
-  auto entries = [&](auto f) {
-    for (int r = w0; r < R; r += warps) {
-      const ForkRow w = fork_row(p, r);
-      const int c = p.children[r];
-      const bool solo = p.solo[r] != 0;
-      for (int e = lane; e < w.have; e += 32) {
-        const int x = w.entries[e];
-        if (x >= 0) f(r, e, x, fork_delta(p, w, e, c, solo));
-      }
-    }
+  auto barrier = [&] {
+    if (blocks > 1) cluster.sync();
+    else __syncthreads();
   };
+  auto fail = [&](unsigned bits) { atomicOr(p.totals + 1, (int)bits); };
+  auto ring_at = [&](int64_t i) {
+    const int64_t x = head + i;
+    return x >= N ? x - N : x;
+  };
+  // (written by other threads: read where the atomics land)
+  auto holders = [&](int x) { return __ldcg(p.extra_out + x); };
 
   // ---- nothing chosen yet --------------------------------------------------------
   for (int r = all; r < R; r += threads) {
     p.children[r] = 0;
     p.first[r] = INT_MAX;
   }
-  if (all < 3) p.totals[all] = 0;
-  if (p.extra_out != p.extra)
-    for (int x = all; x < N; x += threads) p.extra_out[x] = p.extra[x];
-  cluster.sync();
+  if (all < 2) p.totals[all] = 0;
+  if (p.extra_out != p.extra) {
+    constexpr int U = 8;
+    for (int x0 = all; x0 < N; x0 += U * threads) {
+      int v[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (x0 + k * threads < N) v[k] = p.extra[x0 + k * threads];
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (x0 + k * threads < N) p.extra_out[x0 + k * threads] = v[k];
+    }
+  }
+  barrier();
 
   // ---- children; the rows' numbers and entries ------------------------------------
   if (all == 0 && (head < 0 || head >= N || count < 0 || count > N)) fail(PKV_DEV_FREE_LIST);
@@ -132,32 +158,34 @@ __global__ void __launch_bounds__(kForkThreads) fork_tables_kernel(const ForkPar
       fail(PKV_DEV_PAIR_RANGE);
     }
   }
-  for (int r = w0; r < R; r += warps) {
+  for (int r = r0 + warp; r < r1; r += kForkThreads / 32) {
     const int len = p.lens[r];
-    if (len < 0 || len > (int64_t)p.width * b) {
+    if (len < 0 || len > (int64_t)W * b) {
       if (lane == 0) fail(PKV_DEV_SEQ_LEN);
       continue;
     }
     const ForkRow w = fork_row(p, r);
-    bool bad = false;
-    for (int e = lane; e < w.have; e += 32) {
-      const int x = w.entries[e];
-      bad |= x < -1 || x >= N || (x < 0 && e == w.partial);
+    const int last = w.partial >= 0 ? w.entries[w.partial] : 0;
+    bool bad = w.partial >= 0 && last < 0;
+    for (int e0 = lane; e0 < w.have; e0 += B) {
+      int x[kForkBatch];
+      fork_entries(w, e0, x);
+#pragma unroll
+      for (int k = 0; k < kForkBatch; ++k) bad |= x[k] < -1 || x[k] >= N;
     }
     if (bad) fail(PKV_DEV_TABLE_RANGE);
-    if (lane == 0) {
-      const int x = w.partial >= 0 ? w.entries[w.partial] : -1;
-      p.solo[r] = x >= 0 && x < N && p.extra[x] == 0;
-    }
+    if (lane == 0) p.solo[r] = last >= 0 && last < N && p.extra[last] == 0;
   }
-  cluster.sync();
+  barrier();
+  bool ok = __ldcg(p.totals + 1) == 0;
 
-  // ---- fresh blocks, counted in the order of the next rows -------------------------
-  if (rank == 0 && p.totals[2] == 0) {
+  // ---- fresh blocks, in the order of the next rows; holders added up -----------------
+  if (ok && rank == 0) {
     const int taken = block_scan(S, s_scan, p.fresh, [&](int s) {
       const int r = p.parents[s];
-      return r >= 0 && p.lens[r] % b != 0 && (p.first[r] != s || !p.solo[r]);
+      return r >= 0 && p.lens[r] % b != 0 && (__ldcg(p.first + r) != s || !__ldcg(p.solo + r));
     });
+    if (tid == 0) p.totals[0] = taken;
     if (taken > count) {
       if (tid == 0) fail(PKV_DEV_NOMEM);
     } else {
@@ -166,101 +194,170 @@ __global__ void __launch_bounds__(kForkThreads) fork_tables_kernel(const ForkPar
         if (x < 0 || x >= N) fail(PKV_DEV_FREE_LIST);
       }
     }
-    if (tid == 0) p.totals[0] = taken;
   }
-  cluster.sync();
-  bool ok = p.totals[2] == 0;
+  // Runs f(row, entry, change) for the rows' held entries, kForkBatch at a time.
+  auto rows = [&](auto f) {
+    for (int r = r0 + warp; r < r1; r += kForkThreads / 32) {
+      const ForkRow w = fork_row(p, r);
+      const int c = __ldcg(p.children + r);
+      const bool solo = p.solo[r] != 0;  // (this warp's own)
+      for (int e0 = lane; e0 < w.have; e0 += B) {
+        int x[kForkBatch], d[kForkBatch];
+        fork_entries(w, e0, x);
+#pragma unroll
+        for (int k = 0; k < kForkBatch; ++k) d[k] = x[k] < 0 ? 0 : fork_delta(w, e0 + 32 * k, c, solo);
+        f(r, e0, x, d);
+      }
+    }
+  };
+  if (ok)
+    rows([&](int, int, const int (&x)[kForkBatch], const int (&d)[kForkBatch]) {
+#pragma unroll
+      for (int k = 0; k < kForkBatch; ++k) {
+        if (d[k] < 0) p.claim[x[k]] = INT_MAX;
+        if (d[k]) atomicAdd(p.extra_out + x[k], d[k]);
+      }
+    });
+  barrier();
 
-  // ---- holders: added up, looked at, and taken back if they do not hold ------------
+  // ---- holders that do not hold; the first entry of each block that goes back --------
+  if (ok)
+    rows([&](int r, int e0, const int (&x)[kForkBatch], const int (&d)[kForkBatch]) {
+      int left[kForkBatch];
+#pragma unroll
+      for (int k = 0; k < kForkBatch; ++k) left[k] = d[k] < 0 ? holders(x[k]) : 0;
+#pragma unroll
+      for (int k = 0; k < kForkBatch; ++k) {
+        if (left[k] < -1) fail(PKV_DEV_SHARING);
+        if (left[k] == -1) atomicMin(p.claim + x[k], r * W + e0 + 32 * k);
+      }
+    });
+  barrier();
   if (ok) {
-    entries([&](int, int, int x, int d) {
-      if (d) atomicAdd(p.extra_out + x, d);
-    });
-    cluster.sync();
-    entries([&](int, int, int x, int d) {
-      if (d < 0 && p.extra_out[x] < -1) fail(PKV_DEV_SHARING);
-    });
-    cluster.sync();
-    ok = p.totals[2] == 0;
+    for (int r = r0 + warp; r < r1; r += kForkThreads / 32) {
+      const ForkRow w = fork_row(p, r);
+      const int c = __ldcg(p.children + r);
+      const bool solo = p.solo[r] != 0;
+      int n = 0;
+      for (int e0 = lane; e0 - lane < w.have; e0 += B) {
+        int x[kForkBatch], left[kForkBatch], mine[kForkBatch];
+        fork_entries(w, e0, x);
+#pragma unroll
+        for (int k = 0; k < kForkBatch; ++k) {
+          const bool drops = x[k] >= 0 && fork_delta(w, e0 + 32 * k, c, solo) < 0;
+          left[k] = drops ? holders(x[k]) : 0;
+          mine[k] = drops ? __ldcg(p.claim + x[k]) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kForkBatch; ++k) {
+          const unsigned hit =
+              __ballot_sync(kFullMask, left[k] == -1 && mine[k] == r * W + e0 + 32 * k);
+          n += __popc(hit);
+          if (lane == 0 && (e0 >> 5) + k < words) p.gone[(int64_t)r * words + (e0 >> 5) + k] = hit;
+        }
+      }
+      if (lane == 0) p.back[r] = n;
+    }
+  }
+  barrier();
+
+  // ---- what goes back, behind the tail -------------------------------------------------
+  int given = 0;
+  if (ok) {
+    // Blocks that the rows before this block's give back, and all rows.
+    int before = 0;
+    for (int r = tid; r < R; r += kForkThreads) {
+      const int n = __ldcg(p.back + r);
+      given += n;
+      if (r < r0) before += n;
+    }
+    before = block_sum(before, s_scan);
+    given = block_sum(given, s_scan);
+    ok = __ldcg(p.totals + 1) == 0;
+    if (given > N - count) {  // the ring holds a held block
+      if (all == 0) fail(PKV_DEV_FREE_LIST);
+      ok = false;
+    }
     if (ok) {
-      // ---- what goes back: each block at its first entry --------------------------
-      const int W = p.width;
-      entries([&](int r, int e, int x, int d) {
-        if (d < 0 && p.extra_out[x] < 0) atomicMin(p.extra_out + x, INT_MIN + r * W + e);
+      block_scan(r1 - r0, s_scan, p.first + r0, [&](int i) { return p.back[r0 + i]; });
+      // (p.first is read no more as such: the copies' choice is in p.fresh's sums)
+    } else {
+      rows([&](int, int, const int (&x)[kForkBatch], const int (&d)[kForkBatch]) {
+#pragma unroll
+        for (int k = 0; k < kForkBatch; ++k)
+          if (d[k]) atomicAdd(p.extra_out + x[k], -d[k]);
       });
-      cluster.sync();
-      for (int r = w0; r < R; r += warps) {
+    }
+    if (ok)
+      for (int r = r0 + warp; r < r1; r += kForkThreads / 32) {
         const ForkRow w = fork_row(p, r);
-        int n = 0;
-        for (int e = lane; e < w.have; e += 32) {
-          const int x = w.entries[e];
-          n += x >= 0 && p.extra_out[x] == INT_MIN + r * W + e;
-        }
-        n = __reduce_add_sync(kFullMask, n);
-        if (lane == 0) p.back[r] = n;
-      }
-      cluster.sync();
-      if (rank == 0) {
-        const int given = block_scan(R, s_scan, p.back, [&](int r) { return p.back[r]; });
-        if (tid == 0) {
-          p.totals[1] = given;
-          if (given > N - count) fail(PKV_DEV_FREE_LIST);  // (the ring holds a held block)
-        }
-      }
-      cluster.sync();
-      ok = p.totals[2] == 0;
-      for (int r = w0; r < R; r += warps) {
-        const ForkRow w = fork_row(p, r);
-        int64_t at = count + p.back[r];
+        int64_t at = count + before + p.first[r];
         for (int e0 = 0; e0 < w.have; e0 += 32) {
-          const int e = e0 + lane, x = e < w.have ? w.entries[e] : -1;
-          const bool mine = x >= 0 && p.extra_out[x] == INT_MIN + r * W + e;
-          const unsigned hit = __ballot_sync(kFullMask, mine);
-          if (mine) {
-            if (ok) p.ring[ring_at(at + __popc(hit & ((1u << lane) - 1u)))] = x;
-            p.extra_out[x] = ok ? 0 : -1;
+          const unsigned hit = p.gone[(int64_t)r * words + (e0 >> 5)];
+          if (hit >> lane & 1u) {
+            const int x = w.entries[e0 + lane];
+            p.ring[ring_at(at + __popc(hit & ((1u << lane) - 1u)))] = x;
+            p.extra_out[x] = 0;
           }
           at += __popc(hit);
         }
       }
-      if (!ok) cluster.sync();
-    }
-    if (!ok)
-      entries([&](int, int, int x, int d) {
-        if (d) atomicAdd(p.extra_out + x, -d);
-      });
   }
 
   // ---- the next rows, or, after any error, empty ones -------------------------------
+  const int taken = ok ? __ldcg(p.totals) : 0;
   if (all == 0) {
-    if (!ok) set_error(p.err, (unsigned)p.totals[2]);
-    p.state_out[0] = ok ? ring_at(p.totals[0]) : head;
-    p.state_out[1] = ok ? count - p.totals[0] + p.totals[1] : count;
-  }
-  for (int s = w0; s < S; s += warps) {
-    const int r = ok ? p.parents[s] : -1;
-    ForkRow w{0, 0, -1, nullptr};
-    if (r >= 0) w = fork_row(p, r);
-    const bool copies = w.partial >= 0 && (p.first[r] != s || !p.solo[r]);
-    const int fresh = copies ? p.ring[ring_at(p.fresh[s])] : -1;
-    if (lane == 0) {
-      p.lens_out[s] = w.len;
-      p.pairs[2 * (int64_t)s] = copies ? w.entries[w.partial] : 0;
-      p.pairs[2 * (int64_t)s + 1] = copies ? fresh : 0;
+    if (!ok) {
+      set_error(p.err, (unsigned)(__ldcg(p.totals + 1)));
+      p.totals[0] = 0;
     }
-    int32_t* const out = p.tables_out + (int64_t)s * p.width;
-    for (int e = lane; e < p.width; e += 32) {
-      int x = -1;
-      if (e < w.have && fork_keeps(p, w.len, e)) x = copies && e == w.partial ? fresh : w.entries[e];
-      out[e] = x;
+    p.state_out[0] = ok ? ring_at(taken) : head;
+    p.state_out[1] = ok ? count - taken + given : count;
+  }
+  for (int s = all >> 5; s < S; s += threads >> 5) {
+    const int r = ok ? p.parents[s] : -1;
+    ForkRow w{0, 0, -1, 0, 0, nullptr};
+    bool copies = false;
+    int fresh = -1;
+    if (r >= 0) {
+      w = fork_row(p, r);
+      // (one fresh block more after this row than before it)
+      const int at = __ldcg(p.fresh + s);
+      copies = (s + 1 < S ? __ldcg(p.fresh + s + 1) : taken) > at;
+      if (copies) {
+        fresh = p.ring[ring_at(at)];
+        if (lane == 0) {
+          p.from[at] = w.entries[w.partial];
+          p.to[at] = fresh;
+        }
+      }
+    }
+    if (lane == 0) p.lens_out[s] = w.len;
+    int32_t* const out = p.tables_out + (int64_t)s * W;
+    for (int e0 = lane; e0 < W; e0 += B) {
+      int x[kForkBatch];
+      fork_entries(w, e0, x);
+#pragma unroll
+      for (int k = 0; k < kForkBatch; ++k) {
+        const int e = e0 + 32 * k;
+        if (e < W) out[e] = copies && e == w.partial ? fresh : fork_keeps(w, e) ? x[k] : -1;
+      }
     }
   }
 }
 
+// The copies of partly filled last blocks.
+__global__ void __launch_bounds__(kMoveThreads) fork_copy_kernel(const __grid_constant__ ForkParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  move_pages(p.mover, p.from, p.to, p.totals[0]);
+}
+
 }  // namespace pkv
 
-size_t pkv_fork_workspace(int rows, int next) {
-  return 16 * (size_t)next + 4 * ((size_t)4 * rows + next + 4);
+// claim, children, first, solo, back, fresh, from, to, gone, totals
+size_t pkv_fork_workspace(int64_t num_blocks, int rows, int next, int width) {
+  return 4 * ((size_t)num_blocks + 4 * (size_t)rows + 3 * (size_t)next +
+              (size_t)rows * ((width + 31) / 32) + 4);
 }
 
 int pkv_launch_fork_tables(const pkv_cache* c, size_t elem_bytes, int32_t* ring,
@@ -288,24 +385,41 @@ int pkv_launch_fork_tables(const pkv_cache* c, size_t elem_bytes, int32_t* ring,
   p.width = width;
   p.window = window;
   p.sinks = sinks;
+  p.mover = page_mover(c, elem_bytes);
   p.err = pkv_error_word();
-  p.pairs = static_cast<int64_t*>(workspace);
-  p.children = reinterpret_cast<int*>(p.pairs + 2 * (int64_t)next);
+  p.claim = static_cast<int*>(workspace);
+  p.children = p.claim + c->num_blocks;
   p.first = p.children + rows;
   p.solo = p.first + rows;
   p.back = p.solo + rows;
   p.fresh = p.back + rows;
-  p.totals = p.fresh + next;
+  p.from = p.fresh + next;
+  p.to = p.from + next;
+  p.gone = reinterpret_cast<unsigned*>(p.to + next);
+  p.totals = reinterpret_cast<int*>(p.gone + (int64_t)rows * ((width + 31) / 32));
+  const int64_t entries = (int64_t)(rows + next) * width;
+  const bool small = entries <= kForkSmall && c->num_blocks <= 8 * kForkSmall;
+  const int cluster = small ? 1 : kForkCluster;
+  p.share = (rows + cluster - 1) / cluster;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kForkCluster);
+  cfg.gridDim = dim3(cluster);
   cfg.blockDim = dim3(kForkThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = kForkCluster;
+  attr.val.clusterDim.x = (unsigned)cluster;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = small ? 0 : 1;
   if (cudaLaunchKernelEx(&cfg, fork_tables_kernel, p) != cudaSuccess) return pkv_cuda_failed();
-  return next > 0 ? pkv_launch_block_copy(c, p.pairs, next, elem_bytes, stream) : PKV_OK;
+  if (next == 0) return PKV_OK;
+  static PagePlaces places;
+  const int grid = places.of(fork_copy_kernel);
+  if (grid < 1) return pkv_cuda_failed();
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(grid, (int64_t)next * 2 * p.mover.slices()));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.numAttrs = 1;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, fork_copy_kernel, p) == cudaSuccess ? PKV_OK : pkv_cuda_failed();
 }

@@ -273,7 +273,7 @@ def test_captured_steps_in_place():
     d = m.device()
     parents = torch.zeros(4, dtype=torch.int32, device="cuda")
     t2, l2 = torch.empty_like(d["block_tables"]), torch.empty_like(d["seq_lens"])
-    ws = torch.empty(pkv.paged_fork_tables_workspace_bytes(4, 4), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(pkv.paged_fork_tables_workspace_bytes(200, 4, 4, 8), dtype=torch.uint8, device="cuda")
 
     def call():
         pkv.paged_fork_tables(parents=parents, tables_out=t2, lens_out=l2,

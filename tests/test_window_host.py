@@ -114,7 +114,7 @@ def test_fork_tables_argument_errors(lib):
     assert fork(lib, c, sout=0xa004) == -4
     assert fork(lib, c, ws=0) == -5
     assert fork(lib, c, ws=0xb008) == -4
-    assert fork(lib, c, ws_bytes=lib.paged_fork_tables_workspace_bytes(4, 3) - 1) == -5
+    assert fork(lib, c, ws_bytes=lib.paged_fork_tables_workspace_bytes(32, 4, 3, 8) - 1) == -5
     assert fork(lib, c, tout=0x5000) == -3
     assert fork(lib, c, lout=0x6000) == -3
     for kw in (dict(nxt=-1), dict(nxt=65536), dict(n=-1), dict(n=65536), dict(width=0), dict(win=-1),
@@ -122,7 +122,7 @@ def test_fork_tables_argument_errors(lib):
         assert fork(lib, c, **kw) == -3
     assert fork(lib, fake_cache(num_blocks=(1 << 30) + 1)) == -3
     assert fork(lib, fake_cache(v_cache=0)) == -1
-    assert lib.paged_fork_tables_workspace_bytes(-1, 3) == 0
+    assert lib.paged_fork_tables_workspace_bytes(32, -1, 3, 8) == 0
 
 
 def compact(lib, cache, ring=0x1000, state=0x2000, extra=0x3000, tables=0x5000, width=8, lens=0x6000,
