@@ -16,10 +16,12 @@
 // taken back (integer sums are exact in any order) if a block had fewer holders
 // than entries or the step fails otherwise.
 //
-// What bounds it: latency.  One cluster (one block for few entries) does it, a
-// warp per row with four entries a lane in flight, in five stages with a barrier
-// between them; each is a table entry (from L1 after the first) and one gather.
-// A second kernel, launched early, copies the blocks over the whole GPU.
+// What bounds it: latency.  One cluster (one block for few entries) does it in
+// five stages with a barrier between them.  A warp has a group of up to 32 rows:
+// its lanes load the rows' numbers together, then the warp walks row by row with
+// four entries a lane in flight, from L1 after the first stage, and one gather
+// for each.  A second kernel, launched early, copies the blocks over the whole
+// GPU.
 #include <algorithm>
 #include <climits>
 
@@ -74,9 +76,9 @@ struct ForkRow {
   const int32_t* entries;
 };
 
-__device__ __forceinline__ ForkRow fork_row(const ForkParams& p, int r) {
+__device__ __forceinline__ ForkRow fork_row(const ForkParams& p, int r, int len) {
   ForkRow w;
-  w.len = p.lens[r];
+  w.len = len;
   w.have = w.len > 0 ? (w.len - 1) / p.block_size + 1 : 0;
   w.partial = w.len % p.block_size ? w.have - 1 : -1;
   // (e + 1) b > len + 1 - window, e b < sinks
@@ -127,6 +129,17 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
   // (written by other threads: read where the atomics land)
   auto holders = [&](int x) { return __ldcg(p.extra_out + x); };
 
+  // Runs f(row, lane's row numbers) by groups of a warp's rows: `load` gives each
+  // lane its row's numbers, f gets those of row r by shuffles from lane i.
+  const int group = min(32, max(1, (p.share + kForkThreads / 32 - 1) / (kForkThreads / 32)));
+  auto groups = [&](auto load, auto f) {
+    for (int g0 = r0 + warp * group; g0 < r1; g0 += kForkThreads / 32 * group) {
+      const int n = min(group, r1 - g0);
+      const auto mine = load(g0 + min(lane, n - 1));
+      for (int i = 0; i < n; ++i) f(g0 + i, i, mine);
+    }
+  };
+
   // ---- nothing chosen yet --------------------------------------------------------
   for (int r = all; r < R; r += threads) {
     p.children[r] = 0;
@@ -158,24 +171,33 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
       fail(PKV_DEV_PAIR_RANGE);
     }
   }
-  for (int r = r0 + warp; r < r1; r += kForkThreads / 32) {
-    const int len = p.lens[r];
-    if (len < 0 || len > (int64_t)W * b) {
-      if (lane == 0) fail(PKV_DEV_SEQ_LEN);
-      continue;
-    }
-    const ForkRow w = fork_row(p, r);
-    const int last = w.partial >= 0 ? w.entries[w.partial] : 0;
-    bool bad = w.partial >= 0 && last < 0;
-    for (int e0 = lane; e0 < w.have; e0 += B) {
-      int x[kForkBatch];
-      fork_entries(w, e0, x);
+  struct First {
+    int len, last;  // -1: none, -2: no length; the partly filled last block (0: none)
+  };
+  groups(
+      [&](int r) {
+        First m{p.lens[r], 0};
+        if (m.len < 0 || m.len > (int64_t)W * b) m.len = -2;
+        else if (m.len % b) m.last = p.tables[(int64_t)r * W + m.len / b];
+        p.solo[r] = m.last >= 0 && m.last < N && p.extra[m.last] == 0;  // (equal lanes agree)
+        return m;
+      },
+      [&](int r, int i, const First& m) {
+        const int len = __shfl_sync(kFullMask, m.len, i);
+        bool bad = __shfl_sync(kFullMask, m.last, i) < 0;
+        if (len < 0) {
+          if (lane == 0) fail(PKV_DEV_SEQ_LEN);
+          return;
+        }
+        const ForkRow w = fork_row(p, r, len);
+        for (int e0 = lane; e0 < w.have; e0 += B) {
+          int x[kForkBatch];
+          fork_entries(w, e0, x);
 #pragma unroll
-      for (int k = 0; k < kForkBatch; ++k) bad |= x[k] < -1 || x[k] >= N;
-    }
-    if (bad) fail(PKV_DEV_TABLE_RANGE);
-    if (lane == 0) p.solo[r] = last >= 0 && last < N && p.extra[last] == 0;
-  }
+          for (int k = 0; k < kForkBatch; ++k) bad |= x[k] < -1 || x[k] >= N;
+        }
+        if (bad) fail(PKV_DEV_TABLE_RANGE);
+      });
   barrier();
   bool ok = __ldcg(p.totals + 1) == 0;
 
@@ -195,21 +217,29 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
       }
     }
   }
-  // Runs f(row, entry, change) for the rows' held entries, kForkBatch at a time.
-  auto rows = [&](auto f) {
-    for (int r = r0 + warp; r < r1; r += kForkThreads / 32) {
-      const ForkRow w = fork_row(p, r);
-      const int c = __ldcg(p.children + r);
-      const bool solo = p.solo[r] != 0;  // (this warp's own)
-      for (int e0 = lane; e0 < w.have; e0 += B) {
+  struct Numbers {
+    int len, children, solo;
+  };
+  auto numbers = [&](int r) {
+    return Numbers{p.lens[r], __ldcg(p.children + r), __ldcg(p.solo + r)};
+  };
+  // Runs f(row, entry, blocks, changes) for the rows' entries, kForkBatch a lane.
+  auto rows = [&](auto f, auto done) {
+    groups(numbers, [&](int r, int i, const Numbers& m) {
+      const ForkRow w = fork_row(p, r, __shfl_sync(kFullMask, m.len, i));
+      const int c = __shfl_sync(kFullMask, m.children, i);
+      const bool solo = __shfl_sync(kFullMask, m.solo, i) != 0;
+      for (int e0 = lane; e0 - lane < w.have; e0 += B) {
         int x[kForkBatch], d[kForkBatch];
         fork_entries(w, e0, x);
 #pragma unroll
         for (int k = 0; k < kForkBatch; ++k) d[k] = x[k] < 0 ? 0 : fork_delta(w, e0 + 32 * k, c, solo);
         f(r, e0, x, d);
       }
-    }
+      done(r);
+    });
   };
+  auto nothing = [](int) {};
   if (ok)
     rows([&](int, int, const int (&x)[kForkBatch], const int (&d)[kForkBatch]) {
 #pragma unroll
@@ -217,7 +247,7 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
         if (d[k] < 0) p.claim[x[k]] = INT_MAX;
         if (d[k]) atomicAdd(p.extra_out + x[k], d[k]);
       }
-    });
+    }, nothing);
   barrier();
 
   // ---- holders that do not hold; the first entry of each block that goes back --------
@@ -231,33 +261,27 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
         if (left[k] < -1) fail(PKV_DEV_SHARING);
         if (left[k] == -1) atomicMin(p.claim + x[k], r * W + e0 + 32 * k);
       }
-    });
+    }, nothing);
   barrier();
   if (ok) {
-    for (int r = r0 + warp; r < r1; r += kForkThreads / 32) {
-      const ForkRow w = fork_row(p, r);
-      const int c = __ldcg(p.children + r);
-      const bool solo = p.solo[r] != 0;
-      int n = 0;
-      for (int e0 = lane; e0 - lane < w.have; e0 += B) {
-        int x[kForkBatch], left[kForkBatch], mine[kForkBatch];
-        fork_entries(w, e0, x);
+    int n = 0;  // of the row
+    rows([&](int r, int e0, const int (&x)[kForkBatch], const int (&d)[kForkBatch]) {
+      int left[kForkBatch], mine[kForkBatch];
 #pragma unroll
-        for (int k = 0; k < kForkBatch; ++k) {
-          const bool drops = x[k] >= 0 && fork_delta(w, e0 + 32 * k, c, solo) < 0;
-          left[k] = drops ? holders(x[k]) : 0;
-          mine[k] = drops ? __ldcg(p.claim + x[k]) : -1;
-        }
-#pragma unroll
-        for (int k = 0; k < kForkBatch; ++k) {
-          const unsigned hit =
-              __ballot_sync(kFullMask, left[k] == -1 && mine[k] == r * W + e0 + 32 * k);
-          n += __popc(hit);
-          if (lane == 0 && (e0 >> 5) + k < words) p.gone[(int64_t)r * words + (e0 >> 5) + k] = hit;
-        }
+      for (int k = 0; k < kForkBatch; ++k) {
+        left[k] = d[k] < 0 ? holders(x[k]) : 0;
+        mine[k] = d[k] < 0 ? __ldcg(p.claim + x[k]) : -1;
       }
+#pragma unroll
+      for (int k = 0; k < kForkBatch; ++k) {
+        const unsigned hit = __ballot_sync(kFullMask, left[k] == -1 && mine[k] == r * W + e0 + 32 * k);
+        n += __popc(hit);
+        if (lane == 0 && (e0 >> 5) + k < words) p.gone[(int64_t)r * words + (e0 >> 5) + k] = hit;
+      }
+    }, [&](int r) {
       if (lane == 0) p.back[r] = n;
-    }
+      n = 0;
+    });
   }
   barrier();
 
@@ -286,22 +310,27 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
 #pragma unroll
         for (int k = 0; k < kForkBatch; ++k)
           if (d[k]) atomicAdd(p.extra_out + x[k], -d[k]);
-      });
+      }, nothing);
     }
+    struct Back {
+      int len, at, n;
+    };
     if (ok)
-      for (int r = r0 + warp; r < r1; r += kForkThreads / 32) {
-        const ForkRow w = fork_row(p, r);
-        int64_t at = count + before + p.first[r];
-        for (int e0 = 0; e0 < w.have; e0 += 32) {
-          const unsigned hit = p.gone[(int64_t)r * words + (e0 >> 5)];
-          if (hit >> lane & 1u) {
-            const int x = w.entries[e0 + lane];
-            p.ring[ring_at(at + __popc(hit & ((1u << lane) - 1u)))] = x;
-            p.extra_out[x] = 0;
-          }
-          at += __popc(hit);
-        }
-      }
+      groups([&](int r) { return Back{p.lens[r], p.first[r], p.back[r]}; },
+             [&](int r, int i, const Back& m) {
+               if (__shfl_sync(kFullMask, m.n, i) == 0) return;
+               const ForkRow w = fork_row(p, r, __shfl_sync(kFullMask, m.len, i));
+               int64_t at = count + before + __shfl_sync(kFullMask, m.at, i);
+               for (int e0 = 0; e0 < w.have; e0 += 32) {
+                 const unsigned hit = p.gone[(int64_t)r * words + (e0 >> 5)];
+                 if (hit >> lane & 1u) {
+                   const int x = w.entries[e0 + lane];
+                   p.ring[ring_at(at + __popc(hit & ((1u << lane) - 1u)))] = x;
+                   p.extra_out[x] = 0;
+                 }
+                 at += __popc(hit);
+               }
+             });
   }
 
   // ---- the next rows, or, after any error, empty ones -------------------------------
@@ -314,33 +343,34 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
     p.state_out[0] = ok ? ring_at(taken) : head;
     p.state_out[1] = ok ? count - taken + given : count;
   }
-  for (int s = all >> 5; s < S; s += threads >> 5) {
-    const int r = ok ? p.parents[s] : -1;
-    ForkRow w{0, 0, -1, 0, 0, nullptr};
-    bool copies = false;
-    int fresh = -1;
-    if (r >= 0) {
-      w = fork_row(p, r);
-      // (one fresh block more after this row than before it)
-      const int at = __ldcg(p.fresh + s);
-      copies = (s + 1 < S ? __ldcg(p.fresh + s + 1) : taken) > at;
-      if (copies) {
+  const int warps = threads >> 5, out_group = min(32, max(1, (S + warps - 1) / warps));
+  for (int g0 = (all >> 5) * out_group; g0 < S; g0 += warps * out_group) {
+    const int n = min(out_group, S - g0), s = g0 + min(lane, n - 1);
+    const int parent = ok ? p.parents[s] : -1;
+    int len = 0, fresh = -1;
+    if (parent >= 0) {
+      len = p.lens[parent];
+      // (a row that copies has one fresh block more behind it than before it)
+      const int at = __ldcg(p.fresh + s), then = s + 1 < S ? __ldcg(p.fresh + s + 1) : taken;
+      if (then > at) {
         fresh = p.ring[ring_at(at)];
-        if (lane == 0) {
-          p.from[at] = w.entries[w.partial];
-          p.to[at] = fresh;
-        }
+        p.from[at] = p.tables[(int64_t)parent * W + len / b];
+        p.to[at] = fresh;
       }
     }
-    if (lane == 0) p.lens_out[s] = w.len;
-    int32_t* const out = p.tables_out + (int64_t)s * W;
-    for (int e0 = lane; e0 < W; e0 += B) {
-      int x[kForkBatch];
-      fork_entries(w, e0, x);
+    p.lens_out[s] = len;  // (equal lanes write the same)
+    for (int i = 0; i < n; ++i) {
+      const int r = __shfl_sync(kFullMask, parent, i), f = __shfl_sync(kFullMask, fresh, i);
+      const ForkRow w = fork_row(p, max(r, 0), __shfl_sync(kFullMask, len, i));  // (none: empty)
+      int32_t* const out = p.tables_out + (int64_t)(g0 + i) * W;
+      for (int e0 = lane; e0 < W; e0 += B) {
+        int x[kForkBatch];
+        fork_entries(w, e0, x);
 #pragma unroll
-      for (int k = 0; k < kForkBatch; ++k) {
-        const int e = e0 + 32 * k;
-        if (e < W) out[e] = copies && e == w.partial ? fresh : fork_keeps(w, e) ? x[k] : -1;
+        for (int k = 0; k < kForkBatch; ++k) {
+          const int e = e0 + 32 * k;
+          if (e < W) out[e] = f >= 0 && e == w.partial ? f : fork_keeps(w, e) ? x[k] : -1;
+        }
       }
     }
   }
