@@ -8,7 +8,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "cross_tc.cuh"
+#include "window_tc.cuh"
 #include "decode_launch.cuh"
 #include "prefill.cuh"
 
@@ -20,8 +20,8 @@ int pkv_launch_cross_tc_fp8(const pkv::CrossParams&, int, int, bool, const pkv::
                             cudaStream_t);
 int pkv_launch_cross(const pkv::CrossParams& p, int dtype, int io_dtype, int num_seqs, int dim,
                      cudaStream_t stream);
-int pkv_launch_window_tc_f16(const pkv::WindowParams&, int, int, const pkv::CrossMaps&, cudaStream_t);
-int pkv_launch_window_tc_bf16(const pkv::WindowParams&, int, int, const pkv::CrossMaps&, cudaStream_t);
+int pkv_launch_window_tc_f16(const pkv::WindowParams&, int, const pkv::WindowMaps&, int, cudaStream_t);
+int pkv_launch_window_tc_bf16(const pkv::WindowParams&, int, const pkv::WindowMaps&, int, cudaStream_t);
 int pkv_launch_window_tc_fp8(const pkv::WindowParams&, int, int, bool, const pkv::CrossMaps&,
                              cudaStream_t);
 int pkv_launch_window_token(const pkv::WindowParams& p, int dtype, int io_dtype, int num_seqs, int dim,
@@ -685,6 +685,23 @@ bool encode_page_map(CUtensorMap* map, const pkv_cache* c, void* base) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Describes the queries [total][H][D] to the windowed kernel, read 64 elements of
+// a KV head's G heads of 128 / G queries at a time: the rows of a tile.
+bool encode_query_map(CUtensorMap* map, const pkv_cache* c, const void* q, int64_t total, int heads) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const int G = heads / c->num_kv_heads;
+  const cuuint64_t row = (cuuint64_t)c->head_dim * 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)c->head_dim, (cuuint64_t)heads, (cuuint64_t)total};
+  const cuuint64_t strides[2] = {row, heads * row};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, c->dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             3, const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Bytes of the (m, l) pairs and where the partial outputs start.
 WsLayout cross_workspace(int64_t total_queries, int num_heads, int head_dim, int parts) {
   WsLayout w{};
@@ -833,6 +850,7 @@ namespace {
 // chunks as cross attention.
 struct WindowPlan {
   bool token, tc, wide;
+  pkv::WindowParams::Unit unit;
   int parts, part, tile_queries;
 };
 
@@ -856,6 +874,7 @@ WindowPlan window_plan(const pkv_cache* c, int num_seqs, int num_heads, int max_
                                                     ((int64_t)window + 14) / 16 + 1));
   if (max_queries == 1 && c->dtype != PKV_F32) {
     w.token = true;
+    w.unit = pkv::WindowParams::kChunks;
     w.tile_queries = 1;
     const int64_t want = token_parts(c, num_seqs, chunks);
     const int64_t per = (chunks + want - 1) / want;
@@ -866,11 +885,14 @@ WindowPlan window_plan(const pkv_cache* c, int num_seqs, int num_heads, int max_
   w.tc = tensor_cores(c);
   w.wide = w.tc && wide_rows(c, (int64_t)max_queries * G);
   w.tile_queries = (!w.tc ? pkv::kCrossRows : w.wide ? 256 : 128) / G;
-  // The most positions that a row tile walks, in tiles of 64.
-  const int64_t whole = ((int64_t)max_len + 63) / 64;
-  const int64_t most = (std::min<int64_t>(sinks, max_len) + 63) / 64 +
-                       ((int64_t)window + std::min(w.tile_queries, max_queries) + 61) / 64 + 1;
-  const int span = (int)std::min(whole, most) * 64;
+  // The most keys that a row tile walks, in tiles of 64.
+  const bool packed = w.tc && c->dtype != PKV_FP8_E4M3;
+  w.unit = packed ? pkv::WindowParams::kPacked : pkv::WindowParams::kTiles;
+  const int64_t page = packed ? std::min(c->block_size, 64) : 64;
+  const int64_t whole = ((int64_t)max_len + page - 1) / page;
+  const int64_t most = (std::min<int64_t>(sinks, max_len) + page - 1) / page +
+                       ((int64_t)window + std::min(w.tile_queries, max_queries) + page - 3) / page + 1;
+  const int span = (int)((std::min(whole, most) * page + 63) / 64) * 64;
   const CrossPlan sp = cross_plan(c, num_seqs, num_heads, max_queries, span);
   w.parts = sp.parts;
   w.part = sp.part;
@@ -910,7 +932,8 @@ int paged_attention_window(const pkv_cache* cache, const void* q, int64_t total_
   p.window = window;
   p.sinks = sinks;
   p.tile_queries = w.tile_queries;
-  p.token = w.token;
+  p.unit = w.unit;
+  p.num_seqs = num_seqs;
   const int wrc = cross_workspace_params(&p, cache, w.parts, w.part, workspace, workspace_bytes);
   if (wrc) return wrc;
   if (w.token) {
@@ -928,8 +951,12 @@ int paged_attention_window(const pkv_cache* cache, const void* q, int64_t total_
   if (mrc) return mrc;
   if (cache->dtype == PKV_FP8_E4M3)
     return pkv_launch_window_tc_fp8(p, cache->io_dtype, num_seqs, w.wide, maps, stream);
+  pkv::WindowMaps wm;
+  wm.k = maps.k;
+  wm.v = maps.v;
+  if (!encode_query_map(&wm.q, cache, q, total_queries, num_heads)) return PKV_ERR_CUDA;
   return (cache->dtype == PKV_F16 ? pkv_launch_window_tc_f16 : pkv_launch_window_tc_bf16)(
-      p, num_seqs, cache->head_dim, maps, stream);
+      p, cache->head_dim, wm, sm_count(), stream);
 }
 
 int paged_block_copy(const pkv_cache* cache, const int64_t* src_dst_pairs, int64_t num_pairs,

@@ -53,7 +53,10 @@ struct CrossParams {
 struct WindowParams : CrossParams {
   int window, sinks;
   int tile_queries;         // queries in a row tile
-  bool token;               // single tokens: parts are of chunks of 16 positions
+  int num_seqs;
+  // What parts are counted in: tiles of 64 positions; for single tokens chunks of
+  // 16; or tiles of 64 packed keys (whole pages of the sinks and the window).
+  enum Unit { kTiles, kChunks, kPacked } unit;
 };
 
 // Whether the query at position p sees position t.
@@ -110,9 +113,9 @@ __device__ __forceinline__ CrossSeq cross_seq(const CrossParams& p, int s) {
   return c;
 }
 
-// L is the sequence's length with its queries; parts are of the tiles of 64 (or
-// 16) that a row tile walks (where it walks fewer than the sequence's other row
-// tiles its last parts are empty).
+// L is the sequence's length with its queries; parts are of the tiles (p.unit)
+// that a row tile walks (where it walks fewer than the sequence's other row tiles
+// its last parts are empty).
 __device__ __forceinline__ CrossSeq cross_seq(const WindowParams& p, int s) {
   CrossSeq c = cross_seq(static_cast<const CrossParams&>(p), s);
   if (c.Q > c.L) c.bits = PKV_DEV_SEQ_LEN;
@@ -121,16 +124,20 @@ __device__ __forceinline__ CrossSeq cross_seq(const WindowParams& p, int s) {
     c.L = 0;
     return c;
   }
-  if (p.token) {
+  if (p.unit == WindowParams::kChunks) {
     c.parts = (WindowSpan<16>(p, c.L - 1, c.L - 1).tiles + p.part / 16 - 1) / (p.part / 16);
     return c;
   }
-  int tiles = WindowSpan<64>(p, c.L - c.Q, c.L - 1).tiles;
+  const int page = p.unit == WindowParams::kPacked ? min(p.block_size, 64) : 64;
+  const int w0 = max(0, c.L - c.Q - p.window + 1), s0 = min(p.sinks, w0);
+  const int head = (s0 + page - 1) / page;
+  int pages = (c.L - 1) / page + 1 - max(0, w0 / page - head);
   if (c.Q > p.tile_queries) {
-    const int64_t most = (min(p.sinks, c.L) + 63) / 64 +
-                         ((int64_t)p.window + p.tile_queries + 61) / 64 + 1;
-    tiles = (int)min((int64_t)tiles, most);
+    const int64_t most = (min(p.sinks, c.L) + page - 1) / page +
+                         ((int64_t)p.window + p.tile_queries + page - 3) / page + 1;
+    pages = (int)min((int64_t)pages, most);
   }
+  const int tiles = (pages + 64 / page - 1) / (64 / page);
   c.parts = (tiles + p.part / 64 - 1) / (p.part / 64);
   return c;
 }

@@ -1,9 +1,9 @@
 // Windowed attention on tensor cores: instantiations for bf16 pools.
-#include "cross_tc.cuh"
+#include "window_tc.cuh"
 
-int pkv_launch_window_tc_bf16(const pkv::WindowParams& p, int num_seqs, int dim,
-                             const pkv::CrossMaps& maps, cudaStream_t stream) {
+int pkv_launch_window_tc_bf16(const pkv::WindowParams& p, int dim, const pkv::WindowMaps& maps, int sms,
+                             cudaStream_t stream) {
   using T = __nv_bfloat16;
-  return dim == 64 ? pkv::launch_cross_tc<T, 64, 1, false>(p, num_seqs, maps, stream)
-                   : pkv::launch_cross_tc<T, 128, 1, false>(p, num_seqs, maps, stream);
+  return dim == 64 ? pkv::launch_window_tc<T, 64>(p, maps, sms, stream)
+                   : pkv::launch_window_tc<T, 128>(p, maps, sms, stream);
 }
