@@ -151,9 +151,16 @@ __device__ __forceinline__ bool window_row_bad(const WindowParams& p, const Cros
   const int head = (span.s0 + b - 1) / b, gap = max(0, span.w0 / b - head);
   const int n = span.last / b + 1 - gap;
   bool bad = false;
-  for (int i = thread; i < n; i += threads) {
-    const int e = trow[i < head ? i : i + gap];
-    bad |= e < 0 || (int64_t)e >= p.num_blocks;
+  constexpr int U = 4;  // loads in flight
+  for (int i0 = thread; i0 < n; i0 += U * threads) {
+    int e[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = i0 + k * threads;
+      e[k] = i < n ? trow[i < head ? i : i + gap] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) bad |= e[k] < 0 || (int64_t)e[k] >= p.num_blocks;
   }
   return bad;
 }

@@ -11,8 +11,9 @@
 // position, are masked row by row (about 3 of 19 with a window of 1024).  There
 // a value that is not finite must reach the rows that see it and no other,
 // which a product with weights of zero does not do: edge tiles are multiplied
-// with such values cleared, and where there were any, every row that sees them
-// adds them to its O afterwards, read again from the pool.
+// with such values cleared by the converters, and where there were any, every row
+// that sees them adds them to its O afterwards, read again from the pool.  (FP8
+// pools only: window_tc.cuh serves the others.)
 // Roles:
 //   softmax warps, four per row tile  a thread per row (= tensor-memory lane):
 //        the S row to registers, running maximum and sum, P over S's columns;
@@ -96,12 +97,12 @@ struct CrossTcCfg {
   static constexpr int kVRingOff = kKRingOff + kKSlots * kTileBytes;
   static constexpr int kRawOff = kVRingOff + kVSlots * kTileBytes;  // K, then V
   static constexpr int kBarOff = kRawOff + 2 * kRawSlots * kRawBytes;
-  static constexpr int kNumBars = 2 * kSlots + 4 * kRawSlots + QT * (2 * kBufs + 3) + 3;
+  static constexpr int kNumBars = 2 * kSlots + 4 * kRawSlots + QT * (2 * kBufs + 3) + 2;
   static constexpr int kTmemOff = kBarOff + kNumBars * 8;
   static constexpr int kFlagOff = kTmemOff + 4;
-  static constexpr int kDirtyOff = kTmemOff + 8;            // with a window; FP8: 2 a V slot
-  static constexpr int kSpanOff = kDirtyOff + (KV8 ? 8 * kVSlots : 8);  // with a window: WindowEdges
-  static constexpr int kSmemBytes = kSpanOff + 24;
+  static constexpr int kDirtyOff = kTmemOff + 8;            // FP8 with a window: 2 a V slot
+  static constexpr int kSpanOff = kDirtyOff + (KV8 ? 8 * kVSlots : 0);  // and WindowEdges
+  static constexpr int kSmemBytes = kSpanOff + (KV8 ? 24 : 8);
   static constexpr uint32_t kTileCols = 256;
   static constexpr uint32_t kTmemCols = QT * kTileCols;
   static constexpr uint32_t kOCol = kBufs * kKeys;
@@ -341,32 +342,6 @@ __device__ __forceinline__ void clear_tail(unsigned char* v, int valid, int bloc
   fence_proxy_async_smem();
 }
 
-// A value tile at an edge of the window: rows outside `mask` (nobody's) become
-// zeros, elements that are not finite too; returns whether this thread met one
-// in the mask.
-template <typename T, int D, int KEYS>
-__device__ __forceinline__ bool clear_edge(unsigned char* v, uint64_t mask, int thread, int threads) {
-  bool met = false;
-  for (int e = thread; e < KEYS * (D / 8); e += threads) {
-    const int row = e / (D / 8), ch = e % (D / 8);
-    uint4* const at = reinterpret_cast<uint4*>(v + (row >> 3) * (D / 64 * 1024) + (ch >> 3) * 1024 +
-                                               (row & 7) * 128 + ((ch & 7) ^ (row & 7)) * 16);
-    if (!(mask >> row & 1ull)) {
-      *at = make_uint4(0u, 0u, 0u, 0u);
-      continue;
-    }
-    const uint4 x = *at;
-    const uint4 n = make_uint4(not_finite<T>(x.x), not_finite<T>(x.y), not_finite<T>(x.z),
-                               not_finite<T>(x.w));
-    if (n.x | n.y | n.z | n.w) {
-      met = true;
-      *at = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
-    }
-  }
-  fence_proxy_async_smem();
-  return met;
-}
-
 // One page (or the part of it in a tile) of a pool, see kGroupBytes: coordinates
 // are the first group of 8 rows and the page, block * kv_heads + kv_head.
 __device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, int group,
@@ -431,6 +406,7 @@ __global__ void __launch_bounds__(CrossTcCfg<T, D, QT, KV8>::kThreads, QT == 2 ?
 cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tmk,
                 const __grid_constant__ CUtensorMap tmv) {
   constexpr bool WIN = std::is_same<P, WindowParams>::value;
+  static_assert(!WIN || KV8, "16-bit pools with a window: window_tc_kernel");
   using Cfg = CrossTcCfg<T, D, QT, KV8>;
   using Op = typename Cfg::Op;
   constexpr int KT = Cfg::kKeys, NS = Cfg::kBufs;
@@ -515,13 +491,11 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
   const uint32_t q_full = bar0 + 8u * (B1 + 2 * QT * NS + 2 * QT);
   auto drain = [&](int t) { return q_full + 8u * (1 + t); };
   const uint32_t checked = q_full + 8u * (1 + QT);  // the table row
-  const uint32_t cleared = checked + 8u;  // an edge tile's values
   auto tile_warps = [&](int t) {  // softmax warps with rows of row tile t
     return min(4, max(0, (nr - t * 128 + 31) / 32));
   };
-  // Values of an edge tile were cleared.  FP8: a word of each converter warp for
-  // each slot, true or false; else two words for edge tiles in turn, the number
-  // of the last tile that had some.
+  // With a window: values of an edge tile were cleared, a word of each converter
+  // warp for each slot.
   [[maybe_unused]] volatile int* dirty = reinterpret_cast<volatile int*>(smem + Cfg::kDirtyOff);
   [[maybe_unused]] volatile WindowEdges* edges =
       reinterpret_cast<volatile WindowEdges*>(smem + Cfg::kSpanOff);
@@ -551,10 +525,8 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
     }
     mbar_init(q_full, (tile_warps(0) + (QT > 1 ? tile_warps(QT - 1) : 0)) * 32);
     mbar_init(checked, 32);
-    mbar_init(cleared, max(1, tile_warps(0)) * 32);
     fence_mbar_init();
     *reinterpret_cast<int*>(smem + Cfg::kFlagOff) = 0;
-    if constexpr (!KV8) dirty[0] = dirty[1] = -1;
     if constexpr (WIN) {
       edges->first = base_pos + r0 / G;
       edges->last = span.last;
@@ -753,11 +725,9 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     // With a window: the row's position, the last edge tile with values that are
-    // not finite (-1: none waits) and the keys whose weight is 0 in it, and the
-    // number of edge tiles.
+    // not finite (-1: none waits).
     [[maybe_unused]] const int pos = base_pos + (r0 + min(r, nr - 1)) / G;
-    [[maybe_unused]] int odd = -1, met_edges = 0;
-    [[maybe_unused]] uint64_t odd_zero = 0;
+    [[maybe_unused]] int odd = -1;
     // Adds that tile's cleared values to O, once its product is in.
     [[maybe_unused]] auto add_odd = [&] {
       const int bs = b;
@@ -779,18 +749,11 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
           if ((unsigned)e >= (unsigned)p.num_blocks) continue;
           const int64_t at =
               ((((int64_t)e * p.kv_heads + kvh) * bs + (t0 + k) % bs) * D + q * 32);
-          const bool sees = sees_keys >> k & 1ull, zero = odd_zero >> k & 1ull;
+          const bool sees = sees_keys >> k & 1ull;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            float x;
-            if constexpr (KV8) {
-              const unsigned char code = static_cast<const unsigned char*>(p.v_cache)[at + i];
-              x = (code & 0x7F) == 0x7F ? NAN : 0.f;
-            } else {
-              x = static_cast<float>(static_cast<const T*>(p.v_cache)[at + i]);
-            }
-            if (sees && !isfinite(x))
-              o[i] = __float_as_uint(__uint_as_float(o[i]) + (zero ? NAN : x));
+            const unsigned char code = static_cast<const unsigned char*>(p.v_cache)[at + i];
+            if (sees && (code & 0x7F) == 0x7F) o[i] = __float_as_uint(NAN);
           }
         }
         tmem_st32(base + Cfg::kOCol + q * 32, o);
@@ -867,7 +830,6 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
       l += sx.x + sx.y;
       tmem_st32(sp, pk);
       [[maybe_unused]] bool met = false;
-      [[maybe_unused]] uint64_t weightless = 0;
       if constexpr (WIN) {
         if (edge) {
           ok = mbar_wait(v_full(j % NV), (uint32_t)((j / NV) & 1));
@@ -875,31 +837,7 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
             ok = false;
             break;
           }
-          if constexpr (KV8) {
-            met = dirty[2 * (j % NV)] != 0 || dirty[2 * (j % NV) + 1] != 0;
-          } else {
-            met = clear_edge<T, D, KT>(smem + Cfg::kVRingOff + (j % NV) * Cfg::kTileBytes,
-                                       edges->seen(edges->pos<KT>(tile0 + j)), rr,
-                                       32 * tile_warps(t));
-            if (met) dirty[met_edges & 1] = j;
-            mbar_arrive(cleared);
-            ok = mbar_wait(cleared, (uint32_t)(met_edges & 1));
-            if (__any_sync(kFullMask, !ok)) {
-              ok = false;
-              break;
-            }
-            met = dirty[met_edges & 1] == j;
-            ++met_edges;
-          }
-          if (met) {  // (P as it was stored: its registers are not kept for this)
-            uint32_t pw[KT / 2];
-            tmem_ld32(sp, pw);
-#pragma unroll
-            for (int k = 0; k < KT; k += 2) {
-              if (!(pw[k / 2] & 0x7FFFu)) weightless |= 1ull << k;
-              if (!(pw[k / 2] & 0x7FFF0000u)) weightless |= 2ull << k;
-            }
-          }
+          met = dirty[2 * (j % NV)] != 0 || dirty[2 * (j % NV) + 1] != 0;
         }
       } else if (!KV8 && hi - lo - j * KT < KT) {  // (the last tile)
         ok = mbar_wait(v_full(j % NV), (uint32_t)((j / NV) & 1));
@@ -932,10 +870,7 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
       }
       if constexpr (WIN) {
         if (odd >= 0) add_odd();
-        if (met) {
-          odd = j;
-          odd_zero = weightless;
-        }
+        if (met) odd = j;
       }
       tc_fence_before();
       mbar_arrive(p_full(t, j % NS));

@@ -48,6 +48,20 @@ struct WindowItem {
   int w0, s0;             // seen by some row: t < s0, and w0 <= t <= last
   int key0;               // first packed key (of the item's part)
   int head, skip;         // packed keys of the sinks; positions left out behind them
+  // Tiles in which some row does not see some key: those before the window's last
+  // start, unless the sinks cover them, and those behind the first row.
+  int left0, left1, right;
+};
+
+// Whether a tile is one of them (looked up once an item: 110 us of 383 went into
+// finding it out in every tile).
+struct WindowEdge {
+  int left0, left1, right;
+  __device__ __forceinline__ explicit WindowEdge(const volatile WindowItem* it)
+      : left0(it->left0), left1(it->left1), right(it->right) {}
+  __device__ __forceinline__ bool operator()(int j) const {
+    return (j >= left0 && j < left1) || j >= right;
+  }
 };
 
 // Packed key v is position v, or v + skip behind the sinks' pages.
@@ -77,31 +91,73 @@ struct WindowKeys {
     const uint64_t head = below(near);
     return (of(t0) & head) | (of(t1) & ~head);
   }
-  // Whether some row does not see some key.
-  __device__ __forceinline__ bool edge(const WindowParams& p, const volatile WindowItem* it) const {
-    if (near > 0 && near < 64) return true;
-    const int t = near ? t0 : t1;
-    return t + 63 > it->first || (t + 63 >= p.sinks && t <= it->last - p.window);
-  }
 };
 
 template <typename T, int D>
 struct WindowTcCfg : CrossTcCfg<T, D, 1, false> {
   using Base = CrossTcCfg<T, D, 1, false>;
   static constexpr int kItems = 4;                          // ring of items
-  static constexpr int kDirty = 8;                          // tiles with flags, more than V slots
+  static constexpr int kEdges = 8;                          // edge tiles in flight, more than V slots
   // softmax 0-3, K and Q 4, V 5, MMA 6, scout 7
   static constexpr int kScoutWarp = 7, kThreads = 256;
-  static constexpr int kBars = 2 * Base::kSlots + 2 * Base::kBufs + Base::kVSlots + 4 + 3 * kItems;
+  static constexpr int kBars = 2 * Base::kSlots + 2 * Base::kBufs + kEdges + 6 + 3 * kItems;
   static constexpr int kTmemOff = Base::kBarOff + kBars * 8;
+  static constexpr int kIssuedOff = kTmemOff + 4;
   static constexpr int kDirtyOff = kTmemOff + 8;
-  static constexpr int kBadOff = kDirtyOff + 4 * kDirty;
+  static constexpr int kBadOff = kDirtyOff + 4 * kEdges;
   static constexpr int kItemOff = kBadOff + 4 * kItems;
   static constexpr int kSmemBytes = kItemOff + kItems * (int)sizeof(WindowItem);
   static_assert(kSmemBytes <= 113 * 1024, "two blocks on an SM");
   static_assert(3 * kSmemBytes > 228 * 1024, "no more blocks than tensor memory serves");
-  static_assert(Base::kVSlots < kDirty, "a flag is read before its place is used again");
+  static_assert(Base::kVSlots < kEdges, "a flag is read before its place is used again");
 };
+
+// A tile of 64 values at an edge of the window, by one warp: rows outside `mask`
+// (nobody's) become zeros, elements that are not finite too; returns whether there
+// were any of these in the mask.  Eight loads in flight; two elements at a time
+// are not finite if the addition to their exponents carries.
+template <typename T, int D>
+__device__ __forceinline__ bool clear_edge(unsigned char* v, uint64_t mask, int lane) {
+  constexpr uint32_t kExp = std::is_same<T, __nv_bfloat16>::value ? 0x7F807F80u : 0x7C007C00u;
+  constexpr uint32_t kOne = std::is_same<T, __nv_bfloat16>::value ? 0x00800080u : 0x04000400u;
+  constexpr int kRowUnits = D / 8, kUnits = 64 * kRowUnits / 32, kBatch = 8;
+  bool met = false;
+#pragma unroll 1
+  for (int u0 = 0; u0 < kUnits; u0 += kBatch) {
+    uint4 x[kBatch];
+    uint4* at[kBatch];
+    uint32_t odd = 0;
+    bool hide = false;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int e = (u0 + i) * 32 + lane, row = e / kRowUnits, ch = e % kRowUnits;
+      at[i] = reinterpret_cast<uint4*>(v + (row >> 3) * (D / 64 * 1024) + (ch >> 3) * 1024 +
+                                       (row & 7) * 128 + ((ch & 7) ^ (row & 7)) * 16);
+      x[i] = *at[i];
+      hide |= !(mask >> row & 1ull);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      odd |= ((x[i].x & kExp) + kOne) | ((x[i].y & kExp) + kOne) | ((x[i].z & kExp) + kOne) |
+             ((x[i].w & kExp) + kOne);
+    if (!hide && !(odd & 0x80008000u)) continue;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (!(mask >> (((u0 + i) * 32 + lane) / kRowUnits) & 1ull)) {
+        *at[i] = make_uint4(0u, 0u, 0u, 0u);
+        continue;
+      }
+      const uint4 n = make_uint4(not_finite<T>(x[i].x), not_finite<T>(x[i].y), not_finite<T>(x[i].z),
+                                 not_finite<T>(x[i].w));
+      if (n.x | n.y | n.z | n.w) {
+        met = true;
+        *at[i] = make_uint4(x[i].x & ~n.x, x[i].y & ~n.y, x[i].z & ~n.z, x[i].w & ~n.w);
+      }
+    }
+  }
+  fence_proxy_async_smem();
+  return __any_sync(kFullMask, met);
+}
 
 struct WindowMaps {
   CUtensorMap k, v, q;
@@ -146,14 +202,18 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
   const uint32_t o_done = bar0 + 8u * (B1 + 2 * NS);  // P.V of a tile is done
   const uint32_t q_full = o_done + 8u, q_empty = o_done + 16u;
   const uint32_t drained = o_done + 24u;
-  // The scout is done with the tile of a V slot.
-  auto v_clear = [&](int i) { return o_done + 32u + 8u * i; };
+  // The scout is done with an edge tile (of every kEdges-th).
+  const uint32_t flagged = o_done + 32u;  // an edge tile's flag is there
+  const uint32_t q_signed = o_done + 40u;
+  auto v_clear = [&](int i) { return o_done + 48u + 8u * i; };
   // The ring of items: numbers there; table checked; rows written.
-  auto ready = [&](int i) { return o_done + 32u + 8u * (NV + i); };
-  auto checked = [&](int i) { return o_done + 32u + 8u * (NV + NI + i); };
-  auto written = [&](int i) { return o_done + 32u + 8u * (NV + 2 * NI + i); };
+  auto ready = [&](int i) { return o_done + 48u + 8u * (Cfg::kEdges + i); };
+  auto checked = [&](int i) { return o_done + 48u + 8u * (Cfg::kEdges + NI + i); };
+  auto written = [&](int i) { return o_done + 48u + 8u * (Cfg::kEdges + 2 * NI + i); };
   uint32_t* const slot_addr = reinterpret_cast<uint32_t*>(smem + Cfg::kTmemOff);
-  // The last tile, of every kDirty-th, that had values cleared.
+  // Tiles of values whose copies have been issued.
+  volatile int* const v_issued = reinterpret_cast<volatile int*>(smem + Cfg::kIssuedOff);
+  // The last edge tile, of every kEdges-th, that had values cleared.
   volatile int* const dirty = reinterpret_cast<volatile int*>(smem + Cfg::kDirtyOff);
   volatile int* const bad = reinterpret_cast<volatile int*>(smem + Cfg::kBadOff);
   volatile WindowItem* const items = reinterpret_cast<volatile WindowItem*>(smem + Cfg::kItemOff);
@@ -164,8 +224,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
     }
     for (int i = 0; i < NV; ++i) {
       mbar_init(v_full(i), 1);
-      mbar_init(v_empty(i), 2);  // its product is done, and the scout is
-      mbar_init(v_clear(i), 1);
+      mbar_init(v_empty(i), 1);
     }
     for (int i = 0; i < NS; ++i) {
       mbar_init(s_full(i), 1);
@@ -175,13 +234,17 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(drained, 1);
+    mbar_init(flagged, 1);
+    mbar_init(q_signed, 1);
     for (int i = 0; i < NI; ++i) {
       mbar_init(ready(i), 1);
       mbar_init(checked(i), 1);
       mbar_init(written(i), 128);
     }
+    for (int i = 0; i < Cfg::kEdges; ++i) mbar_init(v_clear(i), 1);
     fence_mbar_init();
-    for (int i = 0; i < Cfg::kDirty; ++i) dirty[i] = -1;
+    for (int i = 0; i < Cfg::kEdges; ++i) dirty[i] = -1;
+    *v_issued = 0;
   }
   if (warp == Cfg::kMmaWarp) {
     tmem_alloc(smem_addr(slot_addr), Cfg::kTmemCols);
@@ -198,34 +261,39 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
     const int row_tiles = (int)(((int64_t)p.max_queries * G + 127) / 128);
     const int groups = p.num_seqs * p.kv_heads;                 // (sequence, KV head)
     const int64_t total = (int64_t)p.parts * groups * row_tiles;
-    int n = 0, tiles = 0;  // items and tiles so far
+    int n = 0, tiles = 0, edges = 0;  // items, tiles and edge tiles so far
     RingPos<NV> va;
     int64_t idx = blockIdx.x;
     bool ok = true;
-    // The values of item i's tiles.  Every tile is waited for, edge or not, and its
-    // slot is not filled again before: no barrier is ever a round ahead of a wait.
+    // The values of item i's edge tiles.  (A slot's barrier is waited for once the
+    // tile's copies are issued: before, it may be a round behind.)
     auto look_over = [&](int i) {
       if (i < 0) return;
       const volatile WindowItem* const it = items + i % NI;
       const int count = it->tiles;
+      const WindowEdge edge(it);
       for (int j = 0; j < count; ++j, ++tiles, va.next()) {
-        ok = mbar_wait(v_full(va.slot), va.phase);
+        if (!edge(j)) continue;
+        const uint64_t since = global_ns();
+        while (ok && *v_issued <= tiles) {
+          __nanosleep(100);
+          ok = global_ns() - since <= kWaitLimitNs;
+        }
+        ok = ok && mbar_wait(v_full(va.slot), va.phase);
         if (__any_sync(kFullMask, !ok)) {
           failed = true;
           ok = false;
           break;
         }
         const WindowKeys keys(it, j);
-        if (keys.edge(p, it)) {
-          const bool met = clear_edge<T, D, KT>(smem + Cfg::kVRingOff + va.slot * Cfg::kTileBytes,
-                                                keys.seen(it), lane, 32);
-          if (__any_sync(kFullMask, met) && lane == 0) dirty[tiles % Cfg::kDirty] = tiles;
+        const bool met = clear_edge<T, D>(smem + Cfg::kVRingOff + va.slot * Cfg::kTileBytes,
+                                          keys.seen(it), lane);
+        if (lane == 0) {
+          if (met) dirty[edges % Cfg::kEdges] = edges;
+          mbar_arrive(v_clear(edges % Cfg::kEdges));
         }
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(v_clear(va.slot));
-          mbar_arrive(v_empty(va.slot));
-        }
+        ++edges;
       }
     };
     while (ok) {
@@ -271,6 +339,14 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         it.key0 = it.part * p.part;
         const int keys = (it.last / page + 1) * page - it.skip - it.key0;
         it.tiles = (min(keys, p.part) + KT - 1) / KT;
+        // A tile starts at key v = key0 + 64 j, position v + skip (in the sinks'
+        // tiles, v): v + 64 <= sinks is seen by all; v + skip <= last - window is
+        // not; nor is v + skip + 63 > first.  (The sinks' tiles that pass for
+        // starting before the window's end are all of them but those.)
+        auto tiles_below = [&](int64_t v) { return (int)min((int64_t)1 << 30, max((int64_t)0, v >> 6)); };
+        it.left0 = tiles_below((int64_t)p.sinks - it.key0);
+        it.left1 = tiles_below((int64_t)it.last - p.window - it.skip - it.key0 + 64);
+        it.right = tiles_below((int64_t)it.first + 1 - it.skip - it.key0);
         if (keys > 0) break;
         // a row tile with fewer parts than the sequence: an empty part
         for (int r = 0; r < it.nr; ++r) {
@@ -307,6 +383,9 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
           mine->key0 = it.key0;
           mine->head = it.head;
           mine->skip = it.skip;
+          mine->left0 = it.left0;
+          mine->left1 = it.left1;
+          mine->right = it.right;
         }
         mbar_arrive(ready(at));
       }
@@ -322,6 +401,29 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         mbar_arrive(checked(at));
       }
       look_over(n - 1);
+      // A scale that is not positive goes into the queries (its sign, or zeros, so
+      // that no product of theirs is beyond float32): products then have a factor
+      // that is not negative, and the largest score the largest product.
+      if (ok && p.qscale <= 0.f) {
+        ok = mbar_wait(q_full, (uint32_t)(n & 1));
+        if (__any_sync(kFullMask, !ok)) {
+          failed = true;
+          ok = false;
+          break;
+        }
+        uint4* const q = reinterpret_cast<uint4*>(smem);
+        for (int e = lane; e < Cfg::kQBytes / 16; e += 32) {
+          const uint4 x = q[e];
+          q[e] = p.qscale < 0.f
+                     ? make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u,
+                                  x.w ^ 0x80008000u)
+                     : make_uint4(zero_pair<T>(x.x), zero_pair<T>(x.y), zero_pair<T>(x.z),
+                                  zero_pair<T>(x.w));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_signed);
+      }
       ++n;
       idx += gridDim.x;
     }
@@ -375,6 +477,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
           }
           const uint32_t fb = bars + 8u * slot;
           mbar_arrive_expect_tx(fb, Cfg::kTileBytes);
+          if (!key) *v_issued = issued + 1;
           const WindowKeys keys(it, j);
 #pragma unroll
           for (int x = 0; x < KT / 8; ++x) {
@@ -409,32 +512,12 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
       RingPos<NK> ka;
       RingPos<NV> va;
       bool ok = true;
-      // Scores: item sn, tile sj of s_tiles; -1 tiles: the items have ended.
-      int sn = 0, sj = 0, s_tiles = 0, made = 0;  // made: tiles with scores
-      auto scores = [&](bool wait) {  // false: not there yet, or no more
-        if (!ok || s_tiles < 0) return false;
-        if (sj == s_tiles) {
-          const int at = sn % NI;
-          const uint32_t par = (uint32_t)((sn / NI) & 1), qpar = (uint32_t)(sn & 1);
-          if (!wait && !mbar_test_wait(ready(at), par)) return false;
-          ok = mbar_wait(ready(at), par);
-          if (!ok) return false;
-          const int t = items[at].tiles;
-          if (t < 0) {
-            s_tiles = -1;
-            sj = 0;
-            return false;
-          }
-          if (!wait && !mbar_test_wait(q_full, qpar)) return false;
-          ok = mbar_wait(q_full, qpar);
-          if (!ok) return false;
-          s_tiles = t;
-          sj = 0;
-          ++sn;
-        }
-        if (!wait && !mbar_test_wait(k_full(ka.slot), ka.phase)) return false;
-        ok = mbar_wait(k_full(ka.slot), ka.phase);
-        if (!ok) return false;
+      // Scores run two tiles ahead of P.V, over the S that it has read.  left: tiles
+      // of the scores' item without scores, -1 when the items have ended.
+      int sn = 0, left = 0, made = 0;  // next item, and tiles with scores
+      auto scores = [&] {  // of the item's next tile
+        ok = ok && mbar_wait(k_full(ka.slot), ka.phase);
+        if (!ok) return;
         tc_fence_after();
         const uint64_t kb = kdesc + (uint64_t)((ka.slot * Cfg::kTileBytes) >> 4);
         const int buf = made & 1;
@@ -448,27 +531,59 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         tc_commit(k_empty(ka.slot));
         ka.next();
         ++made;
-        if (++sj == s_tiles) tc_commit(q_empty);
-        return true;
+        if (--left == 0) tc_commit(q_empty);
       };
-      int done = 0;  // tiles with P.V
+      // Goes to the next item once its queries are there; `wait` or not.
+      auto next_item = [&](bool wait) {
+        const int at = sn % NI;
+        const uint32_t par = (uint32_t)((sn / NI) & 1), qpar = (uint32_t)(sn & 1);
+        if (!wait && !mbar_test_wait(ready(at), par)) return;
+        ok = ok && mbar_wait(ready(at), par);
+        if (!ok) return;
+        const int t = items[at].tiles;
+        if (t < 0) {
+          left = -1;
+          return;
+        }
+        const uint32_t there = p.qscale > 0.f ? q_full : q_signed;
+        if (!wait && !mbar_test_wait(there, qpar)) return;
+        ok = mbar_wait(there, qpar);
+        if (!ok) return;
+        left = t;
+        ++sn;
+      };
+      int done = 0, edges = 0;  // tiles with P.V, edge tiles
       for (int n = 0; ok; ++n) {
         const volatile WindowItem* const it = items + n % NI;
         ok = mbar_wait(ready(n % NI), (uint32_t)((n / NI) & 1));
         if (!ok || it->tiles < 0) break;
         const int tiles = it->tiles;
+        const WindowEdge edge(it);
         for (int j = 0; j < tiles && ok; ++j) {
-          // Scores run two tiles ahead, over the S that P.V has read, and as soon as
-          // their keys (and queries) are there: looked for while P is waited for.
-          while (ok && made <= done) scores(true);
+          if (made == done) {  // the first tile of all, or of an item after a short one
+            if (left == 0) next_item(true);
+            scores();
+          }
+          if (left > 0 && made < done + NS) scores();
           const int buf = done & 1;
           const uint32_t par = (uint32_t)((done >> 1) & 1);
-          const uint64_t since = global_ns();
-          for (int spin = 1; ok && !mbar_test_wait(p_full(buf), par); ++spin) {
-            if (made < done + NS) scores(false);
-            if (!(spin & 255) && global_ns() - since > kWaitLimitNs) ok = false;
+          if (left != 0 || made == done + NS) {
+            ok = ok && mbar_wait(p_full(buf), par);
+          } else {
+            // The next item's first scores as soon as its queries are there.
+            const uint64_t since = global_ns();
+            while (ok && !mbar_test_wait(p_full(buf), par)) {
+              if (left == 0) next_item(false);
+              if (left > 0 && made < done + NS) scores();
+              if (global_ns() - since > kWaitLimitNs) ok = false;
+            }
           }
           ok = ok && mbar_wait(v_full(va.slot), va.phase);
+          if (ok && edge(j)) {
+            ok = mbar_wait(v_clear(edges % Cfg::kEdges), (uint32_t)((edges / Cfg::kEdges) & 1));
+            mbar_arrive(flagged);
+            ++edges;
+          }
           if (!ok) break;
           tc_fence_after();
           const uint64_t vb = vdesc + (uint64_t)((va.slot * Cfg::kTileBytes) >> 4);
@@ -481,7 +596,8 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
           tc_commit(v_empty(va.slot));
           va.next();
           ++done;
-          if (made < done + NS) scores(false);
+          if (left == 0) next_item(false);
+          if (left > 0) scores();
         }
       }
       failed = !ok;
@@ -496,11 +612,9 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
     // ---- softmax, row rr of the item's tile ---------------------------------------------
     const int rr = tid;
     const uint32_t base = tmem + ((uint32_t)(warp * 32) << 16);
-    // The factor of a product, never negative: the sign goes to the products.
+    // The factor of a product, never negative: the sign is in the queries.
     const float qscale = p.qscale == 0.f ? 1.f : fabsf(p.qscale);
-    const bool neg = p.qscale < 0.f, zero = p.qscale == 0.f;
-    int t = 0;  // tiles so far
-    RingPos<NV> va;
+    int t = 0, edges = 0;  // tiles, edge tiles so far
     bool ok = true;
     for (int n = 0; ok; ++n) {
       const int at = n % NI;
@@ -512,18 +626,21 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
       }
       const int tiles = it->tiles;
       if (tiles < 0) break;
+      const WindowEdge at_edge(it);
       const bool live = warp * 32 < it->nr;  // the warp has rows
       const int pos = it->pos0 + (it->r0 + min(rr, it->nr - 1)) / G;
       float m = -INFINITY, l = 0.f;
-      // The last edge tile with values that are not finite (-1: none waits), and
-      // the keys whose weight is 0 in it.
+      // The last edge tile with values that are not finite (-1: none waits).
       int odd = -1;
-      uint64_t odd_zero = 0;
-      // Adds that tile's cleared values to O, once its product is in.
+      // Adds that tile's cleared values to O, once its product is in: infinity or
+      // NaN, as the value is, and NaN where the score is minus infinity.
       auto add_odd = [&] {
         const WindowKeys keys(it, odd);
         const uint64_t seen = keys.seen(it), mine = keys.mask(p, pos);
         const int32_t* trow = p.tables + (int64_t)it->seq * p.max_blocks;
+        const int x = it->r0 + min(rr, it->nr - 1);
+        const T* const query = static_cast<const T*>(p.q) +
+                               ((int64_t)(it->q0 + x / G) * H + it->kvh * G + x % G) * D;
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
@@ -533,21 +650,37 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
             if (!(seen >> k & 1ull)) continue;
             const int tk = keys.pos(k), e = trow[tk >> shift];
             if ((unsigned)e >= (unsigned)p.num_blocks) continue;
-            const T* x = static_cast<const T*>(p.v_cache) +
-                         (((int64_t)e * p.kv_heads + it->kvh) * b + (tk & (b - 1))) * D + q * 32;
-            const bool sees = mine >> k & 1ull, none = odd_zero >> k & 1ull;
+            const int64_t row = (((int64_t)e * p.kv_heads + it->kvh) * b + (tk & (b - 1))) * D;
+            const T* const value = static_cast<const T*>(p.v_cache) + row + q * 32;
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) any |= !isfinite(static_cast<float>(value[i]));
+            if (!any || !(mine >> k & 1ull)) continue;
+            const T* const key = static_cast<const T*>(p.k_cache) + row;
+            float z = 0.f;
+            for (int d = 0; d < D; ++d)
+              z += static_cast<float>(query[d]) * static_cast<float>(key[d]);
+            const bool none = z * p.qscale == -INFINITY;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float v = static_cast<float>(x[i]);
-              if (sees && !isfinite(v))
-                o[i] = __float_as_uint(__uint_as_float(o[i]) + (none ? NAN : v));
+              const float v = static_cast<float>(value[i]);
+              if (!isfinite(v)) o[i] = __float_as_uint(__uint_as_float(o[i]) + (none ? NAN : v));
             }
           }
+          __syncwarp();
           tmem_st32(base + Cfg::kOCol + q * 32, o);
         }
         odd = -1;
       };
-      for (int j = 0; j < tiles; ++j, ++t, va.next()) {
+      // Whether the item's tile j, the last with a product, had values cleared.
+      auto flag_of = [&](int j) {
+        if (!at_edge(j)) return true;
+        const int e = edges++;
+        if (!mbar_wait(flagged, (uint32_t)(e & 1))) return false;
+        if (live && dirty[e % Cfg::kEdges] == e) odd = j;
+        return true;
+      };
+      for (int j = 0; j < tiles; ++j, ++t) {
         const int buf = t & 1;
         ok = mbar_wait(s_full(buf), (uint32_t)((t >> 1) & 1));
         if (__any_sync(kFullMask, !ok)) {
@@ -556,23 +689,13 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         }
         tc_fence_after();
         const uint32_t sp = base + buf * KT;
-        bool rescale = false, met = false;
-        uint64_t weightless = 0;
+        bool rescale = false;
         float alpha = 1.f;
         if (live) {
           uint32_t w[KT];
           tmem_ld64(sp, w);
-          if (neg) {
-#pragma unroll
-            for (int k = 0; k < KT; ++k) w[k] ^= 0x80000000u;
-          }
-          if (zero) {
-#pragma unroll
-            for (int k = 0; k < KT; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * 0.f);
-          }
-          const WindowKeys keys(it, j);
-          const bool edge = keys.edge(p, it);
-          if (edge) {
+          if (at_edge(j)) {
+            const WindowKeys keys(it, j);
             const uint64_t sees = keys.mask(p, pos);
             const uint32_t s0 = (uint32_t)sees, s1 = (uint32_t)(sees >> 32);
 #pragma unroll
@@ -617,29 +740,11 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
           const float2 sx = __fadd2_rn(s01, s23);
           l += sx.x + sx.y;
           tmem_st32(sp, pk);
-          if (edge) {
-            // (v_full first: with the tile there, the scout is past the slot's last one)
-            ok = mbar_wait(v_full(va.slot), va.phase) && mbar_wait(v_clear(va.slot), va.phase);
-            if (__any_sync(kFullMask, !ok)) {
-              ok = false;
-              break;
-            }
-            met = dirty[t % Cfg::kDirty] == t;
-            if (met) {  // (P as it was stored: its registers are not kept for this)
-              uint32_t pw[KT / 2];
-              tmem_ld32(sp, pw);
-#pragma unroll
-              for (int k = 0; k < KT; k += 2) {
-                if (!(pw[k / 2] & 0x7FFFu)) weightless |= 1ull << k;
-                if (!(pw[k / 2] & 0x7FFF0000u)) weightless |= 2ull << k;
-              }
-            }
-          }
         }
         // P.V of the item's tile before has been added to O before O or its factor
         // changes (and every phase of its barrier is waited for in turn).
         if (j > 0) {
-          ok = mbar_wait(o_done, (uint32_t)((t - 1) & 1));
+          ok = mbar_wait(o_done, (uint32_t)((t - 1) & 1)) && flag_of(j - 1);
           if (__any_sync(kFullMask, !ok)) {
             ok = false;
             break;
@@ -657,14 +762,10 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
           }
         }
         if (odd >= 0) add_odd();
-        if (met) {
-          odd = j;
-          odd_zero = weightless;
-        }
         tc_fence_before();
         mbar_arrive(p_full(buf));
       }
-      if (ok) ok = mbar_wait(o_done, (uint32_t)((t - 1) & 1)) &&
+      if (ok) ok = mbar_wait(o_done, (uint32_t)((t - 1) & 1)) && flag_of(tiles - 1) &&
                    mbar_wait(checked(at), (uint32_t)((n / NI) & 1));
       if (__any_sync(kFullMask, !ok)) {
         ok = false;
@@ -682,7 +783,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         // l = 0: every score was -inf.  A row of such scores is 0 / 0 (NaN); a
         // part of them leaves O as it is, NaN where a value was not finite, and
         // weighs nothing in the merge.
-        const float inv = l == 0.f && !whole ? 1.f : 1.f / l;
+        const float inv = wrong || (l == 0.f && !whole) ? 1.f : 1.f / l;
         const int64_t wrow = row * p.parts + it->part;
         if (!whole && mine) p.ws_ml[wrow] = wrong ? make_float2(0.f, 1.f) : make_float2(m, l);
         T* const out = static_cast<T*>(p.out) + row * D;
@@ -690,7 +791,11 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         for (int q = 0; q < D / 32; ++q) {
           uint32_t w[32];
           tmem_ld32(base + Cfg::kOCol + q * 32, w);
-          auto o = [&](int d) { return wrong ? 0.f : __uint_as_float(w[d]) * inv; };
+          if (wrong) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = 0u;
+          }
+          auto o = [&](int d) { return __uint_as_float(w[d]) * inv; };
           if (mine && whole) {
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
