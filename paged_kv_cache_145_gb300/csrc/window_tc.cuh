@@ -97,7 +97,7 @@ template <typename T, int D>
 struct WindowTcCfg : CrossTcCfg<T, D, 1, false> {
   using Base = CrossTcCfg<T, D, 1, false>;
   static constexpr int kItems = 4;                          // ring of items
-  static constexpr int kEdges = 8;                          // edge tiles in flight, more than V slots
+  static constexpr int kEdges = 16;                         // flags of edge tiles
   // softmax 0-3, K and Q 4, V 5, MMA 6, scout 7
   static constexpr int kScoutWarp = 7, kThreads = 256;
   static constexpr int kBars = 2 * Base::kSlots + 2 * Base::kBufs + kEdges + 6 + 3 * kItems;
@@ -109,7 +109,9 @@ struct WindowTcCfg : CrossTcCfg<T, D, 1, false> {
   static constexpr int kSmemBytes = kItemOff + kItems * (int)sizeof(WindowItem);
   static_assert(kSmemBytes <= 113 * 1024, "two blocks on an SM");
   static_assert(3 * kSmemBytes > 228 * 1024, "no more blocks than tensor memory serves");
-  static_assert(Base::kVSlots < kEdges, "a flag is read before its place is used again");
+  // 128 rows start and end within 128 positions each: four edge tiles and four; the
+  // scout is at most the V slots ahead of the last one's product.
+  static_assert(8 + Base::kVSlots <= kEdges, "a flag is read before its place is used again");
 };
 
 // A tile of 64 values at an edge of the window, by one warp: rows outside `mask`
@@ -203,7 +205,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
   const uint32_t q_full = o_done + 8u, q_empty = o_done + 16u;
   const uint32_t drained = o_done + 24u;
   // The scout is done with an edge tile (of every kEdges-th).
-  const uint32_t flagged = o_done + 32u;  // an edge tile's flag is there
+  const uint32_t flagged = o_done + 32u;  // the item's flags are there
   const uint32_t q_signed = o_done + 40u;
   auto v_clear = [&](int i) { return o_done + 48u + 8u * i; };
   // The ring of items: numbers there; table checked; rows written.
@@ -581,7 +583,6 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
           ok = ok && mbar_wait(v_full(va.slot), va.phase);
           if (ok && edge(j)) {
             ok = mbar_wait(v_clear(edges % Cfg::kEdges), (uint32_t)((edges / Cfg::kEdges) & 1));
-            mbar_arrive(flagged);
             ++edges;
           }
           if (!ok) break;
@@ -594,6 +595,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
                       (j > 0 || kk > 0) ? 1u : 0u);
           tc_commit(o_done);
           tc_commit(v_empty(va.slot));
+          if (j == tiles - 1) mbar_arrive(flagged);
           va.next();
           ++done;
           if (left == 0) next_item(false);
@@ -630,12 +632,10 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
       const bool live = warp * 32 < it->nr;  // the warp has rows
       const int pos = it->pos0 + (it->r0 + min(rr, it->nr - 1)) / G;
       float m = -INFINITY, l = 0.f;
-      // The last edge tile with values that are not finite (-1: none waits).
-      int odd = -1;
-      // Adds that tile's cleared values to O, once its product is in: infinity or
-      // NaN, as the value is, and NaN where the score is minus infinity.
-      auto add_odd = [&] {
-        const WindowKeys keys(it, odd);
+      // Adds the cleared values of an edge tile to O, once all products are in:
+      // infinity or NaN, as the value is, and NaN where the score is minus infinity.
+      auto add_odd = [&](int j) {
+        const WindowKeys keys(it, j);
         const uint64_t seen = keys.seen(it), mine = keys.mask(p, pos);
         const int32_t* trow = p.tables + (int64_t)it->seq * p.max_blocks;
         const int x = it->r0 + min(rr, it->nr - 1);
@@ -670,22 +670,16 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
           __syncwarp();
           tmem_st32(base + Cfg::kOCol + q * 32, o);
         }
-        odd = -1;
       };
-      // Whether the item's tile j, the last with a product, had values cleared.
-      auto flag_of = [&](int j) {
-        if (!at_edge(j)) return true;
-        const int e = edges++;
-        if (!mbar_wait(flagged, (uint32_t)(e & 1))) return false;
-        if (live && dirty[e % Cfg::kEdges] == e) odd = j;
-        return true;
-      };
-      for (int j = 0; j < tiles; ++j, ++t) {
+      // One tile; EDGE: masked.  Two copies, so that the one that most tiles take has
+      // no more in it than it needs (one for both cost 38 of 333 us).
+      auto tile = [&](auto edge_tag, int j) {
+        constexpr bool EDGE = decltype(edge_tag)::value;
         const int buf = t & 1;
         ok = mbar_wait(s_full(buf), (uint32_t)((t >> 1) & 1));
         if (__any_sync(kFullMask, !ok)) {
           ok = false;
-          break;
+          return;
         }
         tc_fence_after();
         const uint32_t sp = base + buf * KT;
@@ -694,7 +688,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         if (live) {
           uint32_t w[KT];
           tmem_ld64(sp, w);
-          if (at_edge(j)) {
+          if constexpr (EDGE) {
             const WindowKeys keys(it, j);
             const uint64_t sees = keys.mask(p, pos);
             const uint32_t s0 = (uint32_t)sees, s1 = (uint32_t)(sees >> 32);
@@ -744,10 +738,10 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         // P.V of the item's tile before has been added to O before O or its factor
         // changes (and every phase of its barrier is waited for in turn).
         if (j > 0) {
-          ok = mbar_wait(o_done, (uint32_t)((t - 1) & 1)) && flag_of(j - 1);
+          ok = mbar_wait(o_done, (uint32_t)((t - 1) & 1));
           if (__any_sync(kFullMask, !ok)) {
             ok = false;
-            break;
+            return;
           }
           tc_fence_after();
         }
@@ -761,18 +755,28 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
             tmem_st32(base + Cfg::kOCol + q * 32, o);
           }
         }
-        if (odd >= 0) add_odd();
         tc_fence_before();
         mbar_arrive(p_full(buf));
+      };
+      for (int j = 0; j < tiles && ok; ++j, ++t) {
+        if (at_edge(j)) tile(std::true_type{}, j);
+        else tile(std::false_type{}, j);
       }
-      if (ok) ok = mbar_wait(o_done, (uint32_t)((t - 1) & 1)) && flag_of(tiles - 1) &&
+      if (ok) ok = mbar_wait(o_done, (uint32_t)((t - 1) & 1)) && mbar_wait(flagged, (uint32_t)(n & 1)) &&
                    mbar_wait(checked(at), (uint32_t)((n / NI) & 1));
       if (__any_sync(kFullMask, !ok)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      if (odd >= 0) add_odd();
+      for (int j = 0; j < tiles; ++j) {
+        if (!at_edge(j)) {  // to the next that is one
+          j = max(j, (j < at_edge.left0 ? min(at_edge.left0, at_edge.right) : at_edge.right) - 1);
+          continue;
+        }
+        if (dirty[edges % Cfg::kEdges] == edges && live) add_odd(j);
+        ++edges;
+      }
       // ---- the item's rows ----------------------------------------------------------
       const bool wrong = bad[at] != 0, whole = it->whole != 0;
       if (wrong && tid == 0) set_error(p.err, PKV_DEV_TABLE_RANGE);
