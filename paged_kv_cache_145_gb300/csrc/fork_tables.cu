@@ -17,12 +17,19 @@
 // than entries or the step fails otherwise.
 //
 // What bounds it: latency.  One cluster (one block for few entries) does it in
-// five stages with a barrier between them.  A warp has a group of up to 32 rows:
-// its lanes load the rows' numbers together, then the warp walks row by row with
-// four entries a lane in flight, from L1 after the first stage, and one gather
-// for each.  A second kernel, launched early, copies the blocks over the whole
-// GPU.
+// five stages with a barrier between them; a grid-wide barrier would cost more
+// than the SMs it adds save.  A warp has a group of up to 32 rows: its lanes load
+// the rows' numbers together, then the warp walks them (in a cluster two at a
+// time) with four entries a lane and row in flight, from L1 after the first stage,
+// and one gather for each.  A second kernel, launched early, copies the blocks
+// over the whole GPU.
+//
+// Measured, 128 rows x 8 children of 124 entries, window: 34.6 us, 25.3 of them
+// without a block to copy (48.8 with eight blocks and one row at a time); 8 x 4
+// of 32 entries, one block: 16.2 us (19.3 with two rows at a time, whose second
+// is then empty).
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -64,7 +71,7 @@ struct ForkParams {
 };
 
 constexpr int kForkThreads = 1024;
-constexpr int kForkCluster = 8;
+constexpr int kForkCluster = 16;  // where the device has room for one, else 8
 constexpr int64_t kForkSmall = 8192;  // entries that one block takes
 constexpr int kForkBatch = 4;  // entries a lane holds at a time
 
@@ -105,6 +112,8 @@ __device__ __forceinline__ void fork_entries(const ForkRow& w, int e0, int (&x)[
   for (int k = 0; k < kForkBatch; ++k) x[k] = e0 + 32 * k < w.have ? w.entries[e0 + 32 * k] : -1;
 }
 
+// Y: rows that a warp walks together.
+template <int Y>
 __global__ void __launch_bounds__(kForkThreads, 1)
 fork_tables_kernel(const __grid_constant__ ForkParams p) {
   cg::cluster_group cluster = cg::this_cluster();
@@ -129,15 +138,22 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
   // (written by other threads: read where the atomics land)
   auto holders = [&](int x) { return __ldcg(p.extra_out + x); };
 
-  // Runs f(row, lane's row numbers) by groups of a warp's rows: `load` gives each
-  // lane its row's numbers, f gets those of row r by shuffles from lane i.
+  // Runs f(row, i, n, numbers) by groups of a warp's rows: `load` gives each lane
+  // its row's numbers, f gets those of the n <= Y rows from r on by shuffles from
+  // lane i on.
   const int group = min(32, max(1, (p.share + kForkThreads / 32 - 1) / (kForkThreads / 32)));
   auto groups = [&](auto load, auto f) {
     for (int g0 = r0 + warp * group; g0 < r1; g0 += kForkThreads / 32 * group) {
       const int n = min(group, r1 - g0);
       const auto mine = load(g0 + min(lane, n - 1));
-      for (int i = 0; i < n; ++i) f(g0 + i, i, mine);
+      for (int i = 0; i < n; i += Y) f(g0 + i, i, min(Y, n - i), mine);
     }
+  };
+
+  // Number of the k-th of a lane's entries, of Y rows from e0 on.
+  constexpr int U = Y * kForkBatch;
+  auto entry_of = [&](int r, int e0, int k) {
+    return (r + k / kForkBatch) * W + e0 + 32 * (k % kForkBatch);
   };
 
   // ---- nothing chosen yet --------------------------------------------------------
@@ -147,14 +163,14 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
   }
   if (all < 2) p.totals[all] = 0;
   if (p.extra_out != p.extra) {
-    constexpr int U = 8;
-    for (int x0 = all; x0 < N; x0 += U * threads) {
-      int v[U];
+    constexpr int C = 8;
+    for (int x0 = all; x0 < N; x0 += C * threads) {
+      int v[C];
 #pragma unroll
-      for (int k = 0; k < U; ++k)
+      for (int k = 0; k < C; ++k)
         if (x0 + k * threads < N) v[k] = p.extra[x0 + k * threads];
 #pragma unroll
-      for (int k = 0; k < U; ++k)
+      for (int k = 0; k < C; ++k)
         if (x0 + k * threads < N) p.extra_out[x0 + k * threads] = v[k];
     }
   }
@@ -182,19 +198,27 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
         p.solo[r] = m.last >= 0 && m.last < N && p.extra[m.last] == 0;  // (equal lanes agree)
         return m;
       },
-      [&](int r, int i, const First& m) {
-        const int len = __shfl_sync(kFullMask, m.len, i);
-        bool bad = __shfl_sync(kFullMask, m.last, i) < 0;
-        if (len < 0) {
-          if (lane == 0) fail(PKV_DEV_SEQ_LEN);
-          return;
-        }
-        const ForkRow w = fork_row(p, r, len);
-        for (int e0 = lane; e0 < w.have; e0 += B) {
-          int x[kForkBatch];
-          fork_entries(w, e0, x);
+      [&](int r, int i, int n, const First& m) {
+        ForkRow w[Y];
+        bool bad = false;
+        int most = 0;
 #pragma unroll
-          for (int k = 0; k < kForkBatch; ++k) bad |= x[k] < -1 || x[k] >= N;
+        for (int y = 0; y < Y; ++y) {
+          const int j = i + min(y, n - 1), len = __shfl_sync(kFullMask, m.len, j);
+          bad |= __shfl_sync(kFullMask, m.last, j) < 0;
+          if (len < 0 && lane == 0) fail(PKV_DEV_SEQ_LEN);
+          w[y] = fork_row(p, r + j - i, max(len, 0));
+          most = max(most, w[y].have);
+        }
+        for (int e0 = lane; e0 < most; e0 += B) {
+          int x[Y][kForkBatch];
+#pragma unroll
+          for (int y = 0; y < Y; ++y) fork_entries(w[y], e0, x[y]);
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const int v = x[k / kForkBatch][k % kForkBatch];
+            bad |= v < -1 || v >= N;
+          }
         }
         if (bad) fail(PKV_DEV_TABLE_RANGE);
       });
@@ -223,27 +247,43 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
   auto numbers = [&](int r) {
     return Numbers{p.lens[r], __ldcg(p.children + r), __ldcg(p.solo + r)};
   };
-  // Runs f(row, entry, blocks, changes) for the rows' entries, kForkBatch a lane.
+  // Runs f(row, rows, entry, blocks, changes) for the rows' entries, a lane's of Y
+  // rows at a time.
   auto rows = [&](auto f, auto done) {
-    groups(numbers, [&](int r, int i, const Numbers& m) {
-      const ForkRow w = fork_row(p, r, __shfl_sync(kFullMask, m.len, i));
-      const int c = __shfl_sync(kFullMask, m.children, i);
-      const bool solo = __shfl_sync(kFullMask, m.solo, i) != 0;
-      for (int e0 = lane; e0 - lane < w.have; e0 += B) {
-        int x[kForkBatch], d[kForkBatch];
-        fork_entries(w, e0, x);
+    groups(numbers, [&](int r, int i, int n, const Numbers& m) {
+      ForkRow w[Y];
+      int c[Y], solo[Y], most = 0;
 #pragma unroll
-        for (int k = 0; k < kForkBatch; ++k) d[k] = x[k] < 0 ? 0 : fork_delta(w, e0 + 32 * k, c, solo);
-        f(r, e0, x, d);
+      for (int y = 0; y < Y; ++y) {
+        const int j = i + min(y, n - 1);
+        w[y] = fork_row(p, r + j - i, __shfl_sync(kFullMask, m.len, j));
+        c[y] = __shfl_sync(kFullMask, m.children, j);
+        solo[y] = __shfl_sync(kFullMask, m.solo, j);
+        if (y >= n) w[y].have = 0;
+        most = max(most, w[y].have);
       }
-      done(r);
+      for (int e0 = lane; e0 - lane < most; e0 += B) {
+        int x[U], d[U];
+#pragma unroll
+        for (int y = 0; y < Y; ++y) {
+          int z[kForkBatch];
+          fork_entries(w[y], e0, z);
+#pragma unroll
+          for (int k = 0; k < kForkBatch; ++k) {
+            x[y * kForkBatch + k] = z[k];
+            d[y * kForkBatch + k] = z[k] < 0 ? 0 : fork_delta(w[y], e0 + 32 * k, c[y], solo[y] != 0);
+          }
+        }
+        f(r, n, e0, x, d);
+      }
+      done(r, n);
     });
   };
-  auto nothing = [](int) {};
+  auto nothing = [](int, int) {};
   if (ok)
-    rows([&](int, int, const int (&x)[kForkBatch], const int (&d)[kForkBatch]) {
+    rows([&](int, int, int, const int (&x)[U], const int (&d)[U]) {
 #pragma unroll
-      for (int k = 0; k < kForkBatch; ++k) {
+      for (int k = 0; k < U; ++k) {
         if (d[k] < 0) p.claim[x[k]] = INT_MAX;
         if (d[k]) atomicAdd(p.extra_out + x[k], d[k]);
       }
@@ -252,35 +292,39 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
 
   // ---- holders that do not hold; the first entry of each block that goes back --------
   if (ok)
-    rows([&](int r, int e0, const int (&x)[kForkBatch], const int (&d)[kForkBatch]) {
-      int left[kForkBatch];
+    rows([&](int r, int, int e0, const int (&x)[U], const int (&d)[U]) {
+      int left[U];
 #pragma unroll
-      for (int k = 0; k < kForkBatch; ++k) left[k] = d[k] < 0 ? holders(x[k]) : 0;
+      for (int k = 0; k < U; ++k) left[k] = d[k] < 0 ? holders(x[k]) : 0;
 #pragma unroll
-      for (int k = 0; k < kForkBatch; ++k) {
+      for (int k = 0; k < U; ++k) {
         if (left[k] < -1) fail(PKV_DEV_SHARING);
-        if (left[k] == -1) atomicMin(p.claim + x[k], r * W + e0 + 32 * k);
+        if (left[k] == -1) atomicMin(p.claim + x[k], entry_of(r, e0, k));
       }
     }, nothing);
   barrier();
   if (ok) {
-    int n = 0;  // of the row
-    rows([&](int r, int e0, const int (&x)[kForkBatch], const int (&d)[kForkBatch]) {
-      int left[kForkBatch], mine[kForkBatch];
+    int back[Y] = {};  // of the rows
+    rows([&](int r, int n, int e0, const int (&x)[U], const int (&d)[U]) {
+      int left[U], mine[U];
 #pragma unroll
-      for (int k = 0; k < kForkBatch; ++k) {
+      for (int k = 0; k < U; ++k) {
         left[k] = d[k] < 0 ? holders(x[k]) : 0;
         mine[k] = d[k] < 0 ? __ldcg(p.claim + x[k]) : -1;
       }
 #pragma unroll
-      for (int k = 0; k < kForkBatch; ++k) {
-        const unsigned hit = __ballot_sync(kFullMask, left[k] == -1 && mine[k] == r * W + e0 + 32 * k);
-        n += __popc(hit);
-        if (lane == 0 && (e0 >> 5) + k < words) p.gone[(int64_t)r * words + (e0 >> 5) + k] = hit;
+      for (int k = 0; k < U; ++k) {
+        const int y = k / kForkBatch, word = (e0 >> 5) + k % kForkBatch;
+        const unsigned hit = __ballot_sync(kFullMask, left[k] == -1 && mine[k] == entry_of(r, e0, k));
+        back[y] += __popc(hit);
+        if (lane == 0 && word < words && y < n) p.gone[(int64_t)(r + y) * words + word] = hit;
       }
-    }, [&](int r) {
-      if (lane == 0) p.back[r] = n;
-      n = 0;
+    }, [&](int r, int n) {
+#pragma unroll
+      for (int y = 0; y < Y; ++y) {
+        if (lane == 0 && y < n) p.back[r + y] = back[y];
+        back[y] = 0;
+      }
     });
   }
   barrier();
@@ -306,9 +350,9 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
       block_scan(r1 - r0, s_scan, p.first + r0, [&](int i) { return p.back[r0 + i]; });
       // (p.first is read no more as such: the copies' choice is in p.fresh's sums)
     } else {
-      rows([&](int, int, const int (&x)[kForkBatch], const int (&d)[kForkBatch]) {
+      rows([&](int, int, int, const int (&x)[U], const int (&d)[U]) {
 #pragma unroll
-        for (int k = 0; k < kForkBatch; ++k)
+        for (int k = 0; k < U; ++k)
           if (d[k]) atomicAdd(p.extra_out + x[k], -d[k]);
       }, nothing);
     }
@@ -317,18 +361,34 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
     };
     if (ok)
       groups([&](int r) { return Back{p.lens[r], p.first[r], p.back[r]}; },
-             [&](int r, int i, const Back& m) {
-               if (__shfl_sync(kFullMask, m.n, i) == 0) return;
-               const ForkRow w = fork_row(p, r, __shfl_sync(kFullMask, m.len, i));
-               int64_t at = count + before + __shfl_sync(kFullMask, m.at, i);
-               for (int e0 = 0; e0 < w.have; e0 += 32) {
-                 const unsigned hit = p.gone[(int64_t)r * words + (e0 >> 5)];
-                 if (hit >> lane & 1u) {
-                   const int x = w.entries[e0 + lane];
-                   p.ring[ring_at(at + __popc(hit & ((1u << lane) - 1u)))] = x;
-                   p.extra_out[x] = 0;
+             [&](int r, int i, int n, const Back& m) {
+               ForkRow w[Y];
+               int64_t at[Y];
+               int most = 0;
+#pragma unroll
+               for (int y = 0; y < Y; ++y) {
+                 const int j = i + min(y, n - 1);
+                 w[y] = fork_row(p, r + j - i, __shfl_sync(kFullMask, m.len, j));
+                 at[y] = count + before + __shfl_sync(kFullMask, m.at, j);
+                 if (__shfl_sync(kFullMask, m.n, j) == 0 || y >= n) w[y].have = 0;
+                 most = max(most, w[y].have);
+               }
+               for (int e0 = 0; e0 < most; e0 += 32) {
+                 unsigned hit[Y];
+                 int x[Y];
+#pragma unroll
+                 for (int y = 0; y < Y; ++y) {
+                   hit[y] = e0 < w[y].have ? p.gone[(int64_t)(r + y) * words + (e0 >> 5)] : 0u;
+                   x[y] = e0 + lane < w[y].have ? w[y].entries[e0 + lane] : 0;
                  }
-                 at += __popc(hit);
+#pragma unroll
+                 for (int y = 0; y < Y; ++y) {
+                   if (hit[y] >> lane & 1u) {
+                     p.ring[ring_at(at[y] + __popc(hit[y] & ((1u << lane) - 1u)))] = x[y];
+                     p.extra_out[x[y]] = 0;
+                   }
+                   at[y] += __popc(hit[y]);
+                 }
                }
              });
   }
@@ -359,18 +419,30 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
       }
     }
     p.lens_out[s] = len;  // (equal lanes write the same)
-    for (int i = 0; i < n; ++i) {
-      const int r = __shfl_sync(kFullMask, parent, i), f = __shfl_sync(kFullMask, fresh, i);
-      const ForkRow w = fork_row(p, max(r, 0), __shfl_sync(kFullMask, len, i));  // (none: empty)
+    for (int i = 0; i < n; i += Y) {
+      ForkRow w[Y];
+      int f[Y];
+#pragma unroll
+      for (int y = 0; y < Y; ++y) {
+        const int j = min(i + y, n - 1);
+        f[y] = __shfl_sync(kFullMask, fresh, j);
+        w[y] = fork_row(p, max(__shfl_sync(kFullMask, parent, j), 0),
+                        __shfl_sync(kFullMask, len, j));  // (none: empty)
+      }
       int32_t* const out = p.tables_out + (int64_t)(g0 + i) * W;
       for (int e0 = lane; e0 < W; e0 += B) {
-        int x[kForkBatch];
-        fork_entries(w, e0, x);
+        int x[Y][kForkBatch];
 #pragma unroll
-        for (int k = 0; k < kForkBatch; ++k) {
-          const int e = e0 + 32 * k;
-          if (e < W) out[e] = f >= 0 && e == w.partial ? f : fork_keeps(w, e) ? x[k] : -1;
-        }
+        for (int y = 0; y < Y; ++y) fork_entries(w[y], e0, x[y]);
+#pragma unroll
+        for (int y = 0; y < Y; ++y)
+#pragma unroll
+          for (int k = 0; k < kForkBatch; ++k) {
+            const int e = e0 + 32 * k;
+            if (e < W && i + y < n)
+              out[(int64_t)y * W + e] =
+                  f[y] >= 0 && e == w[y].partial ? f[y] : fork_keeps(w[y], e) ? x[y][k] : -1;
+          }
       }
     }
   }
@@ -429,7 +501,30 @@ int pkv_launch_fork_tables(const pkv_cache* c, size_t elem_bytes, int32_t* ring,
   p.totals = reinterpret_cast<int*>(p.gone + (int64_t)rows * ((width + 31) / 32));
   const int64_t entries = (int64_t)(rows + next) * width;
   const bool small = entries <= kForkSmall && c->num_blocks <= 8 * kForkSmall;
-  const int cluster = small ? 1 : kForkCluster;
+  // Sixteen blocks are more than every device promises a cluster: asked for once.
+  static std::atomic<int> most[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return pkv_cuda_failed();
+  int cluster = 1;
+  if (!small && (cluster = most[dev & 63].load()) == 0) {
+    cluster = 8;
+    cudaLaunchConfig_t ask{};
+    cudaLaunchAttribute dim{};
+    ask.gridDim = dim3(kForkCluster);
+    ask.blockDim = dim3(kForkThreads);
+    dim.id = cudaLaunchAttributeClusterDimension;
+    dim.val.clusterDim.x = kForkCluster;
+    dim.val.clusterDim.y = dim.val.clusterDim.z = 1;
+    ask.attrs = &dim;
+    ask.numAttrs = 1;
+    int fit = 0;
+    if (cudaFuncSetAttribute(fork_tables_kernel<2>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                             1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&fit, fork_tables_kernel<2>, &ask) == cudaSuccess && fit > 0)
+      cluster = kForkCluster;
+    (void)cudaGetLastError();
+    most[dev & 63].store(cluster);
+  }
   p.share = (rows + cluster - 1) / cluster;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(cluster);
@@ -441,7 +536,7 @@ int pkv_launch_fork_tables(const pkv_cache* c, size_t elem_bytes, int32_t* ring,
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = small ? 0 : 1;
-  if (cudaLaunchKernelEx(&cfg, fork_tables_kernel, p) != cudaSuccess) return pkv_cuda_failed();
+  if (cudaLaunchKernelEx(&cfg, small ? fork_tables_kernel<1> : fork_tables_kernel<2>, p) != cudaSuccess) return pkv_cuda_failed();
   if (next == 0) return PKV_OK;
   static PagePlaces places;
   const int grid = places.of(fork_copy_kernel);

@@ -9,14 +9,17 @@ namespace pkv {
 
 // Exclusive sums of f(0) .. f(n - 1) into out, by one thread block of whole
 // warps (scan: 33 ints of shared memory); returns the total in every thread.
-// f(i) may be out[i].
 template <typename F>
 __device__ __forceinline__ int block_scan(int n, int* scan, int* out, F f) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (int)blockDim.x >> 5;
   const int per = (n + (int)blockDim.x - 1) / (int)blockDim.x;
   const int i0 = min(tid * per, n), i1 = min(i0 + per, n);
   int sum = 0;
-  for (int i = i0; i < i1; ++i) sum += f(i);
+  for (int i = i0; i < i1; ++i) {
+    const int x = f(i);
+    out[i] = x;
+    sum += x;
+  }
   int up = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -39,7 +42,7 @@ __device__ __forceinline__ int block_scan(int n, int* scan, int* out, F f) {
   __syncthreads();
   int at = scan[warp] + up - sum;
   for (int i = i0; i < i1; ++i) {
-    const int x = f(i);
+    const int x = out[i];
     out[i] = at;
     at += x;
   }
