@@ -257,6 +257,11 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
   tc_fence_after();
   const uint32_t tmem = *slot_addr;
   bool failed = false;
+  // Limit of the waits that may take as long as an item (32 ns a key), the scout's
+  // check of a table (in that), its zeroing of a refused sequence, or its way past
+  // sequences without queries.  The others are a tile long.
+  const uint64_t patience = kWaitLimitNs + 32ull * (uint64_t)p.max_len +
+                            128ull * (uint64_t)(p.total_queries + (int64_t)p.num_seqs * p.kv_heads);
 
   if (warp == Cfg::kScoutWarp) {
     // ---- scout ------------------------------------------------------------------
@@ -282,7 +287,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         const uint64_t since = global_ns();
         while (ok && *v_issued <= tiles) {
           __nanosleep(100);
-          ok = global_ns() - since <= kWaitLimitNs;
+          ok = global_ns() - since <= patience;
         }
         ok = ok && mbar_wait(v_full(va.slot), va.phase);
         if (__any_sync(kFullMask, !ok)) {
@@ -319,15 +324,35 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         if (c.bits && tile == 0 && it.part == 0) {
           if (lane == 0) set_error(p.err, c.bits);
           // the tiles cover max_queries rows only: this one zeroes them all
-          for (int64_t e = lane; e < (int64_t)c.Q * G * D; e += 32)
-            out[((c.q0 + e / (G * D)) * H + it.kvh * G) * D + e % (G * D)] = Elem<T>::from_f(0.f);
+          const int units = G * D / 8;  // of 16 bytes, of a query's heads
+          for (int64_t e = lane; e < (int64_t)c.Q * units; e += 32)
+            reinterpret_cast<uint4*>(out + ((c.q0 + e / units) * H + it.kvh * G) * D)[e % units] =
+                make_uint4(0u, 0u, 0u, 0u);
         }
         const int rows = c.bits ? 0 : c.Q * G;
         it.r0 = tile * 128;
         if (it.r0 >= rows || it.part >= c.parts) {
-          // none here nor in the rest of this group
-          const int64_t left = (group + 1) * row_tiles - idx;
-          idx += ((left - 1) / gridDim.x) * gridDim.x;
+          // None here nor in the rest of this group: on to the next one in which this
+          // block has a tile with rows, or a sequence to refuse, a group per lane
+          // (max_queries may be far above what most sequences have).
+          int64_t next = total;
+          for (int64_t g0 = group + 1; g0 * row_tiles < total; g0 += 32) {
+            const int64_t start = (g0 + lane) * row_tiles;
+            const int64_t off = (idx - start) % (int64_t)gridDim.x;
+            const int64_t at = off < 0 ? off + gridDim.x : off;  // the block's first tile there
+            bool some = false;
+            if (start < total && at < row_tiles) {
+              const int of = (int)((g0 + lane) / groups);
+              const CrossSeq o = cross_seq(p, (int)((g0 + lane) % groups) / p.kv_heads);
+              some = o.bits ? at == 0 && of == 0 : at * 128 < (int64_t)o.Q * G && of < o.parts;
+            }
+            const unsigned hits = __ballot_sync(kFullMask, some);
+            if (hits) {
+              next = __shfl_sync(kFullMask, start + at, __ffs(hits) - 1);
+              break;
+            }
+          }
+          idx = next - gridDim.x;
           continue;
         }
         it.q0 = c.q0;
@@ -364,7 +389,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
       }
       const int at = n % NI;
       volatile WindowItem* const mine = items + at;
-      if (n >= NI) ok = mbar_wait(written(at), (uint32_t)((n / NI - 1) & 1));
+      if (n >= NI) ok = mbar_wait(written(at), (uint32_t)((n / NI - 1) & 1), patience);
       if (__any_sync(kFullMask, !ok)) {
         failed = true;
         ok = false;
@@ -410,7 +435,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
       // that no product of theirs is beyond float32): products then have a factor
       // that is not negative, and the largest score the largest product.
       if (ok && p.qscale <= 0.f) {
-        ok = mbar_wait(q_full, (uint32_t)(n & 1));
+        ok = mbar_wait(q_full, (uint32_t)(n & 1), patience);
         if (__any_sync(kFullMask, !ok)) {
           failed = true;
           ok = false;
@@ -449,7 +474,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
       bool ok = true;
       for (; ok; ++n) {
         const volatile WindowItem* const it = items + n % NI;
-        ok = mbar_wait(ready(n % NI), (uint32_t)((n / NI) & 1));
+        ok = mbar_wait(ready(n % NI), (uint32_t)((n / NI) & 1), patience);
         if (!ok || it->tiles < 0) break;
         const int tiles = it->tiles, kvh = it->kvh, w0 = it->w0, s0 = it->s0, last = it->last;
         const int32_t* trow = p.tables + (int64_t)it->seq * p.max_blocks;
@@ -468,7 +493,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         look(now, 0);
         look(next, 1);
         if (key) {  // the item's queries, once the last one's scores are made
-          if (n > 0) ok = mbar_wait(q_empty, (uint32_t)((n - 1) & 1));
+          if (n > 0) ok = mbar_wait(q_empty, (uint32_t)((n - 1) & 1), patience);
           if (!ok) break;
           mbar_arrive_expect_tx(q_full, Cfg::kQBytes);
           ++queries;
@@ -544,7 +569,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         const int at = sn % NI;
         const uint32_t par = (uint32_t)((sn / NI) & 1), qpar = (uint32_t)(sn & 1);
         if (!wait && !mbar_test_wait(ready(at), par)) return;
-        ok = ok && mbar_wait(ready(at), par);
+        ok = ok && mbar_wait(ready(at), par, patience);
         if (!ok) return;
         const int t = items[at].tiles;
         if (t < 0) {
@@ -553,7 +578,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         }
         const uint32_t there = p.qscale > 0.f ? q_full : q_signed;
         if (!wait && !mbar_test_wait(there, qpar)) return;
-        ok = mbar_wait(there, qpar);
+        ok = mbar_wait(there, qpar, patience);
         if (!ok) return;
         left = t;
         ++sn;
@@ -561,7 +586,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
       int done = 0, edges = 0;  // tiles with P.V, edge tiles
       for (int n = 0; ok; ++n) {
         const volatile WindowItem* const it = items + n % NI;
-        ok = mbar_wait(ready(n % NI), (uint32_t)((n / NI) & 1));
+        ok = mbar_wait(ready(n % NI), (uint32_t)((n / NI) & 1), patience);
         if (!ok || it->tiles < 0) break;
         const int tiles = it->tiles;
         const WindowEdge edge(it);
@@ -586,7 +611,8 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
           }
           ok = ok && mbar_wait(v_full(va.slot), va.phase);
           if (ok && edge(j)) {
-            ok = mbar_wait(v_clear(edges % Cfg::kEdges), (uint32_t)((edges / Cfg::kEdges) & 1));
+            ok = mbar_wait(v_clear(edges % Cfg::kEdges), (uint32_t)((edges / Cfg::kEdges) & 1),
+                           patience);
             ++edges;
           }
           if (!ok) break;
@@ -625,7 +651,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
     for (int n = 0; ok; ++n) {
       const int at = n % NI;
       const volatile WindowItem* const it = items + at;
-      ok = mbar_wait(ready(at), (uint32_t)((n / NI) & 1));
+      ok = mbar_wait(ready(at), (uint32_t)((n / NI) & 1), patience);
       if (__any_sync(kFullMask, !ok)) {
         ok = false;
         break;
@@ -767,7 +793,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         else tile(std::false_type{}, j);
       }
       if (ok) ok = mbar_wait(o_done, (uint32_t)((t - 1) & 1)) && mbar_wait(flagged, (uint32_t)(n & 1)) &&
-                   mbar_wait(checked(at), (uint32_t)((n / NI) & 1));
+                   mbar_wait(checked(at), (uint32_t)((n / NI) & 1), patience);
       if (__any_sync(kFullMask, !ok)) {
         ok = false;
         break;

@@ -348,6 +348,25 @@ def test_equal_bits_on_every_call_stream_and_replay(dtype, D):
         c.check(first)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32, FP8])
+def test_many_sequences_and_a_loose_bound(dtype):
+    """The most sequences, of which few have queries; max_queries far above theirs
+    (more row tiles than blocks); one refused sequence among them."""
+    S = 65535
+    rng = np.random.default_rng(5)
+    some = np.sort(rng.choice(S, 40, replace=False))
+    qlens, lens = np.zeros(S, dtype=int), np.zeros(S, dtype=int)
+    qlens[some] = rng.integers(1, 90, 40)
+    lens[some] = qlens[some] + rng.integers(0, 200, 40)
+    c = Case(qlens.tolist(), lens.tolist(), 8, 2, 64, 70, 5, dtype, io_of(dtype), extra_rows=20000,
+             seed=6)
+    c.lens[some[7]] = 10 ** 6                                  # past the table
+    out = c.call(max_queries=c.q.shape[0])
+    assert pkv.paged_get_device_error() == 4
+    assert (out[c.starts[some[7]]:c.starts[some[7] + 1]] == 0).all()
+    c.check(out, [int(x) for x in some if x != some[7]])
+
+
 def test_lengths_that_change_between_replays():
     """A captured decode step serves the lengths it finds."""
     c = Case([1] * 4, [900, 333, 64, 17], 8, 2, 128, 100, 4, BF16, seed=13)
