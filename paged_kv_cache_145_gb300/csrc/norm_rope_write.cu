@@ -12,6 +12,14 @@
 // shuffles between registers and nothing is read twice.  With halves of whole
 // vectors a lane holds both partners of its pairs; neighbours are in one vector;
 // other halves trade their elements through shared memory.
+//
+// What bounds it: many tokens, HBM and the issue of instructions (8192 tokens of
+// 32 + 8 + 8 heads of 128, bf16: 43.4 us, 4.6 TB/s; the rotary write alone takes
+// 34.7).  Weights in a lane's registers and two elements to an instruction: 44.9
+// of 46.3 us before, and the pairs' parameters read by fewer lanes apart 43.4.
+// Registers capped for four blocks on an SM: 47.2; a warp per token with its
+// cosines in registers: 50.7.  Eight tokens take 3.1 us, a launch and two trips
+// to memory one after the other.
 #include <algorithm>
 #include <atomic>
 
@@ -29,7 +37,9 @@ struct NormRopeParams : RopeParams {
 
 enum class RopeForm { kPairs, kHalves, kSplit };  // neighbours; whole-vector halves; other halves
 
-template <typename TI, bool FP8, RopeForm FORM>
+// HELD: one set of weights of the io type for all query heads, and one for all
+// keys' (or none): a lane's stay in registers.
+template <typename TI, bool FP8, RopeForm FORM, bool HELD>
 __global__ void __launch_bounds__(kRopeThreads)
 norm_rope_write_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int V = 16 / (int)sizeof(TI);
@@ -86,20 +96,53 @@ norm_rope_write_kernel(const __grid_constant__ NormRopeParams p) {
     for (int o = p.lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(mates, x, o);
     return x;
   };
-  auto weigh = [&](float (&f)[V], int which, int h, int vec) {
-    if (!p.w[which]) return;
+  [[maybe_unused]] Unit held[2];
+  if constexpr (HELD) {
+    auto hold = [&](Unit& w, const void* from) {
+      float one[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) one[j] = 1.f;
+      w.a.narrow(one);
+      w.b.narrow(one);
+      if (from && va < vecs) w.a.load(static_cast<const TI*>(from) + va * V);
+      if (from && vb < vecs) w.b.load(static_cast<const TI*>(from) + vb * V);
+    };
+    hold(held[0], p.w[0]);
+    hold(held[1], p.w[1]);
+  }
+  auto weigh = [&](float (&f)[V], bool query, int h, int vec) {
     float g[V];
-    const int64_t at = (int64_t)h * p.w_stride[which] + vec * V;
-    if (p.w_f32[which]) {
+    const void* const w = query ? p.w[0] : p.w[1];
+    if (!w) return;
+    const int64_t at = (int64_t)h * (query ? p.w_stride[0] : p.w_stride[1]) + vec * V;
+    if (query ? p.w_f32[0] : p.w_f32[1]) {
 #pragma unroll
       for (int j = 0; j < V; j += 4)
-        RowLoad<float, 4>::load(static_cast<const float*>(p.w[which]) + at + j,
+        RowLoad<float, 4>::load(static_cast<const float*>(w) + at + j,
                                 *reinterpret_cast<float(*)[4]>(g + j));
     } else {
-      RowLoad<TI, V>::load(static_cast<const TI*>(p.w[which]) + at, g);
+      RowLoad<TI, V>::load(static_cast<const TI*>(w) + at, g);
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) f[j] *= g[j];
+  };
+  // f * by, two elements to an instruction.
+  auto times = [&](float (&f)[V], const float (&by)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      const float2 y = __fmul2_rn(make_float2(f[j], f[j + 1]), make_float2(by[j], by[j + 1]));
+      f[j] = y.x;
+      f[j + 1] = y.y;
+    }
+  };
+  auto squares = [&](const float (&x)[V], const float (&y)[V]) {
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      s = __ffma2_rn(make_float2(x[j], x[j + 1]), make_float2(x[j], x[j + 1]), s);
+      s = __ffma2_rn(make_float2(y[j], y[j + 1]), make_float2(y[j], y[j + 1]), s);
+    }
+    return s.x + s.y;
   };
   auto finish = [&](int64_t t0, const Place& at, const Unit& w, const float2* cs, int64_t row) {
     const bool query = at.head < H, key = !query && at.head < H + Hk;
@@ -110,10 +153,7 @@ norm_rope_write_kernel(const __grid_constant__ NormRopeParams p) {
     w.b.widen(b);
     if (query || key) {
       // ---- norm -----------------------------------------------------------------
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) sum += a[j] * a[j] + b[j] * b[j];
-      sum = group_sum(sum);
+      float sum = group_sum(squares(a, b));
       float scale = 1.f;
       if (sum > 0x1p120f || (p.eps == 0.f && sum < 0x1p-90f)) {
         float top = 0.f;
@@ -124,25 +164,32 @@ norm_rope_write_kernel(const __grid_constant__ NormRopeParams p) {
           int e;
           frexpf(top, &e);
           scale = ldexpf(1.f, min(126, -e));
-          sum = 0.f;
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             a[j] *= scale;
             b[j] *= scale;
-            sum += a[j] * a[j] + b[j] * b[j];
           }
-          sum = group_sum(sum);
+          sum = group_sum(squares(a, b));
         }
       }
       const float r = rsqrtf(sum / (float)D + p.eps * scale * scale);
+      float rs[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        a[j] *= r;
-        b[j] *= r;
+      for (int j = 0; j < V; ++j) rs[j] = r;
+      times(a, rs);
+      times(b, rs);
+      if constexpr (HELD) {
+        Unit w = held[0];
+        if (!query) w = held[1];
+        float g[V];
+        w.a.widen(g);
+        times(a, g);
+        w.b.widen(g);
+        times(b, g);
+      } else {
+        if (va < vecs) weigh(a, query, h, va);
+        if (vb < vecs) weigh(b, query, h, vb);
       }
-      const int which = query ? 0 : 1;
-      if (va < vecs) weigh(a, which, h, va);
-      if (vb < vecs) weigh(b, which, h, vb);
       // ---- rotation --------------------------------------------------------------
       if constexpr (PAIRS) {
         auto turn = [&](float (&f)[V], int vec) {
@@ -246,14 +293,18 @@ int launch_norm_rope(NormRopeParams& p, cudaStream_t stream) {
   if (p.units > 32) return PKV_ERR_GEOMETRY;
   p.lanes = 1;
   while (p.lanes < p.units) p.lanes *= 2;
-  auto kern = form == 0   ? norm_rope_write_kernel<TI, FP8, RopeForm::kPairs>
-              : form == 1 ? norm_rope_write_kernel<TI, FP8, RopeForm::kHalves>
-                          : norm_rope_write_kernel<TI, FP8, RopeForm::kSplit>;
+  const bool held = p.w_stride[0] == 0 && p.w_stride[1] == 0 && !(p.w[0] && p.w_f32[0]) &&
+                    !(p.w[1] && p.w_f32[1]) && form != 2;
+  auto kern = held ? form == 0 ? norm_rope_write_kernel<TI, FP8, RopeForm::kPairs, true>
+                               : norm_rope_write_kernel<TI, FP8, RopeForm::kHalves, true>
+              : form == 0 ? norm_rope_write_kernel<TI, FP8, RopeForm::kPairs, false>
+              : form == 1 ? norm_rope_write_kernel<TI, FP8, RopeForm::kHalves, false>
+                          : norm_rope_write_kernel<TI, FP8, RopeForm::kSplit, false>;
   // Blocks that run at a time, per device and variant (looked up once).
-  static std::atomic<int> running[64][3];
+  static std::atomic<int> running[64][5];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return pkv_cuda_failed();
-  std::atomic<int>& known = running[dev & 63][form];
+  std::atomic<int>& known = running[dev & 63][form + (held ? 3 : 0)];
   int slots = known.load();
   if (slots == 0) {
     int sms = 0, per_sm = 0;

@@ -86,8 +86,11 @@ template <int P>
 __device__ __forceinline__ void rope_chunk(const RopeParams& p, int64_t t0, int nt, int pairs,
                                            int groups, float2* cs, int64_t* row) {
   const int tid = threadIdx.x;
-  for (int e = tid; e < nt * pairs; e += kRopeThreads) {
-    const int tok = e / pairs, i = e - tok * pairs;
+  // (a pair's tokens in neighbouring lanes: each different pair of a warp is a turn
+  // of its own at the parameters)
+  for (int e = tid; e < kRopeTokens * pairs; e += kRopeThreads) {
+    const int i = e / kRopeTokens, tok = e - i * kRopeTokens;
+    if (tok >= nt) continue;
     const int64_t pos = p.positions[(int64_t)p.rot.axis[i] * p.num_tokens + t0 + tok];
     const uint64_t turns = (uint64_t)pos * p.rot.step[i];  // modulo one turn
     const float half_turns = (float)(int32_t)(turns >> 32) * 0x1p-31f;
