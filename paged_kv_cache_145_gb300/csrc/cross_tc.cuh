@@ -102,7 +102,7 @@ struct CrossTcCfg {
   static constexpr int kFlagOff = kTmemOff + 4;
   static constexpr int kDirtyOff = kTmemOff + 8;            // FP8 with a window: 2 a V slot
   static constexpr int kSpanOff = kDirtyOff + (KV8 ? 8 * kVSlots : 0);  // and WindowEdges
-  static constexpr int kSmemBytes = kSpanOff + (KV8 ? 24 : 8);
+  static constexpr int kSmemBytes = kSpanOff + (KV8 ? 44 : 8);
   static constexpr uint32_t kTileCols = 256;
   static constexpr uint32_t kTmemCols = QT * kTileCols;
   static constexpr uint32_t kOCol = kBufs * kKeys;
@@ -136,21 +136,49 @@ __device__ __forceinline__ bool table_row_bad(const CrossParams& p, const int32_
   return bad;
 }
 
-// A block's span as the softmax threads look it up in shared memory, tile by
-// tile: held in registers it does not fit next to a row of scores (36 bytes of
-// spills a thread).
+// The tiles of a row tile's keys in which some row does not see some key: those
+// before the window's last start, unless the sinks cover them, and those behind the
+// first row (looked up once: 110 us of 383 went into finding it out in every tile).
+struct WindowEdge {
+  int left0, left1, right;
+  __device__ __forceinline__ bool operator()(int j) const {
+    return (j >= left0 && j < left1) || j >= right;
+  }
+  // First tile behind j that is not what j is.
+  __device__ __forceinline__ int run(int j) const {
+    if (j >= right) return INT_MAX;
+    if (j < left0 && left0 < left1) return min(left0, right);
+    return j < left1 ? min(left1, right) : right;
+  }
+};
+
+// Of the keys from key0 on, packed (position v, or v + skip behind the sinks'), of
+// rows from position `first` to `last`.  A tile starts at key v = key0 + 64 j,
+// position v + skip (in the sinks' tiles, v): v + 64 <= sinks is seen by all;
+// v + skip <= last - window is not; nor is v + skip + 63 > first.  (The sinks' tiles
+// that pass for starting before the window's end are all of them but those.)
+__device__ __forceinline__ WindowEdge window_edge(const WindowParams& p, int first, int last,
+                                                  int64_t skip, int64_t key0) {
+  auto tiles_below = [](int64_t v) { return (int)min((int64_t)1 << 30, max((int64_t)0, v >> 6)); };
+  return {tiles_below((int64_t)p.sinks - key0),
+          tiles_below((int64_t)last - p.window - skip - key0 + 64),
+          tiles_below((int64_t)first + 1 - skip - key0)};
+}
+
+// A block's span as the softmax threads look it up in shared memory at its edges:
+// held in registers it does not fit next to a row of scores (36 bytes of spills a
+// thread).
 struct WindowEdges {
-  int first, last;  // positions of the first and the last row
+  int last;         // position of the last row
   int w0, s0, head, skip;
+  int tile0, tiles; // of the span, the block's
+  int pos0;         // position of the sequence's first query
+  WindowEdge at;    // the tiles
 
   template <int KT>
   __device__ __forceinline__ int pos(int j) const volatile {
-    return (j < head ? j : j + skip) * KT;
-  }
-  // Whether some row does not see some position of the tile at t0.
-  template <int KT>
-  __device__ __forceinline__ bool edge(const WindowParams& p, int t0) const volatile {
-    return t0 + KT - 1 > first || (t0 + KT - 1 >= p.sinks && t0 <= last - p.window);
+    const int i = tile0 + j;
+    return (i < head ? i : i + skip) * KT;
   }
   // Positions of the tile of 64 at t0 that some row sees.
   __device__ __forceinline__ uint64_t seen(int t0) const volatile {
@@ -182,13 +210,20 @@ __device__ __forceinline__ uint32_t zero_pair(uint32_t w) {
 // A thread's Q row, from global memory into row rr of a 128-row tile in the
 // 128-byte-swizzled operand layout; returns the factor that makes its
 // products scores in base-2 units (never negative: the sign of the scale goes
-// into Q, exactly, so that the largest score has the largest product).
-template <typename T, int D, bool KV8>
+// into Q, exactly, so that the largest score has the largest product).  HOLD: the
+// row stays in registers between its largest element and its conversion.
+template <typename T, int D, bool KV8, bool HOLD>
 __device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const T* row,
                                            unsigned char* tile, int rr) {
   const uint4* src = reinterpret_cast<const uint4*>(row);
   bool neg = p.qscale < 0.f;
   float shift = 1.f, qscale = fabsf(p.qscale);
+  // A row's loads are all in flight before the first is used.
+  [[maybe_unused]] uint4 held[HOLD ? D / 8 : 1];
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) held[i] = src[i];
+  }
   if constexpr (KV8) {
     const float ks = fabsf(p.k_scale[kvh]);
     neg = neg != (p.k_scale[kvh] < 0.f);
@@ -201,9 +236,9 @@ __device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const 
       // from mantissas and exponents, so that no step of it leaves float32's
       // range unless the whole does.
       float amax = 0.f;
-#pragma unroll 4
+#pragma unroll(HOLD ? D / 8 : 4)
       for (int i = 0; i < D / 8; ++i) {
-        const uint4 x = src[i];
+        const uint4 x = HOLD ? held[HOLD ? i : 0] : src[i];
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -222,7 +257,7 @@ __device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const 
   }
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {  // (all loads in flight)
-    const uint4 x = src[i];
+    const uint4 x = HOLD ? held[HOLD ? i : 0] : src[i];
     uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -528,12 +563,19 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
     fence_mbar_init();
     *reinterpret_cast<int*>(smem + Cfg::kFlagOff) = 0;
     if constexpr (WIN) {
-      edges->first = base_pos + r0 / G;
       edges->last = span.last;
       edges->w0 = span.w0;
       edges->s0 = span.s0;
       edges->head = span.head;
       edges->skip = span.skip;
+      edges->tile0 = tile0;
+      edges->tiles = n_tiles;
+      edges->pos0 = base_pos;
+      const WindowEdge at = window_edge(p, base_pos + r0 / G, span.last, (int64_t)span.skip * KT,
+                                        (int64_t)tile0 * KT);
+      edges->at.left0 = at.left0;
+      edges->at.left1 = at.left1;
+      edges->at.right = at.right;
     }
   }
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + Cfg::kTmemOff);
@@ -551,10 +593,15 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
   // Q row while the first tiles are on their way.
   const int t = warp >> 2, rr = (warp & 3) * 32 + lane, r = t * 128 + rr;
   const bool softmax = warp < Cfg::kSoftmaxWarps && (warp & 3) < tile_warps(t);
+  [[maybe_unused]] auto sees = [&](int j) {  // keys of a tile that this thread's row sees
+    if constexpr (WIN)
+      return window_mask(p, edges->pos0 + (r0 + min(r, nr - 1)) / G, edges->pos<KT>(j));
+    else return 0ull;
+  };
   float qscale = 1.f;
   if (softmax) {
     unsigned char* qt = smem + t * Cfg::kQBytes;
-    qscale = bring_row<T, D, KV8>(p, kvh, static_cast<const T*>(p.q) + row_at(min(r, nr - 1)), qt, rr);
+    qscale = bring_row<T, D, KV8, KV8 && QT == 2 && std::is_same<T, __nv_bfloat16>::value>(p, kvh, static_cast<const T*>(p.q) + row_at(min(r, nr - 1)), qt, rr);
     fence_proxy_async_smem();
     mbar_arrive(q_full);
   }
@@ -687,6 +734,8 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
       RingPos<RAW> from;
       int slot = 0;
       uint32_t phase = 0;
+      WindowEdge at_edge{};
+      if constexpr (WIN) at_edge = {edges->at.left0, edges->at.left1, edges->at.right};
       for (int j = 0; j < n_tiles; ++j) {
         bool ok = mbar_wait(raw_full(which, from.slot), from.phase);
         if (ok && j >= slots) ok = mbar_wait(empties + 8u * slot, phase ^ 1u);
@@ -697,9 +746,9 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
         const unsigned char* raw = smem + Cfg::kRawOff + (which * RAW + from.slot) * Cfg::kRawBytes;
         unsigned char* const wide = ring + slot * Cfg::kTileBytes;
         if constexpr (WIN) {
-          const int t0 = edges->pos<KT>(tile0 + j);
-          if (which && edges->edge<KT>(p, t0)) {
-            const bool met = widen_tile<KT, Cfg::kConvThreads, true>(raw, wide, KT, ct, edges->seen(t0));
+          if (which && at_edge(j)) {
+            const uint64_t seen = edges->seen(edges->pos<KT>(j));
+            const bool met = widen_tile<KT, Cfg::kConvThreads, true>(raw, wide, KT, ct, seen);
             const bool any = __any_sync(kFullMask, met);
             if (lane == 0) dirty[2 * slot + (ct >> 5)] = any;
             __syncwarp();
@@ -724,19 +773,17 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
     const uint32_t base = tmem + t * Cfg::kTileCols + ((uint32_t)((warp & 3) * 32) << 16);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    // With a window: the row's position, the last edge tile with values that are
-    // not finite (-1: none waits).
-    [[maybe_unused]] const int pos = base_pos + (r0 + min(r, nr - 1)) / G;
-    [[maybe_unused]] int odd = -1;
+    // With a window: the edge tile had values cleared.
+    [[maybe_unused]] bool odd = false;
     // Adds that tile's cleared values to O, once its product is in.
-    [[maybe_unused]] auto add_odd = [&] {
+    [[maybe_unused]] auto add_odd = [&](int j) {
       const int bs = b;
       int t0 = 0;
       uint64_t seen = 0, sees_keys = 0;
       if constexpr (WIN) {
-        t0 = edges->pos<KT>(tile0 + odd);
+        t0 = edges->pos<KT>(j);
         seen = edges->seen(t0);
-        sees_keys = window_mask(p, pos, t0);
+        sees_keys = sees(j);
       }
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
@@ -758,30 +805,27 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
         }
         tmem_st32(base + Cfg::kOCol + q * 32, o);
       }
-      odd = -1;
     };
-    for (int j = 0; j < n_tiles; ++j) {
+    // One tile; EDGE: masked.  With a window there are two copies, so that the one that
+    // most tiles take has no more in it than it needs.
+    auto one = [&](auto edge_tag, int j) {
+      constexpr bool EDGE = decltype(edge_tag)::value;
       ok = mbar_wait(s_full(t, j % NS), (uint32_t)((j / NS) & 1));
       if (__any_sync(kFullMask, !ok)) {
         ok = false;
-        break;
+        return;
       }
       tc_fence_after();
       const uint32_t sp = base + (j % NS) * KT;
       uint32_t w[KT];
       tmem_ld64(sp, w);
-      [[maybe_unused]] bool edge = false;
-      if constexpr (WIN) {
-        const int t0 = edges->pos<KT>(tile0 + j);
-        edge = edges->edge<KT>(p, t0);
-        if (edge) {
-          const uint64_t sees = window_mask(p, pos, t0);
-          const uint32_t s0 = (uint32_t)sees, s1 = (uint32_t)(sees >> 32);
+      if constexpr (EDGE) {
+        const uint64_t mine = sees(j);
+        const uint32_t s0 = (uint32_t)mine, s1 = (uint32_t)(mine >> 32);
 #pragma unroll
-          for (int k = 0; k < KT; ++k)
-            if (!((k < 32 ? s0 : s1) >> (k & 31) & 1u)) w[k] = __float_as_uint(-INFINITY);
-        }
-      } else {
+        for (int k = 0; k < KT; ++k)
+          if (!((k < 32 ? s0 : s1) >> (k & 31) & 1u)) w[k] = __float_as_uint(-INFINITY);
+      } else if constexpr (!WIN) {
         const int valid = hi - lo - j * KT;
         if (valid < KT) {
 #pragma unroll
@@ -829,21 +873,18 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
       const float2 sx = __fadd2_rn(s01, s23);
       l += sx.x + sx.y;
       tmem_st32(sp, pk);
-      [[maybe_unused]] bool met = false;
-      if constexpr (WIN) {
-        if (edge) {
-          ok = mbar_wait(v_full(j % NV), (uint32_t)((j / NV) & 1));
-          if (__any_sync(kFullMask, !ok)) {
-            ok = false;
-            break;
-          }
-          met = dirty[2 * (j % NV)] != 0 || dirty[2 * (j % NV) + 1] != 0;
-        }
-      } else if (!KV8 && hi - lo - j * KT < KT) {  // (the last tile)
+      if constexpr (EDGE) {
         ok = mbar_wait(v_full(j % NV), (uint32_t)((j / NV) & 1));
         if (__any_sync(kFullMask, !ok)) {
           ok = false;
-          break;
+          return;
+        }
+        odd = dirty[2 * (j % NV)] != 0 || dirty[2 * (j % NV) + 1] != 0;
+      } else if (!WIN && !KV8 && hi - lo - j * KT < KT) {  // (the last tile)
+        ok = mbar_wait(v_full(j % NV), (uint32_t)((j / NV) & 1));
+        if (__any_sync(kFullMask, !ok)) {
+          ok = false;
+          return;
         }
         clear_tail<D, KT>(smem + Cfg::kVRingOff + (j % NV) * Cfg::kTileBytes, hi - lo - j * KT, b, rr,
                           32 * tile_warps(t));
@@ -854,7 +895,7 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
         ok = mbar_wait(o_done(t), (uint32_t)((j - 1) & 1));
         if (__any_sync(kFullMask, !ok)) {
           ok = false;
-          break;
+          return;
         }
         tc_fence_after();
       }
@@ -868,12 +909,32 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
           tmem_st32(base + Cfg::kOCol + q * 32, o);
         }
       }
-      if constexpr (WIN) {
-        if (odd >= 0) add_odd();
-        if (met) odd = j;
-      }
       tc_fence_before();
       mbar_arrive(p_full(t, j % NS));
+    };
+    if constexpr (WIN) {
+      for (int j = 0; j < edges->tiles && ok;) {  // (a bound looked up in every tile: 9 of 111 us)
+        const WindowEdge at{edges->at.left0, edges->at.left1, edges->at.right};
+        const int end = min(edges->tiles, at.run(j));
+        if (!at(j)) {
+          for (; j < end && ok; ++j) one(std::false_type{}, j);
+          continue;
+        }
+        for (; j < end && ok; ++j) {
+          one(std::true_type{}, j);
+          if (!ok || !odd) continue;
+          ok = mbar_wait(o_done(t), (uint32_t)(j & 1));
+          if (__any_sync(kFullMask, !ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          add_odd(j);
+          tc_fence_before();
+        }
+      }
+    } else {
+      for (int j = 0; j < n_tiles && ok; ++j) one(std::false_type{}, j);
     }
     if (ok) {
       ok = mbar_wait(o_last(t), 0);
@@ -890,9 +951,6 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
     const bool whole = c.parts == 1;
     if (ok) {
       tc_fence_after();
-      if constexpr (WIN) {
-        if (odd >= 0) add_odd();
-      }
       // l = 0: every score was -inf.  A row of such scores is 0 / 0 (NaN); a
       // part of them leaves O as it is, NaN where a value was not finite, and
       // weighs nothing in the merge.

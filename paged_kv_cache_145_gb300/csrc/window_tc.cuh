@@ -48,21 +48,12 @@ struct WindowItem {
   int w0, s0;             // seen by some row: t < s0, and w0 <= t <= last
   int key0;               // first packed key (of the item's part)
   int head, skip;         // packed keys of the sinks; positions left out behind them
-  // Tiles in which some row does not see some key: those before the window's last
-  // start, unless the sinks cover them, and those behind the first row.
-  int left0, left1, right;
+  int left0, left1, right;  // WindowEdge
 };
 
-// Whether a tile is one of them (looked up once an item: 110 us of 383 went into
-// finding it out in every tile).
-struct WindowEdge {
-  int left0, left1, right;
-  __device__ __forceinline__ explicit WindowEdge(const volatile WindowItem* it)
-      : left0(it->left0), left1(it->left1), right(it->right) {}
-  __device__ __forceinline__ bool operator()(int j) const {
-    return (j >= left0 && j < left1) || j >= right;
-  }
-};
+__device__ __forceinline__ WindowEdge item_edge(const volatile WindowItem* it) {
+  return {it->left0, it->left1, it->right};
+}
 
 // Packed key v is position v, or v + skip behind the sinks' pages.
 struct WindowKeys {
@@ -280,7 +271,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
       if (i < 0) return;
       const volatile WindowItem* const it = items + i % NI;
       const int count = it->tiles;
-      const WindowEdge edge(it);
+      const WindowEdge edge = item_edge(it);
       const int half = min(count, edge.right);
       for (int j = end ? half : 0; j < (end ? count : half); ++j, ++tiles, va.next()) {
         if (!edge(j)) continue;
@@ -369,14 +360,10 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         it.key0 = it.part * p.part;
         const int keys = (it.last / page + 1) * page - it.skip - it.key0;
         it.tiles = (min(keys, p.part) + KT - 1) / KT;
-        // A tile starts at key v = key0 + 64 j, position v + skip (in the sinks'
-        // tiles, v): v + 64 <= sinks is seen by all; v + skip <= last - window is
-        // not; nor is v + skip + 63 > first.  (The sinks' tiles that pass for
-        // starting before the window's end are all of them but those.)
-        auto tiles_below = [&](int64_t v) { return (int)min((int64_t)1 << 30, max((int64_t)0, v >> 6)); };
-        it.left0 = tiles_below((int64_t)p.sinks - it.key0);
-        it.left1 = tiles_below((int64_t)it.last - p.window - it.skip - it.key0 + 64);
-        it.right = tiles_below((int64_t)it.first + 1 - it.skip - it.key0);
+        const WindowEdge edge = window_edge(p, it.first, it.last, it.skip, it.key0);
+        it.left0 = edge.left0;
+        it.left1 = edge.left1;
+        it.right = edge.right;
         if (keys > 0) break;
         // a row tile with fewer parts than the sequence: an empty part
         for (int r = 0; r < it.nr; ++r) {
@@ -589,7 +576,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
         ok = mbar_wait(ready(n % NI), (uint32_t)((n / NI) & 1), patience);
         if (!ok || it->tiles < 0) break;
         const int tiles = it->tiles;
-        const WindowEdge edge(it);
+        const WindowEdge edge = item_edge(it);
         for (int j = 0; j < tiles && ok; ++j) {
           if (made == done) {  // the first tile of all, or of an item after a short one
             if (left == 0) next_item(true);
@@ -658,7 +645,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
       }
       const int tiles = it->tiles;
       if (tiles < 0) break;
-      const WindowEdge at_edge(it);
+      const WindowEdge at_edge = item_edge(it);
       const bool live = warp * 32 < it->nr;  // the warp has rows
       const int pos = it->pos0 + (it->r0 + min(rr, it->nr - 1)) / G;
       float m = -INFINITY, l = 0.f;
