@@ -42,8 +42,8 @@
 // of 256 rows, although that reads each K and V tile half as often.  Measured
 // (8 sequences of 2048 queries over 2000-6400 states, bf16, 32/8 heads of 128):
 // 792 us (1477 TFLOP/s) with two blocks of 128 rows (784 before scores of minus
-// infinity were provided for); one block of 256 rows with 128-key tiles and one
-// S buffer took 883.  Few rows: HBM, and below some megabytes per SM the fixed
+// infinity were provided for; 2% less since rows come and go by warps, below); one
+// block of 256 rows with 128-key tiles and one S buffer took 883.  Few rows: HBM, and below some megabytes per SM the fixed
 // costs of a block (4 us from launch to first tile and last tile to end).  Copies and MMAs are issued by one elected thread
 // each: an operand in a uniform register costs several instructions to fill,
 // and lanes that each issue one do it one after the other (a copy costs its
@@ -52,6 +52,15 @@
 // tile costs more than the chain (8 x 300-512 queries over 1000-4000 states,
 // 32/8 heads of 128: 150 us, 215 with blocks of 128 rows).  All four converter
 // warps for keys and values in turn took 195 us where two for each took 164.
+// Query and output rows go through shared memory, a row's units in neighbouring
+// lanes: a lane a row took 151 us there, this 142, and bf16 8 x 2048 642, this 628
+// (over 2048-6400 states, another draw).
+//
+// With a window, FP8, 8 x 300-512 queries, window 1500, 32/8 heads of 128: 98 us
+// (153 with blocks of 128 rows).  A block of 14 tiles takes 25 us: 2 until its
+// barriers and tensor memory are there, 4 for the queries, 1 to the first scores,
+// 1.2 a tile at the window's edges and 0.75 else, 2 for the output; one block on
+// an SM, nothing hides the first and the last of these.
 //
 // Tensor memory per row tile: two buffers of S (64 columns each, P in the first
 // 32), then O (D columns).  Every wait is bounded.
@@ -207,23 +216,52 @@ __device__ __forceinline__ uint32_t zero_pair(uint32_t w) {
   return ((w & kExp) == kExp ? 0x7FFFu : 0u) | ((w & kExp << 16) == kExp << 16 ? 0x7FFF0000u : 0u);
 }
 
-// A thread's Q row, from global memory into row rr of a 128-row tile in the
-// 128-byte-swizzled operand layout; returns the factor that makes its
-// products scores in base-2 units (never negative: the sign of the scale goes
-// into Q, exactly, so that the largest score has the largest product).  HOLD: the
-// row stays in registers between its largest element and its conversion.
-template <typename T, int D, bool KV8, bool HOLD>
-__device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const T* row,
+// Where 16-byte unit c of row rr lies in a 128-row tile, 128-byte-swizzled.
+__device__ __forceinline__ unsigned char* row_unit(unsigned char* tile, int rr, int c) {
+  return tile + (c >> 3) * 128 * 128 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
+}
+
+// Moves a warp's 32 rows (at lane's `row`: element offset of row r0 + lane) between
+// global memory and its rows of a tile, a row's units in neighbouring lanes: a lane
+// a row, each load would touch 32 lines.
+template <int D, typename F>
+__device__ __forceinline__ void warp_rows(int64_t row, int r0, int lane, F f) {
+  constexpr int U = D / 8;  // units of a row
+  const int c = lane % U;
+  const int64_t first = __shfl_sync(kFullMask, row, 0);
+  const int behind = (int)(row - first);  // (32 rows: within 32 queries)
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int r = i * (32 / U) + lane / U;
+    f(first + __shfl_sync(kFullMask, behind, r) + c * 8, r0 + r, c);
+  }
+}
+
+// A thread's Q row (element offset `row`), from global memory into row rr of a
+// 128-row tile in the 128-byte-swizzled operand layout, a warp's rows together;
+// returns the factor that makes its products scores in base-2 units (never
+// negative: the sign of the scale goes into Q, exactly, so that the largest score
+// has the largest product).
+template <typename T, int D, bool KV8>
+__device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, int64_t row,
                                            unsigned char* tile, int rr) {
-  const uint4* src = reinterpret_cast<const uint4*>(row);
+  const int lane = rr & 31;
+  uint4 x[D / 8];  // (all loads in flight)
+  {
+    int i = 0;
+    warp_rows<D>(row, rr & ~31, lane, [&](int64_t at, int, int) {
+      x[i++] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + at);
+    });
+  }
   bool neg = p.qscale < 0.f;
   float shift = 1.f, qscale = fabsf(p.qscale);
-  // A row's loads are all in flight before the first is used.
-  [[maybe_unused]] uint4 held[HOLD ? D / 8 : 1];
-  if constexpr (HOLD) {
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) held[i] = src[i];
+  {
+    int i = 0;
+    warp_rows<D>(row, rr & ~31, lane, [&](int64_t, int r, int c) {
+      *reinterpret_cast<uint4*>(row_unit(tile, r, c)) = x[i++];
+    });
   }
+  __syncwarp();
   if constexpr (KV8) {
     const float ks = fabsf(p.k_scale[kvh]);
     neg = neg != (p.k_scale[kvh] < 0.f);
@@ -236,10 +274,10 @@ __device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const 
       // from mantissas and exponents, so that no step of it leaves float32's
       // range unless the whole does.
       float amax = 0.f;
-#pragma unroll(HOLD ? D / 8 : 4)
+#pragma unroll 4
       for (int i = 0; i < D / 8; ++i) {
-        const uint4 x = HOLD ? held[HOLD ? i : 0] : src[i];
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const uint4 y = *reinterpret_cast<const uint4*>(row_unit(tile, rr, i));
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[k] << 16)),
@@ -255,19 +293,21 @@ __device__ __forceinline__ float bring_row(const CrossParams& p, int kvh, const 
       qscale = ldexpf(mq * mk, eq + ek - e);
     }
   }
+  if ((KV8 && std::is_same<T, __nv_bfloat16>::value) || neg) {
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+      uint4* const at = reinterpret_cast<uint4*>(row_unit(tile, rr, i));
+      const uint4 y = *at;
+      uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {  // (all loads in flight)
-    const uint4 x = HOLD ? held[HOLD ? i : 0] : src[i];
-    uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if constexpr (KV8 && std::is_same<T, __nv_bfloat16>::value)
-        w[k] = pack_pair<__half>(__uint_as_float(w[k] << 16) * shift,
-                                 __uint_as_float(w[k] & 0xFFFF0000u) * shift);
-      if (neg) w[k] ^= 0x80008000u;
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (KV8 && std::is_same<T, __nv_bfloat16>::value)
+          w[k] = pack_pair<__half>(__uint_as_float(w[k] << 16) * shift,
+                                   __uint_as_float(w[k] & 0xFFFF0000u) * shift);
+        if (neg) w[k] ^= 0x80008000u;
+      }
+      *at = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    *reinterpret_cast<uint4*>(tile + (i >> 3) * 128 * 128 + rr * 128 +
-                              (((i & 7) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   if (qscale == 0.f) {
     // A zero scale goes into the queries, so that hidden keys stay at -inf.
@@ -601,7 +641,7 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
   float qscale = 1.f;
   if (softmax) {
     unsigned char* qt = smem + t * Cfg::kQBytes;
-    qscale = bring_row<T, D, KV8, KV8 && QT == 2 && std::is_same<T, __nv_bfloat16>::value>(p, kvh, static_cast<const T*>(p.q) + row_at(min(r, nr - 1)), qt, rr);
+    qscale = bring_row<T, D, KV8>(p, kvh, row_at(min(r, nr - 1)), qt, rr);
     fence_proxy_async_smem();
     mbar_arrive(q_full);
   }
@@ -963,7 +1003,7 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
         uint32_t w[32];
         tmem_ld32(base + Cfg::kOCol + q * 32, w);
         auto o = [&](int d) { return bad ? 0.f : __uint_as_float(w[d]) * inv; };
-        if (r < nr && whole) {
+        if (whole) {  // over the queries, whose products are done
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint4 u;
@@ -971,7 +1011,7 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
             u.y = pack_pair<T>(o(8 * v + 2), o(8 * v + 3));
             u.z = pack_pair<T>(o(8 * v + 4), o(8 * v + 5));
             u.w = pack_pair<T>(o(8 * v + 6), o(8 * v + 7));
-            reinterpret_cast<uint4*>(out + at)[q * 4 + v] = u;
+            *reinterpret_cast<uint4*>(row_unit(smem + t * Cfg::kQBytes, rr, q * 4 + v)) = u;
           }
         } else if (r < nr) {
 #pragma unroll
@@ -979,6 +1019,14 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
             reinterpret_cast<float4*>(p.ws_o + wrow * D)[q * 8 + v] =
                 make_float4(o(4 * v), o(4 * v + 1), o(4 * v + 2), o(4 * v + 3));
         }
+      }
+      if (whole) {
+        __syncwarp();
+        warp_rows<D>(at, rr & ~31, lane, [&](int64_t to, int row, int c) {
+          if (t * 128 + row < nr)
+            *reinterpret_cast<uint4*>(out + to) =
+                *reinterpret_cast<const uint4*>(row_unit(smem + t * Cfg::kQBytes, row, c));
+        });
       }
     }
   }
