@@ -262,12 +262,28 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
 
   if (warp == Cfg::kScoutWarp) {
     // ---- scout ------------------------------------------------------------------
-    const int row_tiles = (int)(((int64_t)p.max_queries * G + 127) / 128);
-    const int groups = p.num_seqs * p.kv_heads;                 // (sequence, KV head)
-    const int64_t total = (int64_t)p.parts * groups * row_tiles;
+    // Items are numbered through the sequences (their parts, KV heads and row tiles;
+    // a refused one has an item a KV head) and dealt to the blocks in turn.  With
+    // numbers for row tiles that only the bound on the queries allows, 8 chunks of
+    // 300-512 queries took 137 us, this 118: some blocks had four items, others two.
+    int number = blockIdx.x, before = 0;  // the block's next item; items before seq0
+    int seq0 = 0, upto = 0;               // upto: items of the sequences seq0 .. seq0 + lane
+    CrossSeq mine{};                      // sequence seq0 + lane
+    auto count = [&] {
+      upto = 0;
+      if (seq0 + lane < p.num_seqs) {
+        mine = cross_seq(p, seq0 + lane);
+        upto = p.kv_heads * (mine.bits ? 1 : mine.parts * ((mine.Q * G + 127) / 128));
+      }
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(kFullMask, upto, d);
+        if (lane >= d) upto += x;
+      }
+    };
+    count();
     int n = 0, tiles = 0, edges = 0;  // items, tiles and edge tiles so far
     RingPos<NV> va;
-    int64_t idx = blockIdx.x;
     bool ok = true;
     // The values of item i's edge tiles, those at the start of its keys and then
     // those at the end: the next item is seen to in between, when no product waits
@@ -309,49 +325,38 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
       WindowItem it;
       CrossSeq c;
       it.tiles = -1;
-      for (; idx < total; idx += gridDim.x) {
-        const int64_t group = idx / row_tiles;
-        const int tile = (int)(idx - group * row_tiles);
-        it.part = (int)(group / groups);
-        const int g = (int)(group - (int64_t)it.part * groups);
-        it.seq = g / p.kv_heads;
-        it.kvh = g - it.seq * p.kv_heads;
-        c = cross_seq(p, it.seq);
+      for (;; number += gridDim.x) {
+        int all = __shfl_sync(kFullMask, upto, 31);
+        while (number >= before + all && seq0 + 32 < p.num_seqs) {
+          before += all;
+          seq0 += 32;
+          count();
+          all = __shfl_sync(kFullMask, upto, 31);
+        }
+        if (number >= before + all) break;
+        const int hit = __popc(__ballot_sync(kFullMask, before + upto <= number));
+        const int past = hit ? __shfl_sync(kFullMask, upto, hit - 1) : 0;
+        const int at = number - before - past;  // of the sequence's items
+        it.seq = seq0 + hit;
+        c.q0 = __shfl_sync(kFullMask, mine.q0, hit);
+        c.Q = __shfl_sync(kFullMask, mine.Q, hit);
+        c.L = __shfl_sync(kFullMask, mine.L, hit);
+        c.parts = __shfl_sync(kFullMask, mine.parts, hit);
+        c.bits = __shfl_sync(kFullMask, mine.bits, hit);
         T* const out = static_cast<T*>(p.out);
-        if (c.bits && tile == 0 && it.part == 0) {
+        if (c.bits) {
           if (lane == 0) set_error(p.err, c.bits);
-          // the tiles cover max_queries rows only: this one zeroes them all
           const int units = G * D / 8;  // of 16 bytes, of a query's heads
           for (int64_t e = lane; e < (int64_t)c.Q * units; e += 32)
-            reinterpret_cast<uint4*>(out + ((c.q0 + e / units) * H + it.kvh * G) * D)[e % units] =
+            reinterpret_cast<uint4*>(out + ((c.q0 + e / units) * H + (int64_t)at * G) * D)[e % units] =
                 make_uint4(0u, 0u, 0u, 0u);
-        }
-        const int rows = c.bits ? 0 : c.Q * G;
-        it.r0 = tile * 128;
-        if (it.r0 >= rows || it.part >= c.parts) {
-          // None here nor in the rest of this group: on to the next one in which this
-          // block has a tile with rows, or a sequence to refuse, a group per lane
-          // (max_queries may be far above what most sequences have).
-          int64_t next = total;
-          for (int64_t g0 = group + 1; g0 * row_tiles < total; g0 += 32) {
-            const int64_t start = (g0 + lane) * row_tiles;
-            const int64_t off = (idx - start) % (int64_t)gridDim.x;
-            const int64_t at = off < 0 ? off + gridDim.x : off;  // the block's first tile there
-            bool some = false;
-            if (start < total && at < row_tiles) {
-              const int of = (int)((g0 + lane) / groups);
-              const CrossSeq o = cross_seq(p, (int)((g0 + lane) % groups) / p.kv_heads);
-              some = o.bits ? at == 0 && of == 0 : at * 128 < (int64_t)o.Q * G && of < o.parts;
-            }
-            const unsigned hits = __ballot_sync(kFullMask, some);
-            if (hits) {
-              next = __shfl_sync(kFullMask, start + at, __ffs(hits) - 1);
-              break;
-            }
-          }
-          idx = next - gridDim.x;
           continue;
         }
+        const int rows = c.Q * G, row_tiles = (rows + 127) / 128;
+        const int run = at / row_tiles;
+        it.part = run / p.kv_heads;
+        it.kvh = run - it.part * p.kv_heads;
+        it.r0 = (at - run * row_tiles) * 128;
         it.q0 = c.q0;
         it.nr = min(128, rows - it.r0);
         it.whole = c.parts == 1;
@@ -449,7 +454,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
       }
       if (ok) look_over(n, false);
       ++n;
-      idx += gridDim.x;
+      number += gridDim.x;
     }
   } else if (warp == Cfg::kKeyWarp || warp == Cfg::kValueWarp) {
     // ---- producers ----------------------------------------------------------------
@@ -866,8 +871,12 @@ int launch_window_tc(const WindowParams& p, const WindowMaps& maps, int sms, cud
       return pkv_cuda_failed();
     ready.fetch_or(bit);
   }
-  const int64_t row_tiles = ((int64_t)p.max_queries * p.group + 127) / 128;
-  const int64_t items = row_tiles * p.num_seqs * p.kv_heads * p.parts;
+  // No more items than this (a sequence's last row tile is not full).
+  const int64_t row_tiles = std::min(((int64_t)p.max_queries * p.group + 127) / 128 * p.num_seqs,
+                                     p.total_queries * p.group / 128 + p.num_seqs);
+  const int64_t items = row_tiles * p.kv_heads * p.parts;
+  // Items and a sequence's rows are numbered in 32 bits.
+  if (items > (1 << 30) || p.total_queries * p.group > INT32_MAX) return PKV_ERR_ARG;
   const int64_t grid = items < 2 * (int64_t)sms ? items : 2 * (int64_t)sms;
   kern<<<(unsigned)grid, Cfg::kThreads, Cfg::kSmemBytes, stream>>>(p, maps);
   return launch_cross_merge<T, D>(p, p.num_seqs, stream);
