@@ -265,6 +265,20 @@ def test_steps_that_cannot_be_taken_change_nothing():
     step(m, [0, 0, 2, 3, 1])
 
 
+def test_no_rows_before_or_after():
+    """Rows that begin empty, and a step after which there are none."""
+    m = Model(40, 16, 5, seed=31, head=11)
+    step(m, [])                                      # none, and none next
+    step(m, [-1, -1, -1])
+    assert m.lens == [0, 0, 0]
+    m = Model(40, 16, 5, seed=32, head=11)
+    for n in (33, 80, 1):
+        m.admit(n)
+    step(m, [0, 0, 1, 1, 2])
+    step(m, [])
+    assert sorted(m.free) == list(range(40))
+
+
 def test_captured_steps_in_place():
     """A captured step that swaps its two sets of tables, replayed."""
     m = Model(200, 16, 8, seed=9)

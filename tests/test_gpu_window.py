@@ -273,6 +273,74 @@ def test_scales(dtype, Q):
         c.check(c.call())
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Q", [1, 40, 150])
+@pytest.mark.parametrize("io", [F16, BF16])
+def test_pool_scales_of_either_sign_and_zero(Q, D, io):
+    """FP8 pools whose heads' scales are negative, zero and ordinary."""
+    c = Case([Q, Q], [400, Q + 7], 12, 3, D, 90, 20, FP8, io, 16, seed=Q)
+    c.ks[0], c.ks[1], c.vs[1], c.vs[2] = -c.ks[0], 0.0, -c.vs[1], 0.0
+    c.check(c.call())
+    assert pkv.paged_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (F16, 128), (FP8, 128)])
+@pytest.mark.parametrize("Q", [1, 200])
+def test_a_table_of_millions_of_positions(Q, dtype, D):
+    """Four million positions in three blocks, named again and again.  A row adds
+    P.V in steps of 16 positions, and its sum in runs of 64: L / 16 + 64 additions
+    in place of L + 16 in the tolerance."""
+    L, b, H = 1 << 22, 16, 4
+    c = Case([0], [0], H, 1, D, 2 ** 31 - 1, 0, dtype, io_of(dtype), b, seed=Q)
+    g = torch.Generator().manual_seed(Q)
+    table = torch.randint(0, 3, (L // b,), generator=g).to(torch.int32)
+    kv = [torch.randn(3, 1, b, D, generator=g) for _ in range(2)]
+    if dtype == FP8:
+        kv = [(x * 100).clamp(-448, 448) for x in kv]
+    c.kv = [x.to(dtype) for x in kv]
+    c.q = torch.randn(Q, H, D, generator=g).to(c.io)
+    c.starts, c.tables, c.lens, c.qlens = np.array([0, Q], dtype=np.int32), table[None], [L], [Q]
+    out = c.call().cpu().double()
+    assert pkv.paged_get_device_error() == 0
+    k, v = (x.float().double().reshape(3 * b, D) for x in c.kv)
+    if dtype == FP8:
+        k, v = k * c.ks.double(), v * c.vs.double()
+    z = torch.einsum("qhd,nd->qhn", c.q.double(), k) * c.scale
+    # how often a query sees each of the 48 rows
+    row = (table.long()[:, None] * b + torch.arange(b)).reshape(-1)
+    one = torch.nn.functional.one_hot(row[L - Q + 1:], 3 * b).double()
+    seen = torch.bincount(row[:L - Q + 1], minlength=3 * b).double() + torch.cat(
+        [torch.zeros(1, 3 * b, dtype=torch.double), one.cumsum(0)])
+    w = torch.exp(z - z.amax(2, keepdim=True)) * seen[:, None]
+    w /= w.sum(2, keepdim=True)
+    ref, mass = torch.einsum("qhn,nd->qhd", w, v), torch.einsum("qhn,nd->qhd", w, v.abs())
+    dz = torch.einsum("qhd,nd->qhn", c.q.double().abs(), k.abs()).amax(2) * c.scale * (D + 4) * 2.0 ** -24
+    rel = half(F16 if dtype == FP8 else dtype) + 2 * dz[..., None] + 2.0 ** -20 + \
+        2 * (L / 16 + 64) * 2.0 ** -24
+    err = (out - ref).abs()
+    assert (err <= half(c.io) * ref.abs() + mass * rel * (1 + half(c.io))).all(), float(err.max())
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+def test_calls_at_once(dtype):
+    """Chunks and tokens on two streams at a time, each with its own workspace."""
+    cases = [Case([300, 40, 129], [900, 700, 129], 8, 2, 128, 200, 3, dtype, io_of(dtype), seed=1),
+             Case([1] * 6, [900, 70, 1, 2000, 333, 64], 8, 2, 128, 700, 3, dtype, io_of(dtype), seed=2)]
+    data = [(c.cache(), c.call()) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for i, (c, st) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(st):
+                outs[i].append(c.call(data[i][0]))
+    torch.cuda.synchronize()
+    assert pkv.paged_get_device_error() == 0
+    for (_, first), got in zip(data, outs):
+        for o in got:
+            assert torch.equal(o.view(torch.uint8), first.view(torch.uint8))
+
+
 def test_rows_behind_the_last_sequence_stay():
     for Q in (1, 20):
         c = Case([Q, 0, Q], [90, 10, 300], 4, 2, 64, 40, 2, F16, extra_rows=5, seed=1)
