@@ -631,8 +631,9 @@ int paged_block_swap(const pkv_cache* cache, void* host_k, void* host_v, int64_t
  *   - entries from query_starts[num_seqs] up to max_tokens are padding: slot
  *     -1, position 0.
  * The outputs feed paged_kv_write, paged_rope_kv_write and the attention
- * calls as they are.  Every block belongs to one row: tables with shared
- * blocks (forks) are the host block manager's.
+ * calls as they are.  Every block belongs to one row; rows that share blocks
+ * (forks) are the host block manager's, or paged_fork_tables's: these may grow
+ * here, and end there.
  *
  * All or nothing: if the free blocks do not cover the step (PKV_DEV_NOMEM),
  * the new tokens exceed max_tokens (PKV_DEV_TOKENS), a length is outside
@@ -710,10 +711,10 @@ int paged_build_tables(int64_t num_blocks, int32_t block_size, int32_t* free_lis
  *   block_tables    device, int32[num_seqs][max_blocks_per_seq]
  *   seq_lens        device, int32[num_seqs]
  *   tables_out      device, int32[num_next][max_blocks_per_seq], apart from
- *                   block_tables
- *   lens_out        device, int32[num_next], apart from seq_lens
- *   extra_out       device, int32[num_blocks]; may be extra_refs
- *   state_out       device, int64[2]; may be free_state
+ *                   the inputs
+ *   lens_out        device, int32[num_next], apart from the inputs
+ *   extra_out       device, int32[num_blocks]; may be extra_refs, else apart
+ *   state_out       device, int64[2]; may be free_state, else apart
  *   window, sinks   window 0: nothing is given back for a window
  *   workspace       device, >= paged_fork_tables_workspace_bytes(...) bytes,
  *                   16-byte aligned; calls that may overlap need one each
@@ -751,10 +752,10 @@ int paged_fork_tables(const pkv_cache* cache, int32_t* free_list, const int64_t*
  * moved_to[x] = x, and the outputs are the inputs.
  *
  *   free_list       device, int32[num_blocks], rewritten in place
- *   tables_out      device, as block_tables; may be block_tables
- *   extra_out       device, int32[num_blocks]; may be extra_refs
- *   state_out       device, int64[2]; may be free_state
- *   moved_to        device, int32[num_blocks]
+ *   tables_out      device, as block_tables; may be block_tables, else apart
+ *   extra_out       device, int32[num_blocks]; may be extra_refs, else apart
+ *   state_out       device, int64[2]; may be free_state, else apart
+ *   moved_to        device, int32[num_blocks], apart from the inputs
  *   workspace       device, >= paged_compact_workspace_bytes(num_blocks) bytes,
  *                   16-byte aligned; calls that may overlap need one each
  * and the rest, and the bounds, as for paged_fork_tables.

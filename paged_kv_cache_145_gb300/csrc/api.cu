@@ -982,6 +982,12 @@ size_t paged_fork_tables_workspace_bytes(int64_t num_blocks, int32_t num_seqs, i
   return pkv_fork_workspace(num_blocks, num_seqs, num_next, max_blocks_per_seq);
 }
 
+// Whether two arrays of 32-bit numbers share memory.
+static bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4 * (uintptr_t)nb && y < x + 4 * (uintptr_t)na;
+}
+
 // Checks that paged_fork_tables and paged_compact share.
 static int check_pages(const pkv_cache* cache, const void* free_list, const void* free_state,
                        const void* extra_refs, const void* tables, const void* lens,
@@ -1002,6 +1008,10 @@ static int check_pages(const pkv_cache* cache, const void* free_list, const void
     if (reinterpret_cast<uintptr_t>(x) & 3u) return PKV_ERR_ALIGN;
   for (const void* x : {free_state, state_out})
     if (reinterpret_cast<uintptr_t>(x) & 7u) return PKV_ERR_ALIGN;
+  // the same, or apart
+  if ((extra_out != extra_refs && overlap(extra_out, cache->num_blocks, extra_refs, cache->num_blocks)) ||
+      (state_out != free_state && overlap(state_out, 4, free_state, 4)))
+    return PKV_ERR_ARG;
   return aligned16(workspace) ? PKV_OK : PKV_ERR_ALIGN;
 }
 
@@ -1022,7 +1032,12 @@ int paged_fork_tables(const pkv_cache* cache, int32_t* free_list, const int64_t*
   if (num_next > 0 && (!parents || !tables_out || !lens_out)) return PKV_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(parents) & 3u) || (reinterpret_cast<uintptr_t>(lens_out) & 3u))
     return PKV_ERR_ALIGN;
-  if (num_next > 0 && (tables_out == block_tables || lens_out == seq_lens)) return PKV_ERR_ARG;
+  const int64_t next_entries = (int64_t)num_next * max_blocks_per_seq;
+  if (overlap(tables_out, next_entries, block_tables, (int64_t)num_seqs * max_blocks_per_seq) ||
+      overlap(tables_out, next_entries, parents, num_next) ||
+      overlap(tables_out, next_entries, seq_lens, num_seqs) ||
+      overlap(lens_out, num_next, seq_lens, num_seqs) || overlap(lens_out, num_next, parents, num_next))
+    return PKV_ERR_ARG;
   if (workspace_bytes <
       pkv_fork_workspace(cache->num_blocks, num_seqs, num_next, max_blocks_per_seq))
     return PKV_ERR_WORKSPACE;
@@ -1049,6 +1064,12 @@ int paged_compact(const pkv_cache* cache, int32_t* free_list, const int64_t* fre
   if (rc) return rc;
   if (!moved_to || (num_seqs > 0 && !tables_out)) return PKV_ERR_NULL;
   if (reinterpret_cast<uintptr_t>(moved_to) & 3u) return PKV_ERR_ALIGN;
+  const int64_t entries = (int64_t)num_seqs * max_blocks_per_seq;
+  if ((tables_out != block_tables && overlap(tables_out, entries, block_tables, entries)) ||
+      overlap(tables_out, entries, seq_lens, num_seqs) ||
+      overlap(moved_to, cache->num_blocks, extra_refs, cache->num_blocks) ||
+      overlap(moved_to, cache->num_blocks, block_tables, entries))
+    return PKV_ERR_ARG;
   if (workspace_bytes < pkv_compact_workspace(cache->num_blocks)) return PKV_ERR_WORKSPACE;
   if (!pkv_error_word()) return PKV_ERR_CUDA;
   return pkv_launch_compact(cache, elem_bytes(cache->dtype), free_list, free_state, extra_refs,

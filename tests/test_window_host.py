@@ -117,6 +117,10 @@ def test_fork_tables_argument_errors(lib):
     assert fork(lib, c, ws_bytes=lib.paged_fork_tables_workspace_bytes(32, 4, 3, 8) - 1) == -5
     assert fork(lib, c, tout=0x5000) == -3
     assert fork(lib, c, lout=0x6000) == -3
+    for kw in (dict(tout=0x5000 + 4 * 31), dict(tout=0x5000 - 4 * 23), dict(lout=0x600c),
+               dict(lout=0x4004), dict(tout=0x4008), dict(tout=0x5fa4), dict(eout=0x3000 + 4 * 31),
+               dict(sout=0x2008)):
+        assert fork(lib, c, **kw) == -3                           # in part over an input
     for kw in (dict(nxt=-1), dict(nxt=65536), dict(n=-1), dict(n=65536), dict(width=0), dict(win=-1),
                dict(sinks=-1), dict(n=60000, width=30000), dict(nxt=60000, width=30000)):
         assert fork(lib, c, **kw) == -3
@@ -136,6 +140,9 @@ def test_compact_argument_errors(lib):
     for name in ("ring", "state", "extra", "tables", "lens", "tout", "eout", "sout", "moved"):
         assert compact(lib, c, **{name: 0}) == -1
         assert compact(lib, c, **{name: 0x1002}) == -4
+    for kw in (dict(tout=0x5004), dict(tout=0x5000 - 4 * 31), dict(tout=0x6008), dict(eout=0x3004),
+               dict(sout=0x2008), dict(moved=0x3000), dict(moved=0x5000 + 4 * 31)):
+        assert compact(lib, c, **kw) == -3                        # in part over an input
     assert compact(lib, c, ws=0) == -5
     assert compact(lib, c, ws_bytes=lib.paged_compact_workspace_bytes(32) - 1) == -5
     for kw in (dict(n=-1), dict(n=65536), dict(width=0), dict(n=60000, width=30000)):
