@@ -64,6 +64,9 @@ __device__ __forceinline__ int block_sum(int x, int* scan) {
 }
 
 // ---- whole blocks, keys and values, within one pool ---------------------------
+// Measured (compaction of 192 rows and of 16, us): 512 threads of four vectors 136.4
+// and 12.4, 512 of eight 134.3 and 12.6, 256 of eight 136.4 and 12.5, 256 of sixteen
+// 132.4 and 13.4, 128 of sixteen 135.2 and 13.1.
 constexpr int kMoveThreads = 512;
 constexpr int kMoveUnroll = 4;
 constexpr int kMoveSlice = kMoveThreads * kMoveUnroll;  // 16-byte vectors of an item
