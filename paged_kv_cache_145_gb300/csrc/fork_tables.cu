@@ -67,7 +67,9 @@ struct ForkParams {
   int* from;                // [S]: copies
   int* to;
   unsigned* gone;           // [R][(W + 31) / 32]: entries whose blocks go back
-  int* totals;              // copies, error bits
+  // Copies; error bits of the inputs; error bits of the stages behind them.  A
+  // verdict is read between barriers that no writer of its word stands between.
+  int* totals;
 };
 
 constexpr int kForkThreads = 1024;
@@ -131,6 +133,7 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
     else __syncthreads();
   };
   auto fail = [&](unsigned bits) { atomicOr(p.totals + 1, (int)bits); };
+  auto fail_late = [&](unsigned bits) { atomicOr(p.totals + 2, (int)bits); };
   auto ring_at = [&](int64_t i) {
     const int64_t x = head + i;
     return x >= N ? x - N : x;
@@ -161,7 +164,7 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
     p.children[r] = 0;
     p.first[r] = INT_MAX;
   }
-  if (all < 2) p.totals[all] = 0;
+  if (all < 3) p.totals[all] = 0;
   if (p.extra_out != p.extra) {
     constexpr int C = 8;
     for (int x0 = all; x0 < N; x0 += C * threads) {
@@ -233,11 +236,11 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
     });
     if (tid == 0) p.totals[0] = taken;
     if (taken > count) {
-      if (tid == 0) fail(PKV_DEV_NOMEM);
+      if (tid == 0) fail_late(PKV_DEV_NOMEM);
     } else {
       for (int i = tid; i < taken; i += kForkThreads) {
         const int x = p.ring[ring_at(i)];
-        if (x < 0 || x >= N) fail(PKV_DEV_FREE_LIST);
+        if (x < 0 || x >= N) fail_late(PKV_DEV_FREE_LIST);
       }
     }
   }
@@ -298,7 +301,7 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
       for (int k = 0; k < U; ++k) left[k] = d[k] < 0 ? holders(x[k]) : 0;
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        if (left[k] < -1) fail(PKV_DEV_SHARING);
+        if (left[k] < -1) fail_late(PKV_DEV_SHARING);
         if (left[k] == -1) atomicMin(p.claim + x[k], entry_of(r, e0, k));
       }
     }, nothing);
@@ -331,6 +334,7 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
 
   // ---- what goes back, behind the tail -------------------------------------------------
   int given = 0;
+  unsigned bits = 0;
   if (ok) {
     // Blocks that the rows before this block's give back, and all rows.
     int before = 0;
@@ -341,11 +345,9 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
     }
     before = block_sum(before, s_scan);
     given = block_sum(given, s_scan);
-    ok = __ldcg(p.totals + 1) == 0;
-    if (given > N - count) {  // the ring holds a held block
-      if (all == 0) fail(PKV_DEV_FREE_LIST);
-      ok = false;
-    }
+    bits = (unsigned)__ldcg(p.totals + 2);
+    if (given > N - count) bits |= PKV_DEV_FREE_LIST;  // the ring holds a held block
+    ok = bits == 0;
     if (ok) {
       block_scan(r1 - r0, s_scan, p.first + r0, [&](int i) { return p.back[r0 + i]; });
       // (p.first is read no more as such: the copies' choice is in p.fresh's sums)
@@ -397,7 +399,7 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
   const int taken = ok ? __ldcg(p.totals) : 0;
   if (all == 0) {
     if (!ok) {
-      set_error(p.err, (unsigned)(__ldcg(p.totals + 1)));
+      set_error(p.err, bits | (unsigned)__ldcg(p.totals + 1));
       p.totals[0] = 0;
     }
     p.state_out[0] = ok ? ring_at(taken) : head;
