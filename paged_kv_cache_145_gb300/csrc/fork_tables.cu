@@ -4,8 +4,8 @@
 //
 // The mathematics.  Row r has c_r children (next rows that name it).  A child
 // keeps its parent's entries (with a window, those that a later query sees), so
-// an entry's block gains kept * c_r - 1 holders.  The partly filled last block
-// is written to next and must be its row's own: where it has one holder the
+// an entry's block loses a holder and gains kept * c_r.  The partly filled last
+// block is written to next and must be its row's own: where it has one holder the
 // first child keeps it, every other child takes a fresh block and a copy.  A
 // block whose holders come to none goes back; a block that several rows drop
 // goes back once, at the place of its first entry (rows in order, logical
@@ -13,8 +13,10 @@
 // ring's order does not depend on the order of the threads.
 //
 // All or nothing: the counts are added up before anything else is written, and
-// taken back (integer sums are exact in any order) if a block had fewer holders
-// than entries or the step fails otherwise.
+// taken back (integer sums are exact in any order) if the step fails.  Every
+// entry's hold is taken away before any is added: a block that more entries name
+// than it has holders then falls below none, whatever its rows' children would
+// add, and the entry that takes one too many sees it.
 //
 // What bounds it: latency.  One cluster (one block for few entries) does it in
 // five stages with a barrier between them; a grid-wide barrier would cost more
@@ -24,10 +26,11 @@
 // and one gather for each.  A second kernel, launched early, copies the blocks
 // over the whole GPU.
 //
-// Measured, 128 rows x 8 children of 124 entries, window: 34.6 us, 25.3 of them
-// without a block to copy (48.8 with eight blocks and one row at a time); 8 x 4
-// of 32 entries, one block: 16.2 us (19.3 with two rows at a time, whose second
-// is then empty).
+// Measured, 128 rows x 8 children of 124 entries, window: 37.3 us; 8 x 4 of 32
+// entries, one block: 17.1 us.  33.9 and 15.8 before the holds were taken away
+// apart from what the children add, an atomic with a result for every entry.  (Of
+// the first about 9 are copies; with eight blocks and one row at a time it took 14
+// more, the second with two rows at a time, whose second is then empty, 3 more.)
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -102,10 +105,10 @@ __device__ __forceinline__ bool fork_keeps(const ForkRow& w, int e) {
   return e >= w.near || e < w.far;
 }
 
-// Change of the holders of a row's entry e (of a block, not -1).
-__device__ __forceinline__ int fork_delta(const ForkRow& w, int e, int children, bool solo) {
-  if (e == w.partial) return solo && children > 0 ? 0 : -1;
-  return fork_keeps(w, e) ? children - 1 : -1;
+// Holders that the next rows add to a row's entry e (of a block, not -1).
+__device__ __forceinline__ int fork_gain(const ForkRow& w, int e, int children, bool solo) {
+  if (e == w.partial) return solo && children > 0;
+  return fork_keeps(w, e) ? children : 0;
 }
 
 // A lane's next kForkBatch entries of a row from e0 on (-1 past the row).
@@ -165,6 +168,13 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
     p.first[r] = INT_MAX;
   }
   if (all < 3) p.totals[all] = 0;
+  // (before holders are taken away: extra_out may be extra)
+  for (int r = r0 + tid; r < r1; r += kForkThreads) {
+    const int len = p.lens[r];
+    int x = -1;
+    if (len > 0 && len <= (int64_t)W * b && len % b) x = p.tables[(int64_t)r * W + len / b];
+    p.solo[r] = x >= 0 && x < N && p.extra[x] == 0;
+  }
   if (p.extra_out != p.extra) {
     constexpr int C = 8;
     for (int x0 = all; x0 < N; x0 += C * threads) {
@@ -179,7 +189,7 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
   }
   barrier();
 
-  // ---- children; the rows' numbers and entries ------------------------------------
+  // ---- children; the rows' numbers and entries, whose holds are taken away ----------
   if (all == 0 && (head < 0 || head >= N || count < 0 || count > N)) fail(PKV_DEV_FREE_LIST);
   for (int s = all; s < S; s += threads) {
     const int r = p.parents[s];
@@ -190,43 +200,47 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
       fail(PKV_DEV_PAIR_RANGE);
     }
   }
-  struct First {
-    int len, last;  // -1: none, -2: no length; the partly filled last block (0: none)
-  };
-  groups(
-      [&](int r) {
-        First m{p.lens[r], 0};
-        if (m.len < 0 || m.len > (int64_t)W * b) m.len = -2;
-        else if (m.len % b) m.last = p.tables[(int64_t)r * W + m.len / b];
-        p.solo[r] = m.last >= 0 && m.last < N && p.extra[m.last] == 0;  // (equal lanes agree)
-        return m;
-      },
-      [&](int r, int i, int n, const First& m) {
-        ForkRow w[Y];
-        bool bad = false;
-        int most = 0;
+  // Adds `by` to the holders of every entry's block that is one; `look`: sets the
+  // error bits of what is wrong with the rows.
+  auto hold = [&](int by, bool look) {
+    groups(
+        [&](int r) {
+          const int len = p.lens[r];
+          return len < 0 || len > (int64_t)W * b ? -1 : len;
+        },
+        [&](int r, int i, int n, int mine) {
+          ForkRow w[Y];
+          bool bad = false, over = false;
+          int most = 0;
 #pragma unroll
-        for (int y = 0; y < Y; ++y) {
-          const int j = i + min(y, n - 1), len = __shfl_sync(kFullMask, m.len, j);
-          bad |= __shfl_sync(kFullMask, m.last, j) < 0;
-          if (len < 0 && lane == 0) fail(PKV_DEV_SEQ_LEN);
-          w[y] = fork_row(p, r + j - i, max(len, 0));
-          most = max(most, w[y].have);
-        }
-        for (int e0 = lane; e0 < most; e0 += B) {
-          int x[Y][kForkBatch];
-#pragma unroll
-          for (int y = 0; y < Y; ++y) fork_entries(w[y], e0, x[y]);
-#pragma unroll
-          for (int k = 0; k < U; ++k) {
-            const int v = x[k / kForkBatch][k % kForkBatch];
-            bad |= v < -1 || v >= N;
+          for (int y = 0; y < Y; ++y) {
+            const int len = __shfl_sync(kFullMask, mine, i + min(y, n - 1));
+            if (look && len < 0 && lane == 0) fail(PKV_DEV_SEQ_LEN);
+            w[y] = fork_row(p, r + min(y, n - 1), y < n ? max(len, 0) : 0);
+            most = max(most, w[y].have);
           }
-        }
-        if (bad) fail(PKV_DEV_TABLE_RANGE);
-      });
+          for (int e0 = lane; e0 < most; e0 += B) {
+            int x[Y][kForkBatch], before[U];
+#pragma unroll
+            for (int y = 0; y < Y; ++y) fork_entries(w[y], e0, x[y]);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+              const int v = x[k / kForkBatch][k % kForkBatch], e = e0 + 32 * (k % kForkBatch);
+              // (-1 is an entry, but not where the row is written to next)
+              bad |= v < -1 || v >= N || (v < 0 && e == w[k / kForkBatch].partial);
+              before[k] = v >= 0 && v < N ? atomicAdd(p.extra_out + v, by) : 0;
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) over |= before[k] < 0;  // (none left to take)
+          }
+          if (look && bad) fail(PKV_DEV_TABLE_RANGE);
+          if (look && over) fail(PKV_DEV_SHARING);
+        });
+  };
+  hold(-1, true);
   barrier();
-  bool ok = __ldcg(p.totals + 1) == 0;
+  const bool sound = __ldcg(p.totals + 1) == 0;  // the inputs
+  bool ok = sound;
 
   // ---- fresh blocks, in the order of the next rows; holders added up -----------------
   if (ok && rank == 0) {
@@ -250,8 +264,8 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
   auto numbers = [&](int r) {
     return Numbers{p.lens[r], __ldcg(p.children + r), __ldcg(p.solo + r)};
   };
-  // Runs f(row, rows, entry, blocks, changes) for the rows' entries, a lane's of Y
-  // rows at a time.
+  // Runs f(row, rows, entry, blocks, gains) for the rows' entries, a lane's of Y
+  // rows at a time; the gain of an entry of no block is -1.
   auto rows = [&](auto f, auto done) {
     groups(numbers, [&](int r, int i, int n, const Numbers& m) {
       ForkRow w[Y];
@@ -266,7 +280,7 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
         most = max(most, w[y].have);
       }
       for (int e0 = lane; e0 - lane < most; e0 += B) {
-        int x[U], d[U];
+        int x[U], gain[U];
 #pragma unroll
         for (int y = 0; y < Y; ++y) {
           int z[kForkBatch];
@@ -274,46 +288,45 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
 #pragma unroll
           for (int k = 0; k < kForkBatch; ++k) {
             x[y * kForkBatch + k] = z[k];
-            d[y * kForkBatch + k] = z[k] < 0 ? 0 : fork_delta(w[y], e0 + 32 * k, c[y], solo[y] != 0);
+            gain[y * kForkBatch + k] =
+                z[k] < 0 ? -1 : fork_gain(w[y], e0 + 32 * k, c[y], solo[y] != 0);
           }
         }
-        f(r, n, e0, x, d);
+        f(r, n, e0, x, gain);
       }
       done(r, n);
     });
   };
   auto nothing = [](int, int) {};
   if (ok)
-    rows([&](int, int, int, const int (&x)[U], const int (&d)[U]) {
+    rows([&](int, int, int, const int (&x)[U], const int (&gain)[U]) {
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        if (d[k] < 0) p.claim[x[k]] = INT_MAX;
-        if (d[k]) atomicAdd(p.extra_out + x[k], d[k]);
+        if (gain[k] == 0) p.claim[x[k]] = INT_MAX;
+        if (gain[k] > 0) atomicAdd(p.extra_out + x[k], gain[k]);
       }
     }, nothing);
   barrier();
 
-  // ---- holders that do not hold; the first entry of each block that goes back --------
+  // ---- the first entry of each block that goes back ----------------------------------
   if (ok)
-    rows([&](int r, int, int e0, const int (&x)[U], const int (&d)[U]) {
+    rows([&](int r, int, int e0, const int (&x)[U], const int (&gain)[U]) {
       int left[U];
 #pragma unroll
-      for (int k = 0; k < U; ++k) left[k] = d[k] < 0 ? holders(x[k]) : 0;
+      for (int k = 0; k < U; ++k) left[k] = gain[k] == 0 ? holders(x[k]) : 0;
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        if (left[k] < -1) fail_late(PKV_DEV_SHARING);
+      for (int k = 0; k < U; ++k)
         if (left[k] == -1) atomicMin(p.claim + x[k], entry_of(r, e0, k));
-      }
     }, nothing);
   barrier();
   if (ok) {
     int back[Y] = {};  // of the rows
-    rows([&](int r, int n, int e0, const int (&x)[U], const int (&d)[U]) {
+    rows([&](int r, int n, int e0, const int (&x)[U], const int (&gain)[U]) {
       int left[U], mine[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        left[k] = d[k] < 0 ? holders(x[k]) : 0;
-        mine[k] = d[k] < 0 ? __ldcg(p.claim + x[k]) : -1;
+        left[k] = gain[k] == 0 ? holders(x[k]) : 0;
+        mine[k] = gain[k] == 0 ? __ldcg(p.claim + x[k]) : -1;
       }
 #pragma unroll
       for (int k = 0; k < U; ++k) {
@@ -352,10 +365,10 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
       block_scan(r1 - r0, s_scan, p.first + r0, [&](int i) { return p.back[r0 + i]; });
       // (p.first is read no more as such: the copies' choice is in p.fresh's sums)
     } else {
-      rows([&](int, int, int, const int (&x)[U], const int (&d)[U]) {
+      rows([&](int, int, int, const int (&x)[U], const int (&gain)[U]) {
 #pragma unroll
         for (int k = 0; k < U; ++k)
-          if (d[k]) atomicAdd(p.extra_out + x[k], -d[k]);
+          if (gain[k] >= 0 && gain[k] != 1) atomicAdd(p.extra_out + x[k], 1 - gain[k]);
       }, nothing);
     }
     struct Back {
@@ -393,6 +406,8 @@ fork_tables_kernel(const __grid_constant__ ForkParams p) {
                  }
                }
              });
+  } else {
+    hold(1, false);
   }
 
   // ---- the next rows, or, after any error, empty ones -------------------------------
