@@ -361,9 +361,12 @@ window_token_kernel(const __grid_constant__ WindowParams p, const __grid_constan
           }
         }
       }
-      if (lane == 0) fence_proxy_async();
       __syncwarp();  // the stage and P^T are rewritten next
-      if (j + NST < count) issue(j + NST);
+      if (j + NST < count) {
+        // (behind the barrier: every lane's reads, and zeros, come before the copy)
+        if (lane == 0) fence_proxy_async();
+        issue(j + NST);
+      }
     }
     return j;
   };
