@@ -710,9 +710,8 @@ int paged_build_tables(int64_t num_blocks, int32_t block_size, int32_t* free_lis
  *   parents         device, int32[num_next]
  *   block_tables    device, int32[num_seqs][max_blocks_per_seq]
  *   seq_lens        device, int32[num_seqs]
- *   tables_out      device, int32[num_next][max_blocks_per_seq], apart from
- *                   the inputs
- *   lens_out        device, int32[num_next], apart from the inputs
+ *   tables_out      device, int32[num_next][max_blocks_per_seq], apart
+ *   lens_out        device, int32[num_next], apart
  *   extra_out       device, int32[num_blocks]; may be extra_refs, else apart
  *   state_out       device, int64[2]; may be free_state, else apart
  *   window, sinks   window 0: nothing is given back for a window
@@ -720,7 +719,9 @@ int paged_build_tables(int64_t num_blocks, int32_t block_size, int32_t* free_lis
  *                   16-byte aligned; calls that may overlap need one each
  *
  * num_seqs and num_next at most 65535, rows times width at most 2^30,
- * num_blocks at most 2^30.
+ * num_blocks at most 2^30.  "Apart": the ring, the outputs and the workspace
+ * share no memory with one another or with an input, but where an output may be
+ * one (else PKV_ERR_ARG).
  */
 size_t paged_fork_tables_workspace_bytes(int64_t num_blocks, int32_t num_seqs, int32_t num_next,
                                          int32_t max_blocks_per_seq);
@@ -755,7 +756,7 @@ int paged_fork_tables(const pkv_cache* cache, int32_t* free_list, const int64_t*
  *   tables_out      device, as block_tables; may be block_tables, else apart
  *   extra_out       device, int32[num_blocks]; may be extra_refs, else apart
  *   state_out       device, int64[2]; may be free_state, else apart
- *   moved_to        device, int32[num_blocks], apart from the inputs
+ *   moved_to        device, int32[num_blocks], apart
  *   workspace       device, >= paged_compact_workspace_bytes(num_blocks) bytes,
  *                   16-byte aligned; calls that may overlap need one each
  * and the rest, and the bounds, as for paged_fork_tables.

@@ -6,6 +6,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "window_tc.cuh"
@@ -982,10 +983,29 @@ size_t paged_fork_tables_workspace_bytes(int64_t num_blocks, int32_t num_seqs, i
   return pkv_fork_workspace(num_blocks, num_seqs, num_next, max_blocks_per_seq);
 }
 
-// Whether two arrays of 32-bit numbers share memory.
-static bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + 4 * (uintptr_t)nb && y < x + 4 * (uintptr_t)na;
+// An array of a call, in bytes; an output may be the whole of the input `twin` (its
+// place in the list), or of none (-1).
+struct CallArray {
+  const void* at;
+  int64_t bytes;
+  bool written;
+  int twin;
+};
+
+// Whether an array that is written shares memory with another one.
+static bool overlap(std::initializer_list<CallArray> arrays) {
+  const CallArray* const all = arrays.begin();
+  const int n = (int)arrays.size();
+  for (int i = 0; i < n; ++i) {
+    if (!all[i].written) continue;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(all[i].at);
+    for (int j = 0; j < n; ++j) {
+      const uintptr_t y = reinterpret_cast<uintptr_t>(all[j].at);
+      if (j == i || !all[i].bytes || !all[j].bytes || (j == all[i].twin && x == y)) continue;
+      if (x < y + (uintptr_t)all[j].bytes && y < x + (uintptr_t)all[i].bytes) return true;
+    }
+  }
+  return false;
 }
 
 // Checks that paged_fork_tables and paged_compact share.
@@ -1008,10 +1028,6 @@ static int check_pages(const pkv_cache* cache, const void* free_list, const void
     if (reinterpret_cast<uintptr_t>(x) & 3u) return PKV_ERR_ALIGN;
   for (const void* x : {free_state, state_out})
     if (reinterpret_cast<uintptr_t>(x) & 7u) return PKV_ERR_ALIGN;
-  // the same, or apart
-  if ((extra_out != extra_refs && overlap(extra_out, cache->num_blocks, extra_refs, cache->num_blocks)) ||
-      (state_out != free_state && overlap(state_out, 4, free_state, 4)))
-    return PKV_ERR_ARG;
   return aligned16(workspace) ? PKV_OK : PKV_ERR_ALIGN;
 }
 
@@ -1032,15 +1048,22 @@ int paged_fork_tables(const pkv_cache* cache, int32_t* free_list, const int64_t*
   if (num_next > 0 && (!parents || !tables_out || !lens_out)) return PKV_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(parents) & 3u) || (reinterpret_cast<uintptr_t>(lens_out) & 3u))
     return PKV_ERR_ALIGN;
-  const int64_t next_entries = (int64_t)num_next * max_blocks_per_seq;
-  if (overlap(tables_out, next_entries, block_tables, (int64_t)num_seqs * max_blocks_per_seq) ||
-      overlap(tables_out, next_entries, parents, num_next) ||
-      overlap(tables_out, next_entries, seq_lens, num_seqs) ||
-      overlap(lens_out, num_next, seq_lens, num_seqs) || overlap(lens_out, num_next, parents, num_next))
+  const size_t need =
+      pkv_fork_workspace(cache->num_blocks, num_seqs, num_next, max_blocks_per_seq);
+  if (workspace_bytes < need) return PKV_ERR_WORKSPACE;
+  const int64_t counts = 4 * cache->num_blocks, width = 4 * (int64_t)max_blocks_per_seq;
+  if (overlap({{free_state, 16, false, -1},
+               {extra_refs, counts, false, -1},
+               {block_tables, num_seqs * width, false, -1},
+               {seq_lens, 4 * (int64_t)num_seqs, false, -1},
+               {parents, 4 * (int64_t)num_next, false, -1},
+               {free_list, counts, true, -1},
+               {tables_out, num_next * width, true, -1},
+               {lens_out, 4 * (int64_t)num_next, true, -1},
+               {extra_out, counts, true, 1},
+               {state_out, 16, true, 0},
+               {workspace, (int64_t)need, true, -1}}))
     return PKV_ERR_ARG;
-  if (workspace_bytes <
-      pkv_fork_workspace(cache->num_blocks, num_seqs, num_next, max_blocks_per_seq))
-    return PKV_ERR_WORKSPACE;
   if (!pkv_error_word()) return PKV_ERR_CUDA;
   return pkv_launch_fork_tables(cache, elem_bytes(cache->dtype), free_list, free_state, extra_refs,
                                 parents, num_next, block_tables, seq_lens, num_seqs,
@@ -1064,13 +1087,21 @@ int paged_compact(const pkv_cache* cache, int32_t* free_list, const int64_t* fre
   if (rc) return rc;
   if (!moved_to || (num_seqs > 0 && !tables_out)) return PKV_ERR_NULL;
   if (reinterpret_cast<uintptr_t>(moved_to) & 3u) return PKV_ERR_ALIGN;
-  const int64_t entries = (int64_t)num_seqs * max_blocks_per_seq;
-  if ((tables_out != block_tables && overlap(tables_out, entries, block_tables, entries)) ||
-      overlap(tables_out, entries, seq_lens, num_seqs) ||
-      overlap(moved_to, cache->num_blocks, extra_refs, cache->num_blocks) ||
-      overlap(moved_to, cache->num_blocks, block_tables, entries))
+  const size_t need = pkv_compact_workspace(cache->num_blocks);
+  if (workspace_bytes < need) return PKV_ERR_WORKSPACE;
+  const int64_t counts = 4 * cache->num_blocks;
+  const int64_t entries = 4 * (int64_t)num_seqs * max_blocks_per_seq;
+  if (overlap({{free_state, 16, false, -1},
+               {extra_refs, counts, false, -1},
+               {block_tables, entries, false, -1},
+               {seq_lens, 4 * (int64_t)num_seqs, false, -1},
+               {free_list, counts, true, -1},
+               {tables_out, entries, true, 2},
+               {extra_out, counts, true, 1},
+               {state_out, 16, true, 0},
+               {moved_to, counts, true, -1},
+               {workspace, (int64_t)need, true, -1}}))
     return PKV_ERR_ARG;
-  if (workspace_bytes < pkv_compact_workspace(cache->num_blocks)) return PKV_ERR_WORKSPACE;
   if (!pkv_error_word()) return PKV_ERR_CUDA;
   return pkv_launch_compact(cache, elem_bytes(cache->dtype), free_list, free_state, extra_refs,
                             block_tables, seq_lens, num_seqs, max_blocks_per_seq, tables_out,

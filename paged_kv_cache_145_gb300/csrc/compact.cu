@@ -142,7 +142,7 @@ compact_move_kernel(const __grid_constant__ CompactParams p) {
     for (int e = threadIdx.x; e < p.width; e += kMoveThreads) {
       const int64_t at = (int64_t)r * p.width + e;
       const int x = p.tables[at];
-      p.tables_out[at] = e < have && x >= 0 ? p.moved_to[x] : x;
+      p.tables_out[at] = e < have && (unsigned)x < (unsigned)p.num_blocks ? p.moved_to[x] : x;
     }
   }
 }

@@ -112,3 +112,19 @@ def test_blocks_named_by_as_many_entries_as_holders(cluster):
     m.rows[sound + 1][0] = m.rows[sound][0]                # shared, full (its own first one is lost)
     step(m, [sound, sound + 1, sound + 1] + list(range(sound)), in_place=cluster)
     step(m, [1, -1, 0, 2] + list(range(3, 3 + sound // 2)), window=20)
+
+
+def test_arrays_without_elements_lie_anywhere():
+    """No rows, and none next: empty arrays inside the counts that the call writes."""
+    m = Model(40, 16, 5, seed=1)
+    d = m.device()
+    d.update(block_tables=d["extra_refs"][8:8].view(0, 5), seq_lens=d["extra_refs"][4:4])
+    none = d["extra_refs"][12:12]
+    out = pkv.paged_fork_tables(parents=none, extra_out=d["extra_refs"], free_state_out=d["free_state"],
+                                tables_out=d["free_list"][3:3].view(0, 5), lens_out=none, **d)
+    assert pkv.paged_get_device_error() == 0
+    m.same(out, d["free_list"])
+    out = pkv.paged_compact(extra_out=d["extra_refs"], free_state_out=d["free_state"], **d)
+    assert pkv.paged_get_device_error() == 0
+    assert out[2].tolist() == [0, 40] and d["free_list"].tolist() == list(range(40))
+    assert (out[3] == -1).all() and (out[1] == 0).all()
