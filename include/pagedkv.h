@@ -192,7 +192,8 @@ int paged_rotary_init(pkv_rotary* rotary, int32_t rotary_dim, int32_t num_axes,
  *   positions     device, int32[num_axes][num_tokens]
  *   slot_mapping  device, int64[num_tokens]
  *   num_heads     query heads (any count)
- *   q_out         device, as q with q_out_stride; may be q (same stride)
+ *   q_out         device, as q with q_out_stride; may be q (same stride, else
+ *                 PKV_ERR_ARG)
  *
  * head_dim as for paged_kv_write; rotary_dim at most head_dim.  With halves
  * (not interleaved) whose length rotary_dim / 2 is not a whole number of

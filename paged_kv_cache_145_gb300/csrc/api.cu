@@ -332,6 +332,8 @@ static int check_rope_write(const pkv_cache* cache, const pkv_rotary* rotary, co
       (reinterpret_cast<uintptr_t>(positions) & 3u) ||
       (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
     return PKV_ERR_ALIGN;
+  // In place, a token's queries must not lie where another one's are read.
+  if (num_tokens > 1 && q_out == q && q_out_stride != q_stride) return PKV_ERR_ARG;
   return PKV_OK;
 }
 
