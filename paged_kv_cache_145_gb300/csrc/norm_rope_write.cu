@@ -4,8 +4,8 @@
 // The mathematics.  For a head x of D elements, r = 1 / sqrt(mean(x^2) + eps),
 // y_d = x_d r w_d, and y's leading pairs turn as in paged_rope_kv_write.  All
 // of it in float32 from the stored elements; outputs are rounded once.  Sums of
-// squares beyond float32 (or, with eps = 0, below it) are taken again from the
-// head scaled by a power of two.
+// squares beyond float32 (or, with an eps as small, near its smallest numbers) are
+// taken again from the head, and eps, scaled by a power of two.
 //
 // A head lies in the lanes of one group (a power of two of them, at most a
 // warp), two 16-byte vectors a lane, so that the sum of squares is a few
@@ -155,8 +155,9 @@ norm_rope_write_kernel(const __grid_constant__ NormRopeParams p) {
       // ---- norm -----------------------------------------------------------------
       float sum = group_sum(squares(a, b));
       float scale = 1.f;
-      if (sum > 0x1p120f || (p.eps == 0.f && sum < 0x1p-90f)) {
-        float top = 0.f;
+      if (sum > 0x1p120f || (p.eps < 0x1p-100f && sum < 0x1p-90f)) {
+        // (with the root of a small eps, so that its scaled value is below one)
+        float top = p.eps < 0x1p-100f ? sqrtf(p.eps) : 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) top = fmaxf(top, fmaxf(fabsf(a[j]), fabsf(b[j])));
         for (int o = p.lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(mates, top, o));
