@@ -52,9 +52,12 @@
 // tile costs more than the chain (8 x 300-512 queries over 1000-4000 states,
 // 32/8 heads of 128: 150 us, 215 with blocks of 128 rows).  All four converter
 // warps for keys and values in turn took 195 us where two for each took 164.
-// Query and output rows go through shared memory, a row's units in neighbouring
-// lanes: a lane a row took 151 us there, this 142, and bf16 8 x 2048 642, this 628
-// (over 2048-6400 states, another draw).
+// Query rows go through shared memory, a row's units in neighbouring lanes, and so
+// do many output rows of 128: a lane a row took 144 us there, this 137, and the
+// 8 x 2048 above, in long runs, 855, this 840.  Up to 64 output rows, and rows of 64
+// (one line each), leave a lane a row: 64 sequences of one query, 200-1500 states,
+// 16/16 heads of 64 52.8 us for 54.1, 32/8 heads of 128 in FP8 59.0 for 61.6, 32 of
+// 16 queries (64 rows) 27.8 for 29.2, 8 of 300-512, heads of 64, 80 for 84.
 //
 // With a window, FP8, 8 x 300-512 queries, window 1500, 32/8 heads of 128: 98 us
 // (153 with blocks of 128 rows).  A block of 14 tiles takes 25 us: 2 until its
@@ -544,6 +547,7 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
     return;
   }
   const int row_n = nr > 128 ? 2 : 1;  // row tiles with rows
+  const bool by_lane = D == 64 || nr <= 64;  // output rows leave a lane a row
 
   // ---- barriers, tensor memory, Q ---------------------------------------------
   const uint32_t bar0 = sbase + Cfg::kBarOff;
@@ -1003,7 +1007,7 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
         uint32_t w[32];
         tmem_ld32(base + Cfg::kOCol + q * 32, w);
         auto o = [&](int d) { return bad ? 0.f : __uint_as_float(w[d]) * inv; };
-        if (whole) {  // over the queries, whose products are done
+        if (whole && (!by_lane || r < nr)) {
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint4 u;
@@ -1011,16 +1015,18 @@ cross_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap
             u.y = pack_pair<T>(o(8 * v + 2), o(8 * v + 3));
             u.z = pack_pair<T>(o(8 * v + 4), o(8 * v + 5));
             u.w = pack_pair<T>(o(8 * v + 6), o(8 * v + 7));
-            *reinterpret_cast<uint4*>(row_unit(smem + t * Cfg::kQBytes, rr, q * 4 + v)) = u;
+            if (by_lane) reinterpret_cast<uint4*>(out + at)[q * 4 + v] = u;
+            // (over the queries, whose products are done)
+            else *reinterpret_cast<uint4*>(row_unit(smem + t * Cfg::kQBytes, rr, q * 4 + v)) = u;
           }
-        } else if (r < nr) {
+        } else if (!whole && r < nr) {
 #pragma unroll
           for (int v = 0; v < 8; ++v)
             reinterpret_cast<float4*>(p.ws_o + wrow * D)[q * 8 + v] =
                 make_float4(o(4 * v), o(4 * v + 1), o(4 * v + 2), o(4 * v + 3));
         }
       }
-      if (whole) {
+      if (whole && !by_lane) {
         __syncwarp();
         warp_rows<D>(at, rr & ~31, lane, [&](int64_t to, int row, int c) {
           if (t * 128 + row < nr)
