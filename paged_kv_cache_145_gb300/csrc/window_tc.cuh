@@ -10,7 +10,7 @@
 // they do: 8 prompts of 2048 (32/8 heads of 128, window 1024, 4 sinks) took 409 us
 // as 4096 blocks of one item each, 187 of them for the tiles.  Here two persistent
 // blocks per SM walk the items, and every role goes from one item's tiles to the
-// next one's without a stop (310 us, 890 TFLOP/s of products that some row sees):
+// next one's without a stop (305 us, 905 TFLOP/s of products that some row sees):
 //   scout (one warp)       an item ahead: its numbers into a ring of WindowItem,
 //        the check of its table entries; then the values of the tiles at the
 //        window's edges, see below;
@@ -35,7 +35,7 @@
 // cross_tc.cuh.  Every wait is bounded.
 //
 // What bounds it: each tile's chain from scores over the softmax to P.V; tensor
-// pipes are 40% busy, the special function unit 21%.  Of the 310 us the scout's
+// pipes are 40% busy, the special function unit 21%.  Of 310 us the scout's
 // table checks and its waits take about 35 where they hold the chain up, the stores
 // of the output 15.
 #pragma once
@@ -170,6 +170,60 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(query), "r"(bar)
       : "memory");
+}
+
+// Adds the cleared values of an item's edge tile j to O, once all products are in,
+// for the row rr at position pos with the running maximum m: infinity or NaN, as the
+// value is, and NaN where its weight, as P would hold it, is zero.
+template <typename T, int D>
+__device__ __forceinline__ void add_odd(const WindowParams& p, const volatile WindowItem* it, int j,
+                                        int pos, int rr, uint32_t base, float m) {
+  using Cfg = WindowTcCfg<T, D>;
+  const int H = p.num_heads, G = p.group, b = p.block_size, shift = 31 - __clz(b);
+  const WindowKeys keys(it, j);
+  const uint64_t seen = keys.seen(it), mine = keys.mask(p, pos);
+  const int32_t* trow = p.tables + (int64_t)it->seq * p.max_blocks;
+  const int x = it->r0 + min(rr, it->nr - 1);
+  const T* const query = static_cast<const T*>(p.q) +
+                         ((int64_t)(it->q0 + x / G) * H + it->kvh * G + x % G) * D;
+  const float top = (m == -INFINITY ? 0.f : m) - Cfg::kBias;
+#pragma unroll 1
+  for (int q = 0; q < D / 32; ++q) {
+    uint32_t o[32];
+    tmem_ld32(base + Cfg::kOCol + q * 32, o);
+#pragma unroll 1
+    for (int k = 0; k < Cfg::kKeys; ++k) {
+      if (!(seen >> k & 1ull)) continue;
+      const int tk = keys.pos(k), e = trow[tk >> shift];
+      if ((unsigned)e >= (unsigned)p.num_blocks) continue;
+      const int64_t row = (((int64_t)e * p.kv_heads + it->kvh) * b + (tk & (b - 1))) * D;
+      const T* const value = static_cast<const T*>(p.v_cache) + row + q * 32;
+      bool any = false;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) any |= !isfinite(static_cast<float>(value[i]));
+      if (!any || !(mine >> k & 1ull)) continue;
+      const T* const key = static_cast<const T*>(p.k_cache) + row;
+      float z = 0.f;
+      for (int d = 0; d < D; ++d) z += static_cast<float>(query[d]) * static_cast<float>(key[d]);
+      const float weight = static_cast<float>(Elem<T>::from_f(ex2(z * p.qscale - top)));
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float v = static_cast<float>(value[i]);
+        if (!isfinite(v)) o[i] = __float_as_uint(__uint_as_float(o[i]) + weight * v);
+      }
+    }
+    __syncwarp();
+    tmem_st32(base + Cfg::kOCol + q * 32, o);
+  }
+}
+
+// The same as a function of its own, around which the softmax's registers are not
+// planned: heads of 128, 8 prompts of 2048 305 us, 318 within the softmax; heads of
+// 64, 8 of 300-512 queries 77, 74 within it.
+template <typename T, int D>
+__device__ __noinline__ void add_odd_apart(const WindowParams& p, const volatile WindowItem* it,
+                                           int j, int pos, int rr, uint32_t base, float m) {
+  add_odd<T, D>(p, it, j, pos, rr, base, m);
 }
 
 template <typename T, int D>
@@ -660,45 +714,6 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
       const bool live = warp * 32 < it->nr;  // the warp has rows
       const int pos = it->pos0 + (it->r0 + min(rr, it->nr - 1)) / G;
       float m = -INFINITY, l = 0.f;
-      // Adds the cleared values of an edge tile to O, once all products are in:
-      // infinity or NaN, as the value is, and NaN where the score is minus infinity.
-      auto add_odd = [&](int j) {
-        const WindowKeys keys(it, j);
-        const uint64_t seen = keys.seen(it), mine = keys.mask(p, pos);
-        const int32_t* trow = p.tables + (int64_t)it->seq * p.max_blocks;
-        const int x = it->r0 + min(rr, it->nr - 1);
-        const T* const query = static_cast<const T*>(p.q) +
-                               ((int64_t)(it->q0 + x / G) * H + it->kvh * G + x % G) * D;
-#pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
-          tmem_ld32(base + Cfg::kOCol + q * 32, o);
-#pragma unroll 1
-          for (int k = 0; k < KT; ++k) {
-            if (!(seen >> k & 1ull)) continue;
-            const int tk = keys.pos(k), e = trow[tk >> shift];
-            if ((unsigned)e >= (unsigned)p.num_blocks) continue;
-            const int64_t row = (((int64_t)e * p.kv_heads + it->kvh) * b + (tk & (b - 1))) * D;
-            const T* const value = static_cast<const T*>(p.v_cache) + row + q * 32;
-            bool any = false;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) any |= !isfinite(static_cast<float>(value[i]));
-            if (!any || !(mine >> k & 1ull)) continue;
-            const T* const key = static_cast<const T*>(p.k_cache) + row;
-            float z = 0.f;
-            for (int d = 0; d < D; ++d)
-              z += static_cast<float>(query[d]) * static_cast<float>(key[d]);
-            const bool none = z * p.qscale == -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float v = static_cast<float>(value[i]);
-              if (!isfinite(v)) o[i] = __float_as_uint(__uint_as_float(o[i]) + (none ? NAN : v));
-            }
-          }
-          __syncwarp();
-          tmem_st32(base + Cfg::kOCol + q * 32, o);
-        }
-      };
       // One tile; EDGE: masked.  Two copies, so that the one that most tiles take has
       // no more in it than it needs (one for both cost 38 of 333 us).
       auto tile = [&](auto edge_tag, int j) {
@@ -802,7 +817,10 @@ window_tc_kernel(const __grid_constant__ WindowParams p, const __grid_constant__
           j = max(j, (j < at_edge.left0 ? min(at_edge.left0, at_edge.right) : at_edge.right) - 1);
           continue;
         }
-        if (dirty[edges % Cfg::kEdges] == edges && live) add_odd(j);
+        if (dirty[edges % Cfg::kEdges] == edges && live) {
+          if constexpr (D == 64) add_odd<T, D>(p, it, j, pos, rr, base, m);
+          else add_odd_apart<T, D>(p, it, j, pos, rr, base, m);
+        }
         ++edges;
       }
       // ---- the item's rows ----------------------------------------------------------
