@@ -439,7 +439,9 @@ int paged_attention_cross(const pkv_cache* cache, const void* q, int64_t total_q
  * it sees acts as in the formula, as for paged_attention_cross.
  *
  * Pools, geometry, precision and the split of long spans with few rows are as
- * for paged_attention_cross.
+ * for paged_attention_cross, but that single tokens (max_queries 1) over bf16
+ * pools keep two bf16 parts of a probability, as paged_attention_decode does: an
+ * output moves by at most 2^-15 of the weighted mean of |V_t| there.
  *
  *   q, out, query_starts, max_queries, block_tables, scale, workspace
  *                 as for paged_attention_cross; rows of out from the last

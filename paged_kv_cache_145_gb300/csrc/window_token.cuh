@@ -14,11 +14,13 @@
 // row (the queries hold their elements in the same order), and of the values
 // each lane takes a 4 x 4 block of codes, turned by byte permutes.
 //
-// The running maximum and sum are float32 in base 2.  P is rounded once to the
-// operand type as in cross_tc_kernel (bf16 for bf16 pools, else fp16, scaled by
-// 2^kBias to keep small weights out of the subnormals); a second part of it would
-// make an infinite value's product NaN.  FP8 pools, which have no infinities, take
-// two parts where the head's value scale makes a rounding of 2^-11 show
+// The running maximum and sum are float32 in base 2.  P is rounded once to fp16
+// (scaled by 2^kBias to keep small weights out of the subnormals), as in
+// cross_tc_kernel; bf16 pools take two bf16 parts, as paged_attention_decode does,
+// good to 2^-15.  The first is cut off and the second then not negative, and never
+// zero where the first is not, so that an infinite value's products have one sign
+// and are NaN only where both parts are zero.  FP8 pools, which have no infinities,
+// take two rounded parts where the head's value scale makes a rounding of 2^-11 show
 // (fp8_split_p).  Positions of a chunk that the query does not see have
 // weight 0 and their values are zeros, so that nothing there reaches it; the
 // first chunk of a window may hold none that it sees, so that a maximum of minus
@@ -307,9 +309,14 @@ window_token_kernel(const __grid_constant__ WindowParams p, const __grid_constan
                            (2 * ti + 1) * C + gi + 8};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint16_t hi = Op::bits(pr[e]);
+          const uint16_t hi = SPLIT && !FP8 ? (uint16_t)(__float_as_uint(pr[e]) >> 16)
+                                            : Op::bits(pr[e]);
           pt[at[e]] = hi;
-          if constexpr (SPLIT) pt[8 * C + at[e]] = Op::bits(pr[e] - Op::back(hi));
+          if constexpr (SPLIT) {
+            uint16_t lo = Op::bits(pr[e] - Op::back(hi));
+            if (!FP8 && hi != 0 && lo == 0) lo = 0x0080;  // 2^-126
+            pt[8 * C + at[e]] = lo;
+          }
         }
       }
       if (!FP8 && sees != 0xFFFFu) {
@@ -374,7 +381,7 @@ window_token_kernel(const __grid_constant__ WindowParams p, const __grid_constan
   if constexpr (FP8)
     done = fp8_split_p<T>(p.v_scale[kvh]) ? walk(std::true_type{}) : walk(std::false_type{});
   else
-    done = walk(std::false_type{});
+    done = walk(typename std::is_same<T, __nv_bfloat16>::type{});
   if (timed_out) {
     for (int j = done + 1; j < min(count, done + NST); ++j)
       mbar_wait(bar0 + (j % NST) * 8, (uint32_t)((j / NST) & 1), kWaitLimitNs / 8);
