@@ -59,7 +59,7 @@
 // 16/16 heads of 64 52.8 us for 54.1, 32/8 heads of 128 in FP8 59.0 for 61.6, 32 of
 // 16 queries (64 rows) 27.8 for 29.2, 8 of 300-512, heads of 64, 80 for 84.
 //
-// With a window, FP8, 8 x 300-512 queries, window 1500, 32/8 heads of 128: 98 us
+// With a window, FP8, 8 x 300-512 queries, window 1500, 32/8 heads of 128: 97 us
 // (153 with blocks of 128 rows).  A block of 14 tiles takes 25 us: 2 until its
 // barriers and tensor memory are there, 4 for the queries, 1 to the first scores,
 // 1.2 a tile at the window's edges and 0.75 else, 2 for the output; one block on
